@@ -7,7 +7,7 @@
  * added; the weighted results return to token order.
  *
  *   logits  l[t,e] = sum_i x[t,i] * Wr[e,i]            (row stride n_expert)
- *   score   s = sigmoid(l)  or  s = sqrt(softplus(l))
+ *   score   s = sigmoid(l)  or  s = sqrt(softplus(l))  or  s = softmax(l)
  *   key     s + bias[e]  (bias optional; it selects, it never weights)
  *   select  top-k keys; equal keys -> lower expert index first; NaN last
  *   weight  w_j = route_scale * s_j / sum over the selected s
@@ -42,6 +42,13 @@
  *    reduction dimension.  bf16 and fp16 values are passed as their bit
  *    patterns (uint16).  Q8B32 = int8 quants [n, rows, cols] plus one fp16
  *    scale per 32 consecutive columns [n, rows, cols/32]; weight = scale * q.
+ *    F8B128 = e4m3 codes (OCP, largest value 448) [n, rows, cols] plus one
+ *    fp32 scale per block of 128 x 128 [n, ceil(rows/128), ceil(cols/128)];
+ *    weight = scale * code.
+ *  - Products with F8B128 weights are products of e4m3 operands: activations
+ *    are quantised per row and 128 columns as moe_quantize_rows does (x, and
+ *    the SwiGLU intermediate from its fp32 values), and sums are fp32.  Softmax
+ *    scores are taken over all n_expert logits of a token.
  *  - Results: expert indices and the permutation are exact and do not depend
  *    on the path taken; logits and scores are accumulated in fp64 and rounded
  *    once to fp32; the SwiGLU intermediate is rounded to the activation format
@@ -68,8 +75,8 @@ typedef enum {
     MOE_ERR_DEVICE = 4       /* the HIP runtime refused a launch */
 } moe_status;
 
-typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SQRT_SOFTPLUS = 1 } moe_score;
-typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_Q8B32 = 2 } moe_dtype;
+typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SQRT_SOFTPLUS = 1, MOE_SCORE_SOFTMAX = 2 } moe_score;
+typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_Q8B32 = 2, MOE_DT_F8B128 = 3 } moe_dtype;
 typedef enum { MOE_PATH_AUTO = 0, MOE_PATH_DECODE = 1, MOE_PATH_PREFILL = 2 } moe_path;
 
 /* Largest token count the decode path accepts (MOE_PATH_AUTO takes it for
@@ -87,13 +94,14 @@ typedef struct {
     int32_t score;       /* moe_score */
     float route_scale;   /* finite, > 0: 1.5 for the sqrt(softplus) router, 1.0 for sigmoid */
     int32_t act_dtype;   /* moe_dtype of x and of the SwiGLU intermediate: F32 or BF16 */
-    int32_t w_dtype;     /* moe_dtype of the expert weights: (F32,F32) (BF16,BF16) (BF16,Q8B32) */
+    int32_t w_dtype;     /* moe_dtype of the expert weights: (F32,F32) (BF16,BF16) (BF16,Q8B32) (BF16,F8B128) */
     int32_t path;        /* moe_path, used by moe_layer_forward */
 } moe_config;
 
 typedef struct {
-    const void *q;          /* [n, rows, cols] elements of w_dtype (int8 for Q8B32) */
-    const uint16_t *scale;  /* Q8B32 only: fp16 bits [n, rows, cols/32]; else ignored */
+    const void *q;      /* [n, rows, cols] elements of w_dtype (int8 for Q8B32, e4m3 for F8B128) */
+    const void *scale;  /* Q8B32: fp16 bits [n, rows, cols/32]; F8B128: fp32 [n, ceil(rows/128),
+                           ceil(cols/128)]; 4-byte aligned; else ignored */
 } moe_mat;
 
 typedef struct {
@@ -110,7 +118,8 @@ typedef struct {
  * projection, 5 combine.  The decode path (n_tokens <= MOE_DECODE_MAX_TOKENS)
  * builds the permutation inside the selection kernel and the combine inside
  * the down kernel: it launches no kernel for stages 2 and 5 and leaves their
- * events unrecorded. */
+ * events unrecorded (F8B128 layers run the same launches at every n_tokens,
+ * stages 2 and 5 included; the quantisation of x counts to stage 3). */
 #define MOE_STAGES 6
 #define MOE_STAGE_EVENTS (2 * MOE_STAGES)
 
@@ -147,6 +156,31 @@ int moe_route(const moe_config *cfg, const void *x, const float *w_router, const
 int moe_select(const moe_config *cfg, const float *logits, const float *bias, int32_t *topk_idx,
                float *topk_w, void *stream);
 
+/* Expert groups of a selection.  The n_expert experts form n_group groups of
+ * n_expert / n_group consecutive ones; a group's score is the fp32 sum of its
+ * group_top best keys (of all, if it has fewer); the topk_group best groups
+ * stay (equal scores: the lower group first; NaN last) and the top-k keys are
+ * taken among their experts, with the order of moe_select.
+ * 1 <= n_group <= 64 dividing n_expert, 1 <= topk_group <= n_group, group_top
+ * 1 or 2, top_k <= topk_group * n_expert / n_group, normalise 0 or 1, else
+ * MOE_ERR_INVALID. */
+typedef struct {
+    int32_t n_group;    /* 1: no groups */
+    int32_t topk_group; /* groups that stay */
+    int32_t group_top;  /* keys summed into a group's score: 1 or 2 */
+    int32_t normalise;  /* 1: w_j = route_scale * s_j / sum of the selected s (0 if that is 0);
+                           0: w_j = route_scale * s_j */
+} moe_groups;
+
+/* moe_select and moe_route with expert groups; groups == NULL stands for
+ * {1, 1, 1, 1}, the selection of moe_select.  Every moe_score, softmax
+ * included (as in moe_select, moe_route and the layer calls). */
+int moe_select_grouped(const moe_config *cfg, const moe_groups *groups, const float *logits, const float *bias,
+                       int32_t *topk_idx, float *topk_w, void *stream);
+int moe_route_grouped(const moe_config *cfg, const moe_groups *groups, const void *x, const float *w_router,
+                      const float *bias, float *logits, int32_t *topk_idx, float *topk_w, void *ws,
+                      size_t ws_bytes, void *stream);
+
 /* Token->expert grouping: a stable counting sort of the flat assignments
  * f = t*k + j by expert.  offsets [E+1] (exclusive prefix sum of the expert
  * counts); perm_rows [T*k]: the f of every assignment, ordered by (expert, f);
@@ -175,6 +209,12 @@ int moe_combine(const moe_config *cfg, const float *slot_out, const float *share
  * (grouped GEMMs, bf16 on MFMA); MOE_PATH_AUTO chooses by n_tokens. */
 int moe_layer_forward(const moe_config *cfg, const void *x, const moe_weights *w, float *y,
                       moe_debug *dbg, void *ws, size_t ws_bytes, void *stream);
+
+/* moe_layer_forward with expert groups (NULL: {1, 1, 1, 1}) and a choice of
+ * y's type: y_dtype MOE_DT_F32, or MOE_DT_BF16 (the fp32 sum rounded once;
+ * F8B128 weights only, else MOE_ERR_UNSUPPORTED). */
+int moe_layer_forward_grouped(const moe_config *cfg, const moe_groups *groups, const void *x, const moe_weights *w,
+                              void *y, int32_t y_dtype, moe_debug *dbg, void *ws, size_t ws_bytes, void *stream);
 
 /* moe_layer_forward for callers that cannot allocate device memory: code
  * under HIP graph capture, tight serving loops, harnesses that forbid
@@ -212,6 +252,38 @@ int moe_layer_forward_noalloc(const moe_config *cfg, const void *x, const moe_we
 int moe_topk_rows(const float *scores, int32_t rows, int32_t n, int32_t k, int32_t *idx, float *vals,
                   void **events, void *stream);
 
+/* Rows to e4m3 codes with one power-of-two scale per 128 columns.  x
+ * [rows, cols] of x_dtype (MOE_DT_F32 or MOE_DT_BF16), rows ldx elements
+ * apart.  For each row and each block of 128 columns (the last may be
+ * shorter) with largest magnitude a, the scale s is the smallest power of two
+ * with a <= 448 s, at least 2^-126, and 1 if a = 0; q [rows, cols] = x / s
+ * rounded to e4m3 (nearest, ties to even), and scale [rows,
+ * MOE_F8_SCALE_LD(cols)] holds s as its e8m0 byte (exponent + 127).  A block
+ * with a NaN or an infinity gets the byte 255 (NaN) and NaN codes (0x7F).
+ * The bytes of a row past its last block are written as 127.
+ * rows >= 0 (0 enqueues nothing), 16 <= cols <= 2^20 a multiple of 16 and
+ * ldx >= cols a multiple of 16 bytes, else MOE_ERR_INVALID; x and q 16-byte
+ * aligned, scale 4-byte.  q and scale must not overlap x.  No workspace. */
+#define MOE_F8_SCALE_LD(cols) (((cols) + 511) / 512 * 4)
+int moe_quantize_rows(const void *x, int32_t x_dtype, int32_t rows, int32_t cols, int64_t ldx, uint8_t *q,
+                      uint8_t *scale, void *stream);
+
+/* out [m, n] = x [m, k] w[n, k]^T with e4m3 operands:
+ *   out[i, j] = sum_b s_x[i, b] * s_w[j / 128, b] * sum_{c in block b} q_x[i, c] * q_w[j, c]
+ * (b: the blocks of 128 columns; fp32 sums).  x is MOE_DT_F8B128 codes with
+ * x_scale [m, MOE_F8_SCALE_LD(k)] as moe_quantize_rows writes them, or
+ * MOE_DT_BF16 / MOE_DT_F32 rows, which are quantised that way first (x_scale
+ * NULL, workspace needed).  w [n, k] codes, w_scale [ceil(n/128), ceil(k/128)]
+ * fp32.  out_dtype MOE_DT_F32, or MOE_DT_BF16 (one rounding).  0 <= m <= 2^20
+ * (0 enqueues nothing), 1 <= n <= 2^20, 16 <= k <= 2^20 a multiple of 16,
+ * else MOE_ERR_INVALID; x, w, out and ws 16-byte aligned, the scales 4-byte.
+ * out must not overlap an input.  The workspace size is 0 for F8B128 rows and
+ * for sizes out of range. */
+size_t moe_block_matmul_workspace_bytes(int32_t x_dtype, int32_t m, int32_t k);
+int moe_block_matmul(const void *x, int32_t x_dtype, const uint8_t *x_scale, const uint8_t *w, const float *w_scale,
+                     int32_t m, int32_t n, int32_t k, void *out, int32_t out_dtype, void *ws, size_t ws_bytes,
+                     void *stream);
+
 /* Router look-ahead, its read half (NeutronStar fork page, "Cross-layer
  * expert prefetch": the next layer's router runs on this layer's hidden
  * state and the experts it predicts are read while the GPU still computes).
@@ -220,7 +292,7 @@ int moe_topk_rows(const float *scores, int32_t rows, int32_t n, int32_t k, int32
  * experts ids [n_ids] int32 (device memory, e.g. that topk_idx; entries
  * outside [0, n_expert) are skipped on the device) of the layer w: bit 0 of
  * `which` selects gate, bit 1 up, bit 2 down (for MOE_DT_Q8B32 the codes
- * and their scales), and `rows` > 0 limits the read to the leading rows of
+ * and their scales, for MOE_DT_F8B128 the codes), and `rows` > 0 limits the read to the leading rows of
  * each selected matrix (gate and up have d_ff rows, down d_model; 0: all).
  * It writes no memory, so no result of any call changes; the reads leave
  * those weights in the device's memory-side cache (the Infinity Cache),

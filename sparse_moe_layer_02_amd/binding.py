@@ -15,8 +15,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_mi355x.so")
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE = range(5)
-SCORE = {"sigmoid": 0, "sqrt_softplus": 1}
-DTYPE = {"f32": 0, "bf16": 1, "q8b32": 2}
+SCORE = {"sigmoid": 0, "sqrt_softplus": 1, "softmax": 2}
+DTYPE = {"f32": 0, "bf16": 1, "q8b32": 2, "f8b128": 3}
 PATH = {"auto": 0, "decode": 1, "prefill": 2}
 DECODE_MAX_TOKENS = 8
 
@@ -34,6 +34,11 @@ class moe_config(ctypes.Structure):
                 ("d_ff_shared", ctypes.c_int32), ("score", ctypes.c_int32),
                 ("route_scale", ctypes.c_float), ("act_dtype", ctypes.c_int32),
                 ("w_dtype", ctypes.c_int32), ("path", ctypes.c_int32)]
+
+
+class moe_groups(ctypes.Structure):
+    _fields_ = [("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("normalise", ctypes.c_int32)]
 
 
 class moe_mat(ctypes.Structure):
@@ -60,7 +65,8 @@ class moe_debug(ctypes.Structure):
 
 EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_select", "moe_permute", "moe_expert_ffn",
            "moe_combine", "moe_layer_forward", "moe_layer_forward_noalloc", "moe_topk_rows",
-           "moe_prefetch_experts", "moe_status_str")
+           "moe_prefetch_experts", "moe_select_grouped", "moe_route_grouped", "moe_layer_forward_grouped",
+           "moe_quantize_rows", "moe_block_matmul", "moe_block_matmul_workspace_bytes", "moe_status_str")
 STATIC_SCRATCH_BYTES = 64 << 20  # MOE_STATIC_SCRATCH_BYTES
 TOPK_ROWS_MAX_N = 65536  # MOE_TOPK_ROWS_MAX_N
 PREFETCH_MAX_IDS = 65536  # MOE_PREFETCH_MAX_IDS
@@ -93,10 +99,19 @@ def load(path: str = LIB_PATH):
     I = ctypes.c_int32
     lib.moe_topk_rows.argtypes = [P, I, I, I, P, P, ctypes.POINTER(ctypes.c_void_p), P]
     lib.moe_prefetch_experts.argtypes = [C, W, P, I, I, I, I, ctypes.POINTER(ctypes.c_void_p), P]
+    G = ctypes.POINTER(moe_groups)
+    S, D = ctypes.c_size_t, ctypes.POINTER(moe_debug)
+    lib.moe_select_grouped.argtypes = [C, G, P, P, P, P, P]
+    lib.moe_route_grouped.argtypes = [C, G, P, P, P, P, P, P, P, S, P]
+    lib.moe_layer_forward_grouped.argtypes = [C, G, P, W, P, I, D, P, S, P]
+    lib.moe_quantize_rows.argtypes = [P, I, I, I, ctypes.c_int64, P, P, P]
+    lib.moe_block_matmul.argtypes = [P, I, P, P, P, I, I, I, P, I, P, S, P]
+    lib.moe_block_matmul_workspace_bytes.argtypes = [I, I, I]
     lib.moe_status_str.argtypes = [ctypes.c_int]
     lib.moe_status_str.restype = ctypes.c_char_p
     for name in EXPORTS[1:-1]:
         getattr(lib, name).restype = ctypes.c_int
+    lib.moe_block_matmul_workspace_bytes.restype = ctypes.c_size_t
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -255,6 +270,190 @@ def moe_prefetch_experts(cfg, weights: moe_weights, ids, which=3, rows=0, workgr
     ev = None if events is None else ctypes.cast(events, ctypes.POINTER(ctypes.c_void_p))
     return _check(lib.moe_prefetch_experts(ctypes.byref(cfg), ctypes.byref(weights), ptr(ids), ids.numel(),
                                            which, rows, workgroups, ev, _stream(stream)), lib)
+
+
+# ---------------------------------------------------------------------------
+# expert groups and the 8-bit operators.  These take typed tensors and check
+# their shapes, types and layout against each other; the launch goes to the
+# tensors' device.
+# ---------------------------------------------------------------------------
+
+def make_groups(n_group=1, topk_group=1, group_top=1, normalise=True) -> moe_groups:
+    return moe_groups(n_group, topk_group, group_top, int(normalise))
+
+
+def _invalid(msg):
+    raise MoeError(MOE_ERR_INVALID, "invalid argument: " + msg)
+
+
+def _need(ok, msg):
+    if not ok:
+        _invalid(msg)
+
+
+def _on(device):
+    """Makes ``device`` current for a launch (nothing to do if it is)."""
+    import contextlib
+    import torch
+    _need(device.type == "cuda", "tensors must be on the GPU")
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _row_dtype(t):
+    """DTYPE of activation rows: float32, or bf16 (as bfloat16, or its bits)."""
+    import torch
+    if t.dtype == torch.float32:
+        return DTYPE["f32"]
+    _need(t.dtype in (torch.bfloat16, torch.int16), "expected float32 or bfloat16 rows, got %s" % t.dtype)
+    return DTYPE["bf16"]
+
+
+def _is_f8(t):
+    import torch
+    return t.dtype in (torch.float8_e4m3fn, torch.uint8)
+
+
+def _dense(t, shape, msg):
+    _need(tuple(t.shape) == tuple(shape) and t.is_contiguous(), "%s must be contiguous %s" % (msg, tuple(shape)))
+
+
+def _same_device(first, *rest):
+    for t in rest:
+        _need(t is None or t.device == first.device, "tensors on different devices")
+
+
+def scale_ld(cols: int) -> int:
+    """Bytes of one row's scales (MOE_F8_SCALE_LD)."""
+    return (cols + 511) // 512 * 4
+
+
+def _selection_args(cfg, bias, topk_idx, topk_w):
+    import torch
+    T, E, k = cfg.n_tokens, cfg.n_expert, cfg.top_k
+    _dense(topk_idx, (T, k), "topk_idx")
+    _dense(topk_w, (T, k), "topk_w")
+    _need(topk_idx.dtype == torch.int32 and topk_w.dtype == torch.float32, "topk_idx is int32, topk_w float32")
+    _need(bias is None or (bias.dtype == torch.float32 and bias.numel() == E and bias.is_contiguous()),
+          "bias must be contiguous float32 [E]")
+
+
+def _rows_match(cfg, x):
+    _need(x.dim() == 2 and tuple(x.shape) == (cfg.n_tokens, cfg.d_model) and x.is_contiguous(),
+          "x must be contiguous [T, d]")
+    _need(_row_dtype(x) == cfg.act_dtype, "x is not of the config's activation type")
+
+
+def _ref(groups):
+    return None if groups is None else ctypes.byref(groups)
+
+
+def _bytes(ws):
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def moe_select_grouped(cfg, groups, logits, bias, topk_idx, topk_w, stream=None):
+    """Selection from ``logits`` [T, E] fp32 with expert groups (``make_groups``; None: flat)."""
+    import torch
+    lib = load()
+    _need(logits.dtype == torch.float32, "logits must be float32")
+    _dense(logits, (cfg.n_tokens, cfg.n_expert), "logits")
+    _selection_args(cfg, bias, topk_idx, topk_w)
+    _same_device(logits, bias, topk_idx, topk_w)
+    with _on(logits.device):
+        return _check(lib.moe_select_grouped(ctypes.byref(cfg), _ref(groups), ptr(logits), ptr(bias), ptr(topk_idx),
+                                             ptr(topk_w), _stream(stream)), lib)
+
+
+def moe_route_grouped(cfg, groups, x, w_router, bias, logits, topk_idx, topk_w, ws, stream=None):
+    """Router product and selection with expert groups; ``ws`` is needed only if ``logits`` is None."""
+    import torch
+    lib = load()
+    _rows_match(cfg, x)
+    _need(w_router.dtype == torch.float32, "w_router must be float32")
+    _dense(w_router, (cfg.n_expert, cfg.d_model), "w_router")
+    if logits is not None:
+        _need(logits.dtype == torch.float32, "logits must be float32")
+        _dense(logits, (cfg.n_tokens, cfg.n_expert), "logits")
+    _selection_args(cfg, bias, topk_idx, topk_w)
+    _same_device(x, w_router, bias, logits, topk_idx, topk_w, ws)
+    with _on(x.device):
+        return _check(lib.moe_route_grouped(ctypes.byref(cfg), _ref(groups), ptr(x), ptr(w_router), ptr(bias),
+                                            ptr(logits), ptr(topk_idx), ptr(topk_w), ptr(ws), _bytes(ws),
+                                            _stream(stream)), lib)
+
+
+def moe_layer_forward_grouped(cfg, groups, x, weights: moe_weights, y, ws, debug: dict | None = None, stream=None,
+                              stage_events=None):
+    """moe_layer_forward with expert groups; y float32, or (f8b128 weights) bfloat16."""
+    lib = load()
+    _rows_match(cfg, x)
+    _dense(y, (cfg.n_tokens, cfg.d_model), "y")
+    _same_device(x, y, ws)
+    dbg = _debug_struct(debug, stage_events)
+    with _on(x.device):
+        return _check(lib.moe_layer_forward_grouped(ctypes.byref(cfg), _ref(groups), ptr(x), ctypes.byref(weights),
+                                                    ptr(y), _row_dtype(y), ctypes.byref(dbg) if dbg else None,
+                                                    ptr(ws), _bytes(ws), _stream(stream)), lib)
+
+
+def moe_quantize_rows(x, q, scale, stream=None):
+    """Rows ``x`` [rows, cols] (float32 or bfloat16, unit column stride) to e4m3 codes ``q`` [rows, cols]
+    (float8_e4m3fn or uint8) and e8m0 scale bytes ``scale`` [rows, scale_ld(cols)] uint8."""
+    import torch
+    lib = load()
+    _need(x.dim() == 2 and (x.shape[1] <= 1 or x.stride(1) == 1), "x must be [rows, cols] with adjacent columns")
+    rows, cols = x.shape
+    dt = _row_dtype(x)
+    _need(_is_f8(q) and scale.dtype == torch.uint8, "q is float8_e4m3fn or uint8, scale uint8")
+    _dense(q, (rows, cols), "q")
+    _dense(scale, (rows, scale_ld(cols)), "scale")
+    _same_device(x, q, scale)
+    ld = x.stride(0) if rows > 1 else cols
+    with _on(x.device):
+        return _check(lib.moe_quantize_rows(ptr(x), dt, rows, cols, ld, ptr(q), ptr(scale), _stream(stream)), lib)
+
+
+def moe_block_matmul_workspace_bytes(x_dtype, m, k) -> int:
+    return load().moe_block_matmul_workspace_bytes(DTYPE.get(x_dtype, x_dtype), m, k)
+
+
+def block_matmul_workspace(x, n):
+    """A workspace tensor for moe_block_matmul of rows ``x`` with n weight rows (None if none is needed)."""
+    import torch
+    del n  # the workspace holds the quantised rows only
+    if _is_f8(x):
+        return None
+    size = moe_block_matmul_workspace_bytes(_row_dtype(x), *x.shape)
+    return torch.empty(size, dtype=torch.uint8, device=x.device)
+
+
+def moe_block_matmul(x, x_scale, w, w_scale, out, ws=None, stream=None):
+    """out [m, n] (float32 or bfloat16) = x [m, k] w[n, k]^T with e4m3 operands: ``x`` codes with their
+    ``x_scale`` bytes (moe_quantize_rows), or float32 / bfloat16 rows (x_scale None, ``ws`` needed); ``w`` codes
+    with ``w_scale`` [ceil(n/128), ceil(k/128)] float32."""
+    import torch
+    lib = load()
+    _need(x.dim() == 2 and w.dim() == 2, "x and w must have two dimensions")
+    (m, k), n = x.shape, w.shape[0]
+    f8 = _is_f8(x)
+    _dense(x, (m, k), "x")
+    _need(_is_f8(w), "w must be float8_e4m3fn or uint8")
+    _dense(w, (n, k), "w")
+    _need(w_scale.dtype == torch.float32, "w_scale must be float32")
+    _dense(w_scale, (-(-n // 128), -(-k // 128)), "w_scale")
+    _dense(out, (m, n), "out")
+    if f8:
+        _need(x_scale is not None and x_scale.dtype == torch.uint8, "e4m3 rows need their scale bytes")
+        _dense(x_scale, (m, scale_ld(k)), "x_scale")
+    else:
+        _need(x_scale is None, "x_scale goes with e4m3 rows only")
+    _same_device(x, x_scale, w, w_scale, out, ws)
+    with _on(x.device):
+        return _check(lib.moe_block_matmul(ptr(x), DTYPE["f8b128"] if f8 else _row_dtype(x), ptr(x_scale), ptr(w),
+                                           ptr(w_scale), m, n, k, ptr(out), _row_dtype(out), ptr(ws), _bytes(ws),
+                                           _stream(stream)), lib)
 
 
 def workspace(cfg: moe_config, device="cuda"):

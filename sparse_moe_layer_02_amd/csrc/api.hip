@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "common.h"
+#include "f8_dev.h"
 #include "kernels.h"
 #include "prefetch.h"
 #include "topk_rows.h"
@@ -40,13 +41,14 @@ int validate_config(const moe_config* c) {
     if (c->top_k < 1 || c->top_k > c->n_expert || c->top_k > 32) return MOE_ERR_INVALID;
     if (c->n_shared != 0 && c->n_shared != 1) return MOE_ERR_INVALID;
     if (c->n_shared == 1 && c->d_ff_shared < 1) return MOE_ERR_INVALID;
-    if (c->score != MOE_SCORE_SIGMOID && c->score != MOE_SCORE_SQRT_SOFTPLUS) return MOE_ERR_INVALID;
+    if (c->score < MOE_SCORE_SIGMOID || c->score > MOE_SCORE_SOFTMAX) return MOE_ERR_INVALID;
     if (!(c->route_scale > 0.0f) || isinf(c->route_scale)) return MOE_ERR_INVALID;
-    if (c->act_dtype < 0 || c->act_dtype > 1 || c->w_dtype < 0 || c->w_dtype > 2) return MOE_ERR_INVALID;
+    if (c->act_dtype < 0 || c->act_dtype > 1 || c->w_dtype < 0 || c->w_dtype > MOE_DT_F8B128) return MOE_ERR_INVALID;
     if (c->path < MOE_PATH_AUTO || c->path > MOE_PATH_PREFILL) return MOE_ERR_INVALID;
     const bool pair_ok = (c->act_dtype == MOE_DT_F32 && c->w_dtype == MOE_DT_F32) ||
                          (c->act_dtype == MOE_DT_BF16 && c->w_dtype == MOE_DT_BF16) ||
-                         (c->act_dtype == MOE_DT_BF16 && c->w_dtype == MOE_DT_Q8B32);
+                         (c->act_dtype == MOE_DT_BF16 && c->w_dtype == MOE_DT_Q8B32) ||
+                         (c->act_dtype == MOE_DT_BF16 && c->w_dtype == MOE_DT_F8B128);
     if (!pair_ok) return MOE_ERR_UNSUPPORTED;
     if (c->d_model % 64 || c->d_ff % 64 || (c->n_shared && c->d_ff_shared % 64)) return MOE_ERR_UNSUPPORTED;
     if ((size_t)c->d_model > (1u << 20) || (size_t)c->d_ff > (1u << 20) ||
@@ -66,10 +68,13 @@ int ldh_of(const moe_config* c) {
 // tile that hold rows, so a short tile costs its weight stream, not a full
 // 256-row product.  Fewer rows per expert: 64-row tiles (every expert
 // bandwidth-bound; the register-staged kernels keep more loads in flight per
-// CU).  int8 weights always take 64-row tiles (grouped_gemm_q8.hip).
+// CU).  int8 weights always take 64-row tiles (grouped_gemm_q8.hip).  e4m3
+// weights: the rows one pass over an expert's weights serves (f8_stream.hip).
+constexpr int F8_BM_MIN = 16;
 int gemm_bm(const moe_config* c) {
     if (c->w_dtype == MOE_DT_Q8B32) return 64;
     const long n = (long)c->n_tokens * c->top_k;
+    if (c->w_dtype == MOE_DT_F8B128) return n <= 4L * c->n_expert ? 16 : n <= 20L * c->n_expert ? 32 : 64;
     return n >= 96L * c->n_expert ? 256 : 64;
 }
 
@@ -95,7 +100,8 @@ Layout make_layout(const moe_config* c) {
     const size_t d = (size_t)c->d_model, n = T * k;
     const size_t hsz = c->act_dtype == MOE_DT_BF16 ? 2 : 4;
     L.n_blk = (int)((n + PERM_BLOCK - 1) / PERM_BLOCK);
-    L.max_tiles = max_tiles_of(c, GEMM_BM);  // the smallest tile: capacity for any bm
+    const bool f8 = c->w_dtype == MOE_DT_F8B128;
+    L.max_tiles = max_tiles_of(c, f8 ? F8_BM_MIN : GEMM_BM);  // the smallest tile: capacity for any bm
     size_t o = 0;
     auto take = [&](size_t bytes) {
         size_t at = o;
@@ -113,11 +119,16 @@ Layout make_layout(const moe_config* c) {
     L.meta = take(META_WORDS * 4);
     L.active = take(E * 4);
     L.tiles = take((size_t)L.max_tiles * 8);
-    L.h = take((n + (c->n_shared ? T : 0)) * (size_t)ldh_of(c) * hsz);
+    const size_t hrows = n + (c->n_shared ? T : 0);
+    L.h = take(f8 ? 0 : hrows * (size_t)ldh_of(c) * hsz);
     L.slot_out = take(n * d * 4);
     L.shared_out = take(c->n_shared ? T * d * 4 : 0);
     L.scores = take(T * E * 4);
     L.dslots = take((size_t)n_dslots_of(c) * sizeof(DecodeSlot));
+    L.xq = take(f8 ? T * d : 0);
+    L.xe = take(f8 ? T * f8_scale_ld(c->d_model) : 0);
+    L.hq = take(f8 ? hrows * (size_t)ldh_of(c) : 0);
+    L.he = take(f8 ? hrows * f8_scale_ld(ldh_of(c)) : 0);
     L.total = o;
     return L;
 }
@@ -135,7 +146,9 @@ int check_ws(const moe_config* c, const void* ws, size_t ws_bytes) {
 
 bool mat_ok(const moe_config* c, const moe_mat& m) {
     if (!ptr_ok(m.q)) return false;
-    if (c->w_dtype == MOE_DT_Q8B32 && (m.scale == nullptr || ((uintptr_t)m.scale & 3u))) return false;
+    if ((c->w_dtype == MOE_DT_Q8B32 || c->w_dtype == MOE_DT_F8B128) &&
+        (m.scale == nullptr || ((uintptr_t)m.scale & 3u)))
+        return false;
     return true;
 }
 
@@ -150,7 +163,7 @@ int check_weights(const moe_config* c, const moe_weights* w, bool router) {
 
 int device_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_DEVICE; }
 
-MatRef ref(const moe_mat& m) { return MatRef{m.q, m.scale}; }
+MatRef ref(const moe_mat& m) { return MatRef{m.q, static_cast<const uint16_t*>(m.scale)}; }
 
 PermArgs perm_args(const moe_config* c, const Layout& L, void* ws, const int32_t* idx, int32_t* off,
                    int32_t* perm, int32_t* inv) {
@@ -233,12 +246,25 @@ hipError_t run_bf16_experts(const FfnArgs& f, hipStream_t st, const KTime& kg = 
     return launch_down_mfma(f, st, kd);
 }
 
-hipError_t run_expert_kernels(const FfnArgs& f, hipStream_t st) {
-    hipError_t e;
-    if (f.wdt == MOE_DT_BF16) return run_bf16_experts(f, st);
-    e = q8_mfma_gateup(f) ? launch_gateup_mfma_q8(f, st) : launch_gateup_gemv(f, st);
+// e4m3 experts: x quantised once per token, then gate/up (which quantises h)
+// and down.
+hipError_t run_f8_experts(const FfnArgs& f, const Layout& L, void* ws, hipStream_t st, const KTime& kg = KTime(),
+                          const KTime& kd = KTime()) {
+    F8Ffn a{f, at<uint8_t>(ws, L.xq), at<uint8_t>(ws, L.xe), at<uint8_t>(ws, L.hq), at<uint8_t>(ws, L.he)};
+    hipError_t e = launch_quantize_rows(QuantArgs{f.x, MOE_DT_BF16, f.T, f.d, f.d, a.xq, a.xe}, st, kg.first());
     if (e != hipSuccess) return e;
-    return q8_mfma_down(f) ? launch_down_mfma_q8(f, st) : launch_down_slots_gemv(f, st);
+    if ((e = launch_f8_gateup(a, st, kg.last())) != hipSuccess) return e;
+    return launch_f8_down(a, st, kd);
+}
+
+hipError_t run_expert_kernels(const FfnArgs& f, const Layout& L, void* ws, hipStream_t st,
+                              const KTime& kg = KTime(), const KTime& kd = KTime()) {
+    hipError_t e;
+    if (f.wdt == MOE_DT_BF16) return run_bf16_experts(f, st, kg, kd);
+    if (f.wdt == MOE_DT_F8B128) return run_f8_experts(f, L, ws, st, kg, kd);
+    e = q8_mfma_gateup(f) ? launch_gateup_mfma_q8(f, st, kg) : launch_gateup_gemv(f, st, kg);
+    if (e != hipSuccess) return e;
+    return q8_mfma_down(f) ? launch_down_mfma_q8(f, st, kd) : launch_down_slots_gemv(f, st, kd);
 }
 
 // The caller's stage events (if any) as per-stage kernel timings.
@@ -269,8 +295,34 @@ SelectArgs select_args(const moe_config* c, const float* logits, const float* bi
 }
 
 
+// Groups that keep every group select nothing out; softmax scores need a
+// whole row's logits: both take the grouped selection (group_dev.h).
+bool is_grouped(const moe_config* c, const GroupArgs& g) {
+    return c->score == MOE_SCORE_SOFTMAX || g.topk_group < g.n_group || !g.normalise;
+}
+
+hipError_t run_select(const moe_config* c, const GroupArgs& g, const SelectArgs& a, hipStream_t st,
+                      const KTime& kt = KTime()) {
+    return is_grouped(c, g) ? launch_group_topk(a, g, st, kt) : launch_topk(a, st, kt);
+}
+
+int check_groups(const moe_config* c, const moe_groups* g, GroupArgs* out) {
+    *out = GroupArgs();
+    if (!g) return MOE_OK;
+    if (g->n_group < 1 || g->n_group > 64 || c->n_expert % g->n_group) return MOE_ERR_INVALID;
+    if (g->topk_group < 1 || g->topk_group > g->n_group) return MOE_ERR_INVALID;
+    if ((g->group_top != 1 && g->group_top != 2) || (g->normalise != 0 && g->normalise != 1)) return MOE_ERR_INVALID;
+    if (c->top_k > g->topk_group * (c->n_expert / g->n_group)) return MOE_ERR_INVALID;
+    out->n_group = g->n_group;
+    out->topk_group = g->topk_group;
+    out->group_top = g->group_top;
+    out->normalise = g->normalise;
+    out->inv_size = (float)g->n_group / (float)c->n_expert;
+    return MOE_OK;
+}
+
 // Arguments of a whole-layer call other than its workspace.
-int check_layer_args(const moe_config* cfg, const void* x, const moe_weights* w, const float* y,
+int check_layer_args(const moe_config* cfg, const void* x, const moe_weights* w, const void* y,
                      const moe_debug* dbg) {
     int s = validate_config(cfg);
     if (s) return s;
@@ -285,8 +337,8 @@ int check_layer_args(const moe_config* cfg, const void* x, const moe_weights* w,
     return MOE_OK;
 }
 
-int enqueue_layer(const moe_config* cfg, const void* x, const moe_weights* w, float* y, moe_debug* dbg,
-                  void* ws, void* stream);
+int enqueue_layer(const moe_config* cfg, const GroupArgs& g, const void* x, const moe_weights* w, void* y, int ydt,
+                  moe_debug* dbg, void* ws, void* stream);
 
 // ---------------------------------------------------------------------------
 // The library's own scratch for moe_layer_forward_noalloc: one array per GPU
@@ -339,10 +391,13 @@ const char* moe_status_str(int status) {
     }
 }
 
-int moe_route(const moe_config* cfg, const void* x, const float* w_router, const float* bias,
-              float* logits, int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes, void* stream) {
+int moe_route_grouped(const moe_config* cfg, const moe_groups* groups, const void* x, const float* w_router,
+                      const float* bias, float* logits, int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,
+                      void* stream) {
     int s = validate_config(cfg);
     if (s) return s;
+    GroupArgs g;
+    if ((s = check_groups(cfg, groups, &g))) return s;
     if (!ptr_ok(x) || !ptr_ok(w_router) || !opt_elt_ok(bias) || !opt_elt_ok(logits) || !elt_ok(topk_idx) ||
         !elt_ok(topk_w))
         return MOE_ERR_INVALID;
@@ -353,18 +408,78 @@ int moe_route(const moe_config* cfg, const void* x, const float* w_router, const
     RouteArgs r{x, w_router, cfg->n_tokens, cfg->d_model, cfg->n_expert, cfg->act_dtype, lg,
                 cfg->path == MOE_PATH_PREFILL};
     hipError_t e = launch_router_logits(r, st);
-    if (e == hipSuccess) e = launch_topk(select_args(cfg, lg, bias, topk_idx, topk_w), st);
+    if (e == hipSuccess) e = run_select(cfg, g, select_args(cfg, lg, bias, topk_idx, topk_w), st);
     return device_status(e);
+}
+
+int moe_route(const moe_config* cfg, const void* x, const float* w_router, const float* bias,
+              float* logits, int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes, void* stream) {
+    return moe_route_grouped(cfg, nullptr, x, w_router, bias, logits, topk_idx, topk_w, ws, ws_bytes, stream);
+}
+
+int moe_select_grouped(const moe_config* cfg, const moe_groups* groups, const float* logits, const float* bias,
+                       int32_t* topk_idx, float* topk_w, void* stream) {
+    int s = validate_config(cfg);
+    if (s) return s;
+    GroupArgs g;
+    if ((s = check_groups(cfg, groups, &g))) return s;
+    if (!elt_ok(logits) || !opt_elt_ok(bias) || !elt_ok(topk_idx) || !elt_ok(topk_w)) return MOE_ERR_INVALID;
+    SelectArgs a = select_args(cfg, logits, bias, topk_idx, topk_w);
+    a.generic_only = cfg->path == MOE_PATH_PREFILL;  // lets tests reach the generic kernel at E = 256
+    return device_status(run_select(cfg, g, a, static_cast<hipStream_t>(stream)));
 }
 
 int moe_select(const moe_config* cfg, const float* logits, const float* bias, int32_t* topk_idx,
                float* topk_w, void* stream) {
-    int s = validate_config(cfg);
-    if (s) return s;
-    if (!elt_ok(logits) || !opt_elt_ok(bias) || !elt_ok(topk_idx) || !elt_ok(topk_w)) return MOE_ERR_INVALID;
-    SelectArgs a = select_args(cfg, logits, bias, topk_idx, topk_w);
-    a.generic_only = cfg->path == MOE_PATH_PREFILL;  // lets tests reach the generic kernel at E = 256
-    return device_status(launch_topk(a, static_cast<hipStream_t>(stream)));
+    return moe_select_grouped(cfg, nullptr, logits, bias, topk_idx, topk_w, stream);
+}
+
+namespace {
+constexpr int F8_MAX_DIM = 1 << 20;
+bool f8_cols_ok(int32_t k) { return k >= 16 && k <= F8_MAX_DIM && k % 16 == 0; }
+}  // namespace
+
+int moe_quantize_rows(const void* x, int32_t x_dtype, int32_t rows, int32_t cols, int64_t ldx, uint8_t* q,
+                      uint8_t* scale, void* stream) {
+    if (x_dtype != MOE_DT_F32 && x_dtype != MOE_DT_BF16) return MOE_ERR_INVALID;
+    if (rows < 0 || !f8_cols_ok(cols)) return MOE_ERR_INVALID;
+    const int64_t per16 = x_dtype == MOE_DT_BF16 ? 8 : 4;  // elements in 16 bytes
+    if (ldx < cols || ldx % per16 || ldx > INT64_MAX / 4 / (rows ? rows : 1)) return MOE_ERR_INVALID;
+    if (rows == 0) return MOE_OK;
+    if (!ptr_ok(x) || !ptr_ok(q) || !elt_ok(scale)) return MOE_ERR_INVALID;
+    return device_status(
+        launch_quantize_rows(QuantArgs{x, x_dtype, rows, cols, ldx, q, scale}, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_block_matmul_workspace_bytes(int32_t x_dtype, int32_t m, int32_t k) {
+    if ((x_dtype != MOE_DT_F32 && x_dtype != MOE_DT_BF16) || m < 0 || m > F8_MAX_DIM || !f8_cols_ok(k)) return 0;
+    return align256((size_t)m * k) + align256((size_t)m * f8_scale_ld(k));
+}
+
+int moe_block_matmul(const void* x, int32_t x_dtype, const uint8_t* x_scale, const uint8_t* w, const float* w_scale,
+                     int32_t m, int32_t n, int32_t k, void* out, int32_t out_dtype, void* ws, size_t ws_bytes,
+                     void* stream) {
+    static_assert(MOE_F8_SCALE_LD(513) == 8, "scale bytes of a row");
+    if (x_dtype != MOE_DT_F32 && x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_F8B128) return MOE_ERR_INVALID;
+    if (out_dtype != MOE_DT_F32 && out_dtype != MOE_DT_BF16) return MOE_ERR_INVALID;
+    if (m < 0 || m > F8_MAX_DIM || n < 1 || n > F8_MAX_DIM || !f8_cols_ok(k)) return MOE_ERR_INVALID;
+    const bool codes = x_dtype == MOE_DT_F8B128;
+    if (codes ? (m && !elt_ok(x_scale)) : x_scale != nullptr) return MOE_ERR_INVALID;
+    if (m == 0) return MOE_OK;
+    if (!ptr_ok(x) || !ptr_ok(w) || !elt_ok(w_scale) || !ptr_ok(out)) return MOE_ERR_INVALID;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    BlockArgs a{static_cast<const uint8_t*>(x), x_scale, w, w_scale, m, n, k, out, out_dtype};
+    if (!codes) {
+        if (!ptr_ok(ws)) return MOE_ERR_INVALID;
+        if (ws_bytes < moe_block_matmul_workspace_bytes(x_dtype, m, k)) return MOE_ERR_WORKSPACE;
+        uint8_t* q = static_cast<uint8_t*>(ws);
+        uint8_t* e = q + align256((size_t)m * k);
+        const hipError_t err = launch_quantize_rows(QuantArgs{x, x_dtype, m, k, k, q, e}, st);
+        if (err != hipSuccess) return MOE_ERR_DEVICE;
+        a.xq = q;
+        a.xe = e;
+    }
+    return device_status(launch_block_matmul(a, st));
 }
 
 int moe_topk_rows(const float* scores, int32_t rows, int32_t n, int32_t k, int32_t* idx, float* vals,
@@ -401,7 +516,7 @@ int moe_prefetch_experts(const moe_config* cfg, const moe_weights* w, const int3
     // every matrix of an expert holds F * d elements: gate and up F rows of d,
     // down d rows of F
     const int64_t elems = (int64_t)cfg->d_ff * cfg->d_model;
-    const int64_t esize = cfg->w_dtype == MOE_DT_F32 ? 4 : cfg->w_dtype == MOE_DT_BF16 ? 2 : 1;
+    const int64_t esize = cfg->w_dtype == MOE_DT_F32 ? 4 : cfg->w_dtype == MOE_DT_BF16 ? 2 : 1;  // (F8B128: codes)
     if (elems * esize > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;  // one buffer descriptor per expert matrix
     const bool q8 = cfg->w_dtype == MOE_DT_Q8B32;
     const moe_mat* mats[3] = {&w->gate, &w->up, &w->down};
@@ -458,7 +573,7 @@ int moe_expert_ffn(const moe_config* cfg, const void* x, const moe_weights* w, c
     FfnArgs f = ffn_args(cfg, L, ws, x, w, offsets, perm_rows, topk_w);
     f.slot_out = slot_out;
     f.shared_out = cfg->n_shared ? shared_out : nullptr;
-    return device_status(run_expert_kernels(f, st));
+    return device_status(run_expert_kernels(f, L, ws, st));
 }
 
 int moe_combine(const moe_config* cfg, const float* slot_out, const float* shared_out, float* y, void* stream) {
@@ -474,7 +589,19 @@ int moe_layer_forward(const moe_config* cfg, const void* x, const moe_weights* w
     int s = check_layer_args(cfg, x, w, y, dbg);
     if (s) return s;
     if ((s = check_ws(cfg, ws, ws_bytes))) return s;
-    return enqueue_layer(cfg, x, w, y, dbg, ws, stream);
+    return enqueue_layer(cfg, GroupArgs(), x, w, y, MOE_DT_F32, dbg, ws, stream);
+}
+
+int moe_layer_forward_grouped(const moe_config* cfg, const moe_groups* groups, const void* x, const moe_weights* w,
+                              void* y, int32_t y_dtype, moe_debug* dbg, void* ws, size_t ws_bytes, void* stream) {
+    int s = check_layer_args(cfg, x, w, y, dbg);
+    if (s) return s;
+    GroupArgs g;
+    if ((s = check_groups(cfg, groups, &g))) return s;
+    if (y_dtype != MOE_DT_F32 && y_dtype != MOE_DT_BF16) return MOE_ERR_INVALID;
+    if (y_dtype == MOE_DT_BF16 && cfg->w_dtype != MOE_DT_F8B128) return MOE_ERR_UNSUPPORTED;
+    if ((s = check_ws(cfg, ws, ws_bytes))) return s;
+    return enqueue_layer(cfg, g, x, w, y, y_dtype, dbg, ws, stream);
 }
 
 int moe_layer_forward_noalloc(const moe_config* cfg, const void* x, const moe_weights* w, float* y,
@@ -484,7 +611,7 @@ int moe_layer_forward_noalloc(const moe_config* cfg, const void* x, const moe_we
     if (make_layout(cfg).total > (size_t)MOE_STATIC_SCRATCH_BYTES) return MOE_ERR_WORKSPACE;
     void* scratch_ptr = nullptr;
     if ((s = static_scratch(&scratch_ptr))) return s;
-    return enqueue_layer(cfg, x, w, y, dbg, scratch_ptr, stream);
+    return enqueue_layer(cfg, GroupArgs(), x, w, y, MOE_DT_F32, dbg, scratch_ptr, stream);
 }
 
 }  // extern "C"
@@ -492,10 +619,11 @@ int moe_layer_forward_noalloc(const moe_config* cfg, const void* x, const moe_we
 namespace {
 
 // The layer's launches over a workspace `ws` already checked to be large enough.
-int enqueue_layer(const moe_config* cfg, const void* x, const moe_weights* w, float* y, moe_debug* dbg,
-                  void* ws, void* stream) {
-    const bool decode = cfg->path == MOE_PATH_DECODE ||
-                        (cfg->path == MOE_PATH_AUTO && cfg->n_tokens <= MOE_DECODE_MAX_TOKENS);
+int enqueue_layer(const moe_config* cfg, const GroupArgs& g, const void* x, const moe_weights* w, void* y, int ydt,
+                  moe_debug* dbg, void* ws, void* stream) {
+    const bool decode = cfg->w_dtype != MOE_DT_F8B128 &&  // (e4m3 layers have one path)
+                        (cfg->path == MOE_PATH_DECODE ||
+                         (cfg->path == MOE_PATH_AUTO && cfg->n_tokens <= MOE_DECODE_MAX_TOKENS));
     const Layout L = make_layout(cfg);
     hipStream_t st = static_cast<hipStream_t>(stream);
 
@@ -517,23 +645,20 @@ int enqueue_layer(const moe_config* cfg, const void* x, const moe_weights* w, fl
         dr.s = select_args(cfg, logits, w->bias, idx, wts);
         dr.p = perm_args(cfg, L, ws, idx, off, perm, inv);
         dr.f = ffn_args(cfg, L, ws, x, w, off, perm, wts);
-        dr.f.y = y;
+        dr.f.y = static_cast<float*>(y);
         dr.scores = at<float>(ws, L.scores);
+        dr.g = g;
+        dr.grouped = is_grouped(cfg, g);
         return device_status(launch_decode(dr, kt, st));
     }
     hipError_t e = launch_router_logits(r, st, kt[0]);
-    if (e == hipSuccess) e = launch_topk(select_args(cfg, logits, w->bias, idx, wts), st, kt[1]);
+    if (e == hipSuccess) e = run_select(cfg, g, select_args(cfg, logits, w->bias, idx, wts), st, kt[1]);
     if (e == hipSuccess) e = launch_permute(perm_args(cfg, L, ws, idx, off, perm, inv), st, kt[2]);
     if (e != hipSuccess) return MOE_ERR_DEVICE;
     FfnArgs f = ffn_args(cfg, L, ws, x, w, off, perm, wts);
-    if (f.wdt == MOE_DT_BF16) {
-        e = run_bf16_experts(f, st, kt[3], kt[4]);
-    } else {
-        e = q8_mfma_gateup(f) ? launch_gateup_mfma_q8(f, st, kt[3]) : launch_gateup_gemv(f, st, kt[3]);
-        if (e == hipSuccess) e = q8_mfma_down(f) ? launch_down_mfma_q8(f, st, kt[4]) : launch_down_slots_gemv(f, st, kt[4]);
-    }
+    e = run_expert_kernels(f, L, ws, st, kt[3], kt[4]);
     if (e == hipSuccess) {
-        CombineArgs c{f.slot_out, f.shared_out, y, cfg->n_tokens, cfg->top_k, cfg->d_model};
+        CombineArgs c{f.slot_out, f.shared_out, y, cfg->n_tokens, cfg->top_k, cfg->d_model, ydt};
         e = launch_combine(c, st, kt[5]);
     }
     return device_status(e);

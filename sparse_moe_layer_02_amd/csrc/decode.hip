@@ -24,6 +24,7 @@
 // memory bandwidth (NeutronStar README, MTP paragraph and closing paragraph).
 #include "common.h"
 #include "gemv_dev.h"
+#include "group_dev.h"
 #include "kernels.h"
 #include "permute_dev.h"
 #include "route_dev.h"
@@ -208,7 +209,9 @@ __device__ void group_in_registers(const DecodeRouteArgs& a, const int32_t* s_id
     }
 }
 
-template <int KPL, int EFIX, int WF, int AF, int MT>
+// GROUPED: selection with expert groups or softmax scores, from the logits
+// (the scores launch 1 wrote are not read).
+template <int KPL, int EFIX, int WF, int AF, int MT, bool GROUPED>
 __global__ __launch_bounds__(DS_THREADS) void decode_select_kernel(DecodeRouteArgs a) {
     const int lane = lane_id(), wave = wave_index();
     if (blockIdx.x > 0) {
@@ -226,9 +229,16 @@ __global__ __launch_bounds__(DS_THREADS) void decode_select_kernel(DecodeRouteAr
     const int E = a.r.E, T = a.r.T, k = a.s.k, n = T * k;
     if (wave < T) {
         float wl;
-        const int my = topk_token<KPL, EFIX, true>(a.scores + (size_t)wave * E, a.s.bias, E, k, a.s.score,
-                                                   a.s.route_scale, a.s.topk_idx + (size_t)wave * k,
-                                                   a.s.topk_w + (size_t)wave * k, &wl);
+        int my;
+        if constexpr (GROUPED) {
+            __shared__ uint32_t s_key[DS_WAVES][KPL * WAVE];
+            my = group_topk_token<KPL>(a.r.logits + (size_t)wave * E, a.s.bias, E, k, a.s.score, a.s.route_scale, a.g,
+                                       s_key[wave], a.s.topk_idx + (size_t)wave * k, a.s.topk_w + (size_t)wave * k,
+                                       &wl);
+        } else {
+            my = topk_token<KPL, EFIX, true>(a.scores + (size_t)wave * E, a.s.bias, E, k, a.s.score, a.s.route_scale,
+                                             a.s.topk_idx + (size_t)wave * k, a.s.topk_w + (size_t)wave * k, &wl);
+        }
         if (lane < k) {
             s_idx[wave * k + lane] = my;
             s_w[wave * k + lane] = wl;
@@ -568,19 +578,19 @@ static void router_launch_mt(const DecodeRouteArgs& a, int mt, dim3 grid, hipStr
     else launch_kernel(decode_router_kernel<WF, AF, 8>, grid, 256, st, kt, a);
 }
 
-template <int KPL, int EFIX, int WF, int AF>
+template <int KPL, int EFIX, int WF, int AF, bool GROUPED>
 static void select_launch_mt(const DecodeRouteArgs& a, int mt, dim3 grid, hipStream_t st, const KTime& kt) {
-    if (mt == 1) launch_kernel(decode_select_kernel<KPL, EFIX, WF, AF, 1>, grid, DS_THREADS, st, kt, a);
-    else if (mt == 2) launch_kernel(decode_select_kernel<KPL, EFIX, WF, AF, 2>, grid, DS_THREADS, st, kt, a);
-    else if (mt == 4) launch_kernel(decode_select_kernel<KPL, EFIX, WF, AF, 4>, grid, DS_THREADS, st, kt, a);
-    else launch_kernel(decode_select_kernel<KPL, EFIX, WF, AF, 8>, grid, DS_THREADS, st, kt, a);
+    if (mt == 1) launch_kernel(decode_select_kernel<KPL, EFIX, WF, AF, 1, GROUPED>, grid, DS_THREADS, st, kt, a);
+    else if (mt == 2) launch_kernel(decode_select_kernel<KPL, EFIX, WF, AF, 2, GROUPED>, grid, DS_THREADS, st, kt, a);
+    else if (mt == 4) launch_kernel(decode_select_kernel<KPL, EFIX, WF, AF, 4, GROUPED>, grid, DS_THREADS, st, kt, a);
+    else launch_kernel(decode_select_kernel<KPL, EFIX, WF, AF, 8, GROUPED>, grid, DS_THREADS, st, kt, a);
 }
 
-template <int KPL, int EFIX>
+template <int KPL, int EFIX, bool GROUPED = false>
 static void select_launch_fmt(const DecodeRouteArgs& a, int mt, dim3 grid, hipStream_t st, const KTime& kt) {
-    if (a.f.wdt == MOE_DT_F32) select_launch_mt<KPL, EFIX, MOE_DT_F32, MOE_DT_F32>(a, mt, grid, st, kt);
-    else if (a.f.wdt == MOE_DT_BF16) select_launch_mt<KPL, EFIX, MOE_DT_BF16, MOE_DT_BF16>(a, mt, grid, st, kt);
-    else select_launch_mt<KPL, EFIX, MOE_DT_Q8B32, MOE_DT_BF16>(a, mt, grid, st, kt);
+    if (a.f.wdt == MOE_DT_F32) select_launch_mt<KPL, EFIX, MOE_DT_F32, MOE_DT_F32, GROUPED>(a, mt, grid, st, kt);
+    else if (a.f.wdt == MOE_DT_BF16) select_launch_mt<KPL, EFIX, MOE_DT_BF16, MOE_DT_BF16, GROUPED>(a, mt, grid, st, kt);
+    else select_launch_mt<KPL, EFIX, MOE_DT_Q8B32, MOE_DT_BF16, GROUPED>(a, mt, grid, st, kt);
 }
 
 hipError_t launch_decode(const DecodeRouteArgs& a, const KTime* kt, hipStream_t st) {
@@ -596,7 +606,9 @@ hipError_t launch_decode(const DecodeRouteArgs& a, const KTime* kt, hipStream_t 
     if (e == hipSuccess) {
         dim3 grid(1 + (a.f.n_shared ? (a.f.d + DS_WAVES * DS_ROWS - 1) / (DS_WAVES * DS_ROWS) : 0));
         const int kpl = (E + WAVE - 1) / WAVE;
-        if (E == 256) select_launch_fmt<4, 256>(a, mt, grid, st, kt[1]);
+        if (a.grouped && kpl <= 4) select_launch_fmt<4, 0, true>(a, mt, grid, st, kt[1]);
+        else if (a.grouped) select_launch_fmt<16, 0, true>(a, mt, grid, st, kt[1]);
+        else if (E == 256) select_launch_fmt<4, 256>(a, mt, grid, st, kt[1]);
         else if (kpl <= 1) select_launch_fmt<1, 0>(a, mt, grid, st, kt[1]);
         else if (kpl <= 2) select_launch_fmt<2, 0>(a, mt, grid, st, kt[1]);
         else if (kpl <= 3) select_launch_fmt<3, 0>(a, mt, grid, st, kt[1]);

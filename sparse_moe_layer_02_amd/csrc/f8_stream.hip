@@ -1,0 +1,357 @@
+// f8_stream.hip - e4m3 products for few activation rows per weight matrix.
+//
+//   gate/up:  h[r, c] = silu(x_r Wg_c) (x_r Wu_c), quantised per 128 columns
+//   down:     slot_out[f, :] = w_f (h_r Wd^T)
+//   dense:    out[m, n] = x_m W_n
+//
+// Bound by the weight bytes, each read once.  The weights go from memory
+// straight into the registers of the wavefront that uses them, in the order
+// the matrix instruction takes them, so neither LDS nor a barrier stands
+// between HBM and the multiply.  A wavefront owns 16 weight rows (16 gate and
+// 16 up rows); the 128 columns that share a scale are one step, whose codes
+// are widened to bf16 (exact) and multiplied on the matrix cores with fp32
+// sums (f8_dev.h: why not the 8-bit instruction; its rate is not needed
+// here).  A step's sum is multiplied by the activation row's power-of-two scale
+// (exact) and added with the weight block's fp32 scale.  Lane l reads columns 16 (l / 16) .. +15 of both
+// 64-column halves, so a load touches 64 consecutive bytes of 16 rows; the
+// activation rows are read the same way (their order in K is free as long as
+// both operands agree).
+#include "common.h"
+#include "dma_dev.h"
+#include "f8_dev.h"
+#include "gemm_dev.h"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int SW = 8;  // wavefronts per workgroup
+
+template <bool NT>
+__device__ __forceinline__ f8_u4 f8_ld(const uint8_t* p) {
+    if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const f8_u4*>(p));
+    else return *reinterpret_cast<const f8_u4*>(p);
+}
+
+// Fragments of U steps of 128 columns: NR weight row tiles, NT activation row tiles.
+template <int NR, int NT, int U>
+struct F8Frag {
+    f8_u4 w[U][NR][2], x[U][NT][2];
+    uint32_t e[U][NT];
+};
+
+// acc[r][t] += the products over the 128-column steps [kb0, kb1).  wp, xp:
+// this lane's rows; ep: their scale bytes; sp: the weight rows' block scales
+// (wave-uniform).  kb1 may be the step that K ends in: its columns past K
+// count as zeros and are not read.
+template <int NR, int NT, int U>
+__device__ __forceinline__ void f8_stream(const uint8_t* const (&wp)[NR], const float* const (&sp)[NR],
+                                          const uint8_t* const (&xp)[NT], const uint8_t* const (&ep)[NT], int kb0,
+                                          int kb1, int K, f8_f4 (&acc)[NR][NT]) {
+    using Frag = F8Frag<NR, NT, U>;
+    const int lo = 16 * (lane_id() / 16), kfull = K / F8_BLK, kbe = min(kb1, kfull);
+    auto load = [&](Frag& f, int kb) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = min(kb + u, kbe - 1);  // (steps past the end repeat the last; not used)
+            const size_t o = (size_t)k * F8_BLK + lo;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                f.w[u][r][0] = f8_ld<true>(wp[r] + o);
+                f.w[u][r][1] = f8_ld<true>(wp[r] + o + 64);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                f.x[u][t][0] = f8_ld<false>(xp[t] + o);
+                f.x[u][t][1] = f8_ld<false>(xp[t] + o + 64);
+                f.e[u][t] = ep[t][k];
+            }
+        }
+        pin();
+    };
+    auto step = [&](const f8_u4 (&w)[NR][2], const f8_u4 (&x)[NT][2], const uint32_t (&e)[NT], int k) {
+        F8Wide ww[NR];
+        float s[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            ww[r] = f8_widen(w[r][0], w[r][1]);
+            s[r] = f8_uniform(sp[r], k);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const F8Wide xw = f8_widen(x[t][0], x[t][1]);
+            const float sx = f8_scale_value(e[t]);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const f8_f4 p = f8_dot16(ww[r], xw, f8_f4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[r][t][v] = fmaf(s[r], p[v] * sx, acc[r][t][v]);
+            }
+        }
+    };
+    auto compute = [&](const Frag& f, int kb) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (kb + u < kbe) step(f.w[u], f.x[u], f.e[u], kb + u);
+    };
+    if (kb0 < kbe) {
+        Frag a, b;
+        load(a, kb0);
+        for (int kb = kb0; kb < kbe; kb += 2 * U) {
+            if (kb + U < kbe) load(b, kb + U);
+            compute(a, kb);
+            if (kb + U < kbe) {
+                if (kb + 2 * U < kbe) load(a, kb + 2 * U);
+                compute(b, kb + U);
+            }
+        }
+    }
+    if (kb0 <= kfull && kfull < kb1) {  // the step that K ends in
+        const int k0 = kfull * F8_BLK + lo;
+        const f8_u4 zero = f8_u4{0, 0, 0, 0};
+        f8_u4 w[NR][2], x[NT][2];
+        uint32_t e[NT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool in = k0 + 64 * h < K;  // K is a multiple of 16
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                w[r][h] = zero;
+                if (in) w[r][h] = f8_ld<true>(wp[r] + k0 + 64 * h);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                x[t][h] = zero;
+                if (in) x[t][h] = f8_ld<false>(xp[t] + k0 + 64 * h);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) e[t] = ep[t][kfull];
+        step(w, x, e, kfull);
+    }
+}
+
+// Activation row of tile row r (rows past the tile repeat its first; their
+// results are not stored): the token in gate/up.
+__device__ __forceinline__ int f8_token(const FfnArgs& a, const TileRows& tr, int r) {
+    r = r < tr.nrows ? r : 0;
+    if (tr.g == a.E) return tr.rbeg - a.T * a.k + r;
+    const int f = a.perm_rows[tr.rbeg + r];
+    return f >= 0 && f < a.T * a.k ? f / a.k : 0;
+}
+
+// ---------------------------------------------------------------------------
+// gate/up: a workgroup takes the 128 h columns of one scale block for a tile
+// of 16 NT rows, 16 columns per wavefront.
+// ---------------------------------------------------------------------------
+template <int NT>
+__global__ __launch_bounds__(64 * SW) void f8_gateup_stream_kernel(F8Ffn a) {
+    __shared__ uint32_t red[SW][16 * NT];
+    int tile, ntile;
+    if (!work_item<16>(tile_count(a.f), tile, ntile)) return;
+    TileRows tr;
+    if (!tile_rows<16 * NT>(a.f, tile, tr)) return;
+    const bool shared = tr.g == a.f.E;
+    const int F = shared ? a.f.Fs : a.f.F, d = a.f.d, n0 = ntile * F8_BLK;
+    if (n0 >= F) return;
+    const int lane = lane_id(), wave = wave_index(), KB = f8_blocks(d);
+    const MatRef& G = shared ? a.f.s_gate : a.f.gate;
+    const MatRef& U = shared ? a.f.s_up : a.f.up;
+    const int e = shared ? 0 : tr.g, c0 = n0 + 16 * wave;
+    const size_t wrow = ((size_t)e * F + min(c0 + lane % 16, F - 1)) * d;
+    const size_t srow = ((size_t)e * f8_blocks(F) + ntile) * KB;
+    const uint8_t* wp[2] = {static_cast<const uint8_t*>(G.q) + wrow, static_cast<const uint8_t*>(U.q) + wrow};
+    const float* sp[2] = {reinterpret_cast<const float*>(G.scale) + srow, reinterpret_cast<const float*>(U.scale) + srow};
+    const uint8_t *xp[NT], *ep[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int tok = f8_token(a.f, tr, 16 * t + lane % 16);
+        xp[t] = a.xq + (size_t)tok * d;
+        ep[t] = a.xe + (size_t)tok * f8_scale_ld(d);
+    }
+    f8_f4 acc[2][NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = f8_f4{0.f, 0.f, 0.f, 0.f};
+    f8_stream<2, NT, NT <= 2 ? 2 : 1>(wp, sp, xp, ep, 0, KB, d, acc);
+    // h, then its scale over the workgroup's 128 columns
+    const bool in = c0 < F;  // (F is a multiple of 64: a wavefront's columns are all in or all out)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            acc[0][t][v] = silu_f32(acc[0][t][v]) * acc[1][t][v];
+            m = max(m, f8_abs_bits(acc[0][t][v]));
+        }
+        m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+        if (lane < 16) red[wave][16 * t + lane] = in ? m : 0u;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = 16 * t + lane % 16;
+        uint32_t m = 0;
+#pragma unroll
+        for (int w = 0; w < SW; ++w) m = max(m, red[w][r]);
+        const uint32_t byte = f8_scale_byte(m);
+        const f8_f4 h = acc[0][t];
+        if (r >= tr.nrows) continue;
+        const size_t hrow = (size_t)(tr.rbeg + r);
+        if (in)
+            *reinterpret_cast<uint32_t*>(a.hq + hrow * a.f.ldh + c0 + 4 * (lane / 16)) =
+                f8_pack4(h[0], h[1], h[2], h[3], f8_inv_scale(byte), byte);
+        if (wave == 0 && lane < 16) a.he[hrow * f8_scale_ld(a.f.ldh) + ntile] = (uint8_t)byte;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// down: 128 output columns per workgroup, 16 per wavefront.
+// ---------------------------------------------------------------------------
+template <int NT>
+__global__ __launch_bounds__(64 * SW) void f8_down_stream_kernel(F8Ffn a) {
+    int tile, ntile;
+    if (!work_item<16>(tile_count(a.f), tile, ntile)) return;
+    TileRows tr;
+    if (!tile_rows<16 * NT>(a.f, tile, tr)) return;
+    const bool shared = tr.g == a.f.E;
+    const int F = shared ? a.f.Fs : a.f.F, d = a.f.d;
+    const int lane = lane_id(), wave = wave_index(), KB = f8_blocks(F), c0 = ntile * F8_BLK + 16 * wave;
+    if (c0 >= d) return;  // (d is a multiple of 64)
+    const MatRef& D = shared ? a.f.s_down : a.f.down;
+    const int e = shared ? 0 : tr.g;
+    const uint8_t* wp[1] = {static_cast<const uint8_t*>(D.q) + ((size_t)e * d + c0 + lane % 16) * F};
+    const float* sp[1] = {reinterpret_cast<const float*>(D.scale) + ((size_t)e * f8_blocks(d) + ntile) * KB};
+    const uint8_t *xp[NT], *ep[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = 16 * t + lane % 16;
+        const size_t hrow = (size_t)(tr.rbeg + (r < tr.nrows ? r : 0));
+        xp[t] = a.hq + hrow * a.f.ldh;
+        ep[t] = a.he + hrow * f8_scale_ld(a.f.ldh);
+    }
+    f8_f4 acc[1][NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[0][t] = f8_f4{0.f, 0.f, 0.f, 0.f};
+    f8_stream<1, NT, NT <= 2 ? 4 : 2>(wp, sp, xp, ep, 0, KB, F, acc);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = 16 * t + lane % 16;
+        if (r >= tr.nrows) continue;
+        int dst = tr.rbeg - a.f.T * a.f.k + r;
+        float w = 1.0f;
+        if (!shared) {
+            dst = a.f.perm_rows[tr.rbeg + r];
+            if (dst < 0 || dst >= a.f.T * a.f.k) continue;
+            w = a.f.topk_w[dst];
+        }
+        float* out = (shared ? a.f.shared_out : a.f.slot_out) + (size_t)dst * d + c0 + 4 * (lane / 16);
+        st_stream16(out, make_float4(w * acc[0][t][0], w * acc[0][t][1], w * acc[0][t][2], w * acc[0][t][3]));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dense: 16 RB output columns per workgroup, K split over KS = SW / RB
+// wavefronts whose partial sums are added in LDS in a fixed order.
+// ---------------------------------------------------------------------------
+template <int OF>
+__device__ __forceinline__ void f8_store4(void* out, size_t at, int left, const float (&v)[4], bool wide) {
+    if constexpr (OF == MOE_DT_BF16) {
+        uint16_t* p = static_cast<uint16_t*>(out) + at;
+        if (wide) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
+                                                      f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16);
+        } else {
+            for (int j = 0; j < 4; ++j)
+                if (j < left) p[j] = f32_to_bf16(v[j]);
+        }
+    } else {
+        float* p = static_cast<float*>(out) + at;
+        if (wide) {
+            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+            for (int j = 0; j < 4; ++j)
+                if (j < left) p[j] = v[j];
+        }
+    }
+}
+
+template <int NT, int RB, int OF>
+__global__ __launch_bounds__(64 * SW) void f8_dense_stream_kernel(BlockArgs a) {
+    constexpr int KS = SW / RB;
+    __shared__ f8_f4 part[KS > 1 ? KS - 1 : 1][RB][NT][WAVE];
+    const int lane = lane_id(), wave = wave_index(), rb = wave % RB, ks = wave / RB;
+    const int c0 = (blockIdx.x * RB + rb) * 16, m0 = blockIdx.y * 16 * NT, KB = f8_blocks(a.k);
+    const bool live = c0 < a.n;
+    f8_f4 acc[1][NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[0][t] = f8_f4{0.f, 0.f, 0.f, 0.f};
+    if (live) {
+        const uint8_t* wp[1] = {a.wq + (size_t)min(c0 + lane % 16, a.n - 1) * a.k};
+        const float* sp[1] = {a.ws + (size_t)(c0 / F8_BLK) * KB};
+        const uint8_t *xp[NT], *ep[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const size_t r = (size_t)min(m0 + 16 * t + lane % 16, a.m - 1);
+            xp[t] = a.xq + r * a.k;
+            ep[t] = a.xe + r * f8_scale_ld(a.k);
+        }
+        const int per = (KB + KS - 1) / KS;
+        f8_stream<1, NT, NT <= 2 ? 4 : 2>(wp, sp, xp, ep, ks * per, min(KB, (ks + 1) * per), a.k, acc);
+    }
+    if constexpr (KS > 1) {
+        if (ks > 0)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) part[ks - 1][rb][t][lane] = acc[0][t];
+        __syncthreads();
+        if (ks > 0) return;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int s = 0; s < KS - 1; ++s) acc[0][t] += part[s][rb][t][lane];
+    }
+    const int c = c0 + 4 * (lane / 16);
+    if (c >= a.n) return;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = m0 + 16 * t + lane % 16;
+        if (r >= a.m) continue;
+        const float v[4] = {acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3]};
+        f8_store4<OF>(a.out, (size_t)r * a.n + c, a.n - c, v, a.n % 4 == 0);
+    }
+}
+
+template <int NT, int RB>
+hipError_t dense_launch(const BlockArgs& a, hipStream_t st) {
+    const dim3 grid((a.n + 16 * RB - 1) / (16 * RB), (a.m + 16 * NT - 1) / (16 * NT));
+    if (a.odt == MOE_DT_BF16) f8_dense_stream_kernel<NT, RB, MOE_DT_BF16><<<grid, 64 * SW, 0, st>>>(a);
+    else f8_dense_stream_kernel<NT, RB, MOE_DT_F32><<<grid, 64 * SW, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_f8_gateup(const F8Ffn& a, hipStream_t st, const KTime& kt) {
+    const int fmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F;
+    const dim3 grid(a.f.max_tiles, f8_blocks(fmax));
+    if (a.f.bm == 16) launch_kernel(f8_gateup_stream_kernel<1>, grid, 64 * SW, st, kt, a);
+    else if (a.f.bm == 32) launch_kernel(f8_gateup_stream_kernel<2>, grid, 64 * SW, st, kt, a);
+    else launch_kernel(f8_gateup_stream_kernel<4>, grid, 64 * SW, st, kt, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_f8_down(const F8Ffn& a, hipStream_t st, const KTime& kt) {
+    const dim3 grid(a.f.max_tiles, f8_blocks(a.f.d));
+    if (a.f.bm == 16) launch_kernel(f8_down_stream_kernel<1>, grid, 64 * SW, st, kt, a);
+    else if (a.f.bm == 32) launch_kernel(f8_down_stream_kernel<2>, grid, 64 * SW, st, kt, a);
+    else launch_kernel(f8_down_stream_kernel<4>, grid, 64 * SW, st, kt, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_block_matmul(const BlockArgs& a, hipStream_t st) {
+    if (a.m <= 16) return dense_launch<1, 1>(a, st);
+    if (a.m <= 32) return dense_launch<2, 2>(a, st);
+    return dense_launch<4, 4>(a, st);
+}
+
+}  // namespace moe

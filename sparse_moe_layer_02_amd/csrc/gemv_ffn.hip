@@ -90,6 +90,8 @@ __global__ __launch_bounds__(256) void down_slots_kernel(FfnArgs a) {
 // what they hold (c5: 188 -> 161 us).  The additions keep their order.
 // ---------------------------------------------------------------------------
 typedef float cf4 __attribute__((ext_vector_type(4)));
+typedef uint32_t cu2 __attribute__((ext_vector_type(2)));
+template <int YF>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     const size_t n4 = (size_t)a.T * a.d / 4;
     for (size_t q = (size_t)blockIdx.x * blockDim.x + threadIdx.x; q < n4; q += (size_t)gridDim.x * blockDim.x) {
@@ -98,7 +100,13 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
                                : cf4{0.f, 0.f, 0.f, 0.f};
         for (int j = 0; j < a.k; ++j)
             acc += __builtin_nontemporal_load(reinterpret_cast<const cf4*>(a.slot_out + (t * a.k + j) * a.d + c));
-        __builtin_nontemporal_store(acc, reinterpret_cast<cf4*>(a.y + t * a.d + c));
+        if constexpr (YF == MOE_DT_F32) {
+            __builtin_nontemporal_store(acc, reinterpret_cast<cf4*>(static_cast<float*>(a.y) + t * a.d + c));
+        } else {  // the caller's bf16 rows: one rounding of the fp32 sum
+            const cu2 b = cu2{f32_to_bf16(acc.x) | (uint32_t)f32_to_bf16(acc.y) << 16,
+                              f32_to_bf16(acc.z) | (uint32_t)f32_to_bf16(acc.w) << 16};
+            __builtin_nontemporal_store(b, reinterpret_cast<cu2*>(static_cast<uint16_t*>(a.y) + t * a.d + c));
+        }
     }
 }
 // ---------------------------------------------------------------------------
@@ -161,7 +169,8 @@ hipError_t launch_combine(const CombineArgs& a, hipStream_t st, const KTime& kt)
     const size_t n4 = (size_t)a.T * a.d / 4;
     const size_t want = (n4 + 255) / 256;
     const int blocks = (int)(want < 4096 ? want : 4096);
-    launch_kernel(combine_kernel, blocks, 256, st, kt, a);
+    if (a.ydt == MOE_DT_BF16) launch_kernel(combine_kernel<MOE_DT_BF16>, blocks, 256, st, kt, a);
+    else launch_kernel(combine_kernel<MOE_DT_F32>, blocks, 256, st, kt, a);
     return hipGetLastError();
 }
 

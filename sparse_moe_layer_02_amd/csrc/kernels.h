@@ -47,6 +47,35 @@ struct SelectArgs {
 };
 hipError_t launch_topk(const SelectArgs& a, hipStream_t st, const KTime& kt = KTime());
 
+// Expert groups of a selection; n_group 1 is the flat one.
+struct GroupArgs {
+    int n_group = 1, topk_group = 1, group_top = 1, normalise = 1;
+    float inv_size = 0.0f;  // n_group / n_expert
+};
+hipError_t launch_group_topk(const SelectArgs& a, const GroupArgs& g, hipStream_t st, const KTime& kt = KTime());
+
+// Rows [rows, cols] (row stride ldx elements) to codes [rows, cols] and scale
+// bytes [rows, f8_scale_ld(cols)].
+struct QuantArgs {
+    const void* x;
+    int xdt;  // MOE_DT_F32 or MOE_DT_BF16
+    int rows, cols;
+    int64_t ldx;
+    uint8_t *q, *e;
+};
+hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t st, const KTime& kt = KTime());
+
+// Dense product out[m, n] = x[m, k] w[n, k]^T of e4m3 operands.
+struct BlockArgs {
+    const uint8_t *xq, *xe;  // [m, k] codes, [m, f8_scale_ld(k)] scale bytes
+    const uint8_t* wq;       // [n, k]
+    const float* ws;         // [ceil(n / 128), ceil(k / 128)]
+    int m, n, k;
+    void* out;               // [m, n]
+    int odt;                 // MOE_DT_F32 or MOE_DT_BF16
+};
+hipError_t launch_block_matmul(const BlockArgs& a, hipStream_t st);
+
 struct PermArgs {
     const int32_t* topk_idx;
     int T, k, E;
@@ -127,6 +156,15 @@ hipError_t launch_gateup_q8_dma(const FfnArgs& a, hipStream_t st, const KTime& k
 hipError_t launch_down_q8_dma(const FfnArgs& a, hipStream_t st, const KTime& kt = KTime());
 hipError_t launch_down_dma(const FfnArgs& a, hipStream_t st, const KTime& kt = KTime());
 
+// Experts with e4m3 weights: rows of x and h as codes and scale bytes.
+struct F8Ffn {
+    FfnArgs f;               // h unused; ldh is the row stride of hq
+    uint8_t *xq, *xe;        // [T, d], [T, f8_scale_ld(d)]
+    uint8_t *hq, *he;        // [T*k + T*n_shared, ldh], [.., f8_scale_ld(ldh)]
+};
+hipError_t launch_f8_gateup(const F8Ffn& a, hipStream_t st, const KTime& kt = KTime());
+hipError_t launch_f8_down(const F8Ffn& a, hipStream_t st, const KTime& kt = KTime());
+
 // The decode path (T <= MOE_DECODE_MAX_TOKENS) in four launches: router;
 // selection + grouping beside the shared gate/up; routed gate/up; down +
 // combine into f.y.  kt[s] times stage s (MOE_STAGES entries); the decode
@@ -137,14 +175,17 @@ struct DecodeRouteArgs {
     PermArgs p;
     FfnArgs f;
     float* scores;  // [T, E] fp32 router scores (workspace)
+    GroupArgs g;
+    bool grouped;   // selection with groups or softmax scores, from the logits
 };
 hipError_t launch_decode(const DecodeRouteArgs& a, const KTime* kt, hipStream_t st);
 
 struct CombineArgs {
     const float* slot_out;
     const float* shared_out;
-    float* y;
+    void* y;        // [T, d] of ydt
     int T, k, d;
+    int ydt = MOE_DT_F32;  // or MOE_DT_BF16
 };
 hipError_t launch_combine(const CombineArgs& a, hipStream_t st, const KTime& kt = KTime());
 

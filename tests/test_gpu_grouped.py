@@ -1,0 +1,181 @@
+"""Grouped routing on the GPU against the float64 definition (f8_ref.select):
+indices exact, weights within one unit in the last place of fp32 (both sides
+round one fp64 quotient once; the fp64 sums may differ in their last bits)."""
+import sys
+
+import numpy as np
+import pytest
+
+import f8_ref as R
+import gpu_harness as H
+from synth import configs
+
+pytestmark = pytest.mark.gpu
+
+
+def say(*a):
+    print(*a, flush=True)
+    sys.stdout.flush()
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    import sparse_moe_layer_02_amd as moe
+    moe.load()
+    return torch, moe
+
+
+def logits_of(T, E, rng):
+    """Random rows, then rows at the selection order's corners."""
+    l = rng.standard_normal((T, E)).astype(np.float32) * 2
+    special = [np.full(E, 0.5), np.full(E, -np.inf), np.where(rng.random(E) < 0.5, -np.inf, 1.0),
+               np.where(rng.random(E) < 0.3, np.nan, rng.standard_normal(E)), np.full(E, np.nan),
+               rng.choice([0.0, -0.0, 1.0], E), np.where(np.arange(E) == E // 2, np.inf, 0.0),
+               rng.integers(-2, 3, E).astype(float), np.full(E, -1e4), np.full(E, 1e4),
+               np.where(rng.random(E) < 0.9, np.finfo(np.float32).min, 0.0)]
+    for i, row in enumerate(special):
+        if i + 1 < T:
+            l[i + 1] = row
+    return l
+
+
+def check(got_idx, got_w, want_idx, want_w, label):
+    bad = np.argwhere(got_idx != want_idx)
+    assert len(bad) == 0, "%s: indices differ at %s: %s, want %s" % (
+        label, bad[:4].tolist(), got_idx[bad[0][0]], want_idx[bad[0][0]])
+    assert np.array_equal(np.isnan(got_w), np.isnan(want_w)), label
+    ok = ~np.isnan(want_w)
+    ref = want_w[ok].astype(np.float32)
+    assert H.ulp_diff_f32(got_w[ok], ref).max(initial=0) <= 1, label
+
+
+GROUPS = [(1, 1, 1, True), (1, 1, 1, False), (4, 2, 1, True), (4, 1, 2, True), (4, 4, 2, False), (2, 1, 2, False)]
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid", "sqrt_softplus"])
+@pytest.mark.parametrize("E,T", [(4, 3), (60, 17), (64, 1), (100, 40), (128, 21), (192, 5), (256, 70), (520, 13),
+                                 (1024, 14)])
+def test_select(dev, E, T, kind):
+    torch, moe = dev
+    rng = np.random.default_rng(E * 100 + T)
+    l = logits_of(T, E, rng)
+    bias = (rng.random(E) * 0.2 - 0.1).astype(np.float32)
+    for n, (G, tg, top, norm) in enumerate(GROUPS):
+        k = min(8, tg * (E // G), 32)
+        if E == 1024 and G == 1:
+            k = 32
+        b = bias if n % 2 else None
+        label = "select E=%d T=%d %s G=%d/%d top=%d norm=%d k=%d" % (E, T, kind, tg, G, top, norm, k)
+        say(label)
+        c = moe.make_config(T, 64, E, k, 64, n_shared=0, score=kind, route_scale=1.5)
+        idx = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+        w = torch.full((T, k), -7.0, device="cuda")
+        moe.moe_select_grouped(c, moe.make_groups(G, tg, top, norm), torch.from_numpy(l).cuda(),
+                               None if b is None else torch.from_numpy(b).cuda(), idx, w)
+        torch.cuda.synchronize()
+        check(idx.cpu().numpy(), w.cpu().numpy(), *R.select(l, b, k, kind, 1.5, G, tg, top, norm), label)
+
+
+@pytest.mark.parametrize("G,E", [(64, 64), (64, 256), (32, 1024), (8, 8), (12, 60)])
+def test_many_groups(dev, G, E):
+    """One expert per group, the most groups, sizes that are no power of two."""
+    torch, moe = dev
+    rng = np.random.default_rng(G + E)
+    T, tg = 25, max(1, G // 3)
+    k = min(8, tg * (E // G))
+    l = logits_of(T, E, rng)
+    c = moe.make_config(T, 64, E, k, 64, n_shared=0, score="sigmoid")
+    idx, w = torch.empty((T, k), dtype=torch.int32, device="cuda"), torch.empty((T, k), device="cuda")
+    for top in (1, 2):
+        moe.moe_select_grouped(c, moe.make_groups(G, tg, top), torch.from_numpy(l).cuda(), None, idx, w)
+        torch.cuda.synchronize()
+        check(idx.cpu().numpy(), w.cpu().numpy(), *R.select(l, None, k, "sigmoid", 1.0, G, tg, top, True), "G=%d" % G)
+
+
+def test_flat_groups_equal_select(dev):
+    """groups = None and {1, 1, 1, 1} are moe_select, bit for bit."""
+    torch, moe = dev
+    l = torch.randn((300, 256), device="cuda")
+    out = []
+    c = moe.make_config(300, 64, 256, 8, 64, n_shared=0, score="sigmoid")
+    for call in (lambda i, w: moe.moe_select(c, l, None, i, w),
+                 lambda i, w: moe.moe_select_grouped(c, None, l, None, i, w),
+                 lambda i, w: moe.moe_select_grouped(c, moe.make_groups(8, 8, 2), l, None, i, w)):
+        i, w = torch.empty((300, 8), dtype=torch.int32, device="cuda"), torch.empty((300, 8), device="cuda")
+        call(i, w)
+        out.append((i, w))
+    for i, w in out[1:]:
+        assert torch.equal(i, out[0][0]) and torch.equal(w, out[0][1])
+
+
+@pytest.mark.parametrize("T,d,act", [(1, 256, "bf16"), (9, 320, "f32"), (70, 192, "bf16"), (513, 128, "bf16")])
+def test_route(dev, T, d, act):
+    torch, moe = dev
+    rng = np.random.default_rng(T)
+    E, k = 64, 6
+    x = torch.from_numpy(rng.standard_normal((T, d)).astype(np.float32)).cuda()
+    x = x.bfloat16() if act == "bf16" else x
+    wr = torch.from_numpy((rng.standard_normal((E, d)) / np.sqrt(d)).astype(np.float32)).cuda()
+    c = moe.make_config(T, d, E, k, 64, n_shared=0, score="softmax", route_scale=2.5, act=act, w=act)
+    g = moe.make_groups(8, 3, 2)
+    lg, idx, w = (torch.empty((T, E), device="cuda"), torch.empty((T, k), dtype=torch.int32, device="cuda"),
+                  torch.empty((T, k), device="cuda"))
+    moe.moe_route_grouped(c, g, x, wr, None, lg, idx, w, None)
+    idx2, w2 = torch.empty_like(idx), torch.empty_like(w)
+    moe.moe_route_grouped(c, g, x, wr, None, None, idx2, w2, moe.workspace(c))  # logits in the workspace
+    torch.cuda.synchronize()
+    want = (x.double() @ wr.double().t()).float().cpu().numpy()
+    assert H.ulp_diff_f32(lg.cpu().numpy(), want).max() <= 1
+    check(idx.cpu().numpy(), w.cpu().numpy(), *R.select(lg.cpu().numpy(), None, k, "softmax", 2.5, 8, 3, 2, True), "route")
+    assert torch.equal(idx, idx2) and torch.equal(w, w2)
+
+
+@pytest.mark.parametrize("wt,act", [("bf16", "bf16"), ("q8b32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("T", [1, 3, 8, 40])
+def test_layer_of_existing_weights(dev, orc, T, wt, act):
+    """Grouped routing in the whole layer: the routing against the definition, y
+    against moe_expert_ffn and moe_combine over that routing (same kernels on
+    the prefill path: equal bits; the decode path adds in another order, so
+    within the layers' own tolerances)."""
+    torch, moe = dev
+    cfg = configs.custom(T=T, d=256, E=40, k=4, F=128, Fs=128, n_shared=1, act=act, w=wt, x_sigma=1.0, w_sigma=0.05,
+                         wr_sigma=1 / 16.0, score="sigmoid", bias="uniform")
+    L = configs.make_layer(cfg)
+    W = H.upload_layer(L)
+    Wm = moe.make_weights(W)
+    x = H.to_dev(L["x"])
+    for kind, groups in (("softmax", None), ("sigmoid", moe.make_groups(8, 2, 2)),
+                         ("softmax", moe.make_groups(4, 2, 1, False))):
+        c = moe.make_config(T, 256, 40, 4, 128, score=kind, route_scale=1.5, act=act, w=wt)
+        E, k, n = 40, 4, T * 4
+        out = dict(logits=torch.empty((T, E), device="cuda"), topk_idx=torch.empty((T, k), dtype=torch.int32, device="cuda"),
+                   topk_w=torch.empty((T, k), device="cuda"), offsets=torch.empty(E + 1, dtype=torch.int32, device="cuda"),
+                   perm_rows=torch.empty(n, dtype=torch.int32, device="cuda"),
+                   inv_perm=torch.empty(n, dtype=torch.int32, device="cuda"))
+        y = torch.full((T, 256), float("nan"), device="cuda")
+        ws = moe.workspace(c)
+        ws.fill_(0xA5)
+        moe.moe_layer_forward_grouped(c, groups, x, Wm, y, ws, debug=out)
+        if groups is None:
+            y2 = torch.empty_like(y)
+            moe.moe_layer_forward(c, x, Wm, y2, ws)
+            torch.cuda.synchronize()
+            assert torch.equal(y, y2)
+        torch.cuda.synchronize()
+        g = (1, 1, 1, 1) if groups is None else (groups.n_group, groups.topk_group, groups.group_top, groups.normalise)
+        check(out["topk_idx"].cpu().numpy(), out["topk_w"].cpu().numpy(),
+              *R.select(out["logits"].cpu().numpy(), L["bias"], k, kind, 1.5, *g), "layer T=%d %s" % (T, kind))
+        off, perm, inv = (torch.empty_like(out[key]) for key in ("offsets", "perm_rows", "inv_perm"))
+        moe.moe_permute(c, out["topk_idx"], off, perm, inv, ws)
+        slot, sh, want = torch.empty((n, 256), device="cuda"), torch.empty((T, 256), device="cuda"), torch.empty_like(y)
+        moe.moe_expert_ffn(c, x, Wm, off, perm, out["topk_w"], slot, sh, ws)
+        moe.moe_combine(c, slot, sh, want)
+        torch.cuda.synchronize()
+        for key, v in (("offsets", off), ("perm_rows", perm), ("inv_perm", inv)):
+            assert torch.equal(out[key], v), key
+        if T > 8:
+            assert torch.equal(y, want)
+        else:
+            H.check_y(y.cpu().numpy(), want.double().cpu().numpy(), cfg, "layer")
