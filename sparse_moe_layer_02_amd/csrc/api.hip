@@ -74,7 +74,10 @@ constexpr int F8_BM_MIN = 16;
 int gemm_bm(const moe_config* c) {
     if (c->w_dtype == MOE_DT_Q8B32) return 64;
     const long n = (long)c->n_tokens * c->top_k;
-    if (c->w_dtype == MOE_DT_F8B128) return n <= 4L * c->n_expert ? 16 : n <= 20L * c->n_expert ? 32 : 64;
+    if (c->w_dtype == MOE_DT_F8B128) {
+        const long e = c->n_expert;
+        return n <= 4 * e ? 16 : n <= 20 * e ? 32 : n <= 48 * e ? 64 : n <= 96 * e ? 128 : 256;
+    }
     return n >= 96L * c->n_expert ? 256 : 64;
 }
 

@@ -132,4 +132,28 @@ __device__ __forceinline__ f8_f16 f8_mfma32(i32x8_t w, i32x8_t x, f8_f16 c, uint
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, 0, 0, 0, F8_ONE, SEL, (int)e);
 }
 
+// Four adjacent results of a row (left: columns up to the row's end; wide: the
+// row's start and the column are multiples of 4).
+template <int OF>
+__device__ __forceinline__ void f8_store4(void* out, size_t at, int left, const float (&v)[4], bool wide) {
+    if constexpr (OF == MOE_DT_BF16) {
+        uint16_t* p = static_cast<uint16_t*>(out) + at;
+        if (wide) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
+                                                      f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16);
+        } else {
+            for (int j = 0; j < 4; ++j)
+                if (j < left) p[j] = f32_to_bf16(v[j]);
+        }
+    } else {
+        float* p = static_cast<float*>(out) + at;
+        if (wide) {
+            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+            for (int j = 0; j < 4; ++j)
+                if (j < left) p[j] = v[j];
+        }
+    }
+}
+
 }  // namespace moe

@@ -254,28 +254,6 @@ __global__ __launch_bounds__(64 * SW) void f8_down_stream_kernel(F8Ffn a) {
 // dense: 16 RB output columns per workgroup, K split over KS = SW / RB
 // wavefronts whose partial sums are added in LDS in a fixed order.
 // ---------------------------------------------------------------------------
-template <int OF>
-__device__ __forceinline__ void f8_store4(void* out, size_t at, int left, const float (&v)[4], bool wide) {
-    if constexpr (OF == MOE_DT_BF16) {
-        uint16_t* p = static_cast<uint16_t*>(out) + at;
-        if (wide) {
-            *reinterpret_cast<uint2*>(p) = make_uint2(f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
-                                                      f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16);
-        } else {
-            for (int j = 0; j < 4; ++j)
-                if (j < left) p[j] = f32_to_bf16(v[j]);
-        }
-    } else {
-        float* p = static_cast<float*>(out) + at;
-        if (wide) {
-            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-            for (int j = 0; j < 4; ++j)
-                if (j < left) p[j] = v[j];
-        }
-    }
-}
-
 template <int NT, int RB, int OF>
 __global__ __launch_bounds__(64 * SW) void f8_dense_stream_kernel(BlockArgs a) {
     constexpr int KS = SW / RB;
@@ -332,6 +310,7 @@ hipError_t dense_launch(const BlockArgs& a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_f8_gateup(const F8Ffn& a, hipStream_t st, const KTime& kt) {
+    if (a.f.bm >= 128) return launch_f8_gateup_tile(a, st, kt);
     const int fmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F;
     const dim3 grid(a.f.max_tiles, f8_blocks(fmax));
     if (a.f.bm == 16) launch_kernel(f8_gateup_stream_kernel<1>, grid, 64 * SW, st, kt, a);
@@ -341,6 +320,7 @@ hipError_t launch_f8_gateup(const F8Ffn& a, hipStream_t st, const KTime& kt) {
 }
 
 hipError_t launch_f8_down(const F8Ffn& a, hipStream_t st, const KTime& kt) {
+    if (a.f.bm >= 128) return launch_f8_down_tile(a, st, kt);
     const dim3 grid(a.f.max_tiles, f8_blocks(a.f.d));
     if (a.f.bm == 16) launch_kernel(f8_down_stream_kernel<1>, grid, 64 * SW, st, kt, a);
     else if (a.f.bm == 32) launch_kernel(f8_down_stream_kernel<2>, grid, 64 * SW, st, kt, a);
@@ -349,6 +329,7 @@ hipError_t launch_f8_down(const F8Ffn& a, hipStream_t st, const KTime& kt) {
 }
 
 hipError_t launch_block_matmul(const BlockArgs& a, hipStream_t st) {
+    if (a.m > 128) return launch_block_matmul_tile(a, st);
     if (a.m <= 16) return dense_launch<1, 1>(a, st);
     if (a.m <= 32) return dense_launch<2, 2>(a, st);
     return dense_launch<4, 4>(a, st);

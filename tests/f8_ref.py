@@ -9,6 +9,12 @@ is a power of two (exact); the weight scale is one fused multiply-add per block
 (half a unit each), and up to 8 partial sums are added at the end.  So
 |error| <= (128 + blocks + 8) 2^-23 * sum |terms|.  bf16 outputs add half a
 step, 2^-8 of the value.
+
+Results that are rounded to 16 or 8 bits next may come from the 8-bit matrix
+instruction.  It cuts (towards zero) each product of 8 consecutive columns
+below 2^-13 of the largest one's power of two before it adds them: the other
+seven lose less than 2^-13 of the largest each.  ``cut`` adds that,
+7 * 2^-13 * max |x| max |w| for each group of 8 columns.
 """
 import numpy as np
 
@@ -60,11 +66,15 @@ def dequant_weight(q, s):
     return q * np.repeat(np.repeat(s, B, axis=0), B, axis=1)[:q.shape[0], :q.shape[1]]
 
 
-def matmul(xd, wd):
-    """(product, bound on the library's fp32 sum) of dequantised float64 operands."""
+def matmul(xd, wd, cut=False):
+    """(product, bound on the library's sum) of dequantised float64 operands."""
     k = xd.shape[1]
     blocks = -(-k // B)
-    return xd @ wd.T, (128 + blocks + 8) * 2.0 ** -23 * (np.abs(xd) @ np.abs(wd).T)
+    err = (128 + blocks + 8) * 2.0 ** -23 * (np.abs(xd) @ np.abs(wd).T)
+    if cut:
+        top = [np.abs(pad(a)).reshape(len(a), -1, 8).max(2) for a in (xd, wd)]
+        err = err + 7 * 2.0 ** -13 * (top[0] @ top[1].T)
+    return xd @ wd.T, err
 
 
 def bf16_bound(y, err):
@@ -95,15 +105,15 @@ def silu(g):
     return g / (1.0 + np.exp(-g))
 
 
-def expert(xd, wg, wu, wd):
+def expert(xd, wg, wu, wd, cut=False):
     """(SwiGLU expert output, bound) of dequantised rows through dequantised weights."""
-    g, eg = matmul(xd, wg)
-    u, eu = matmul(xd, wu)
+    g, eg = matmul(xd, wg, cut)
+    u, eu = matmul(xd, wu, cut)
     h = silu(g) * u
     # |silu'| <= 1.1; silu itself in fp32: a few units (16 * 2^-23 covers exp, reciprocal and products)
     eh = 1.1 * eg * (np.abs(u) + eu) + (np.abs(silu(g)) + 1.1 * eg) * eu + 16 * 2.0 ** -23 * np.abs(h)
     hd, far = quantize_interval(h, eh)
-    y, ey = matmul(hd, wd)
+    y, ey = matmul(hd, wd, cut)
     return y, ey + far @ np.abs(wd).T * (1 + 2.0 ** -10)
 
 

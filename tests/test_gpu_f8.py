@@ -135,8 +135,8 @@ def test_matmul(dev, m, n, k, xdt):
         x = x.bfloat16() if xdt == "bf16" else x
         xd = R.dequant_rows(*R.quantize(x.double().numpy()))
         x, xs = x.cuda(), None
-    ref, err = R.matmul(xd, wd)
     for odt in (torch.float32, torch.bfloat16):
+        ref, err = R.matmul(xd, wd, cut=odt == torch.bfloat16)
         say("matmul m=%d n=%d k=%d %s -> %s" % (m, n, k, xdt, odt))
         out = torch.full((m + 1, n), 123.0, dtype=odt, device="cuda")
         wk = moe.block_matmul_workspace(x, n)
@@ -266,7 +266,8 @@ def upload(L):
 
 
 def layer_ref(L, idx, w, n_shared):
-    """(y, bound) of the layer for a given routing."""
+    """(y, bound) of the layer for a given routing (many rows per expert: the 8-bit instruction's bound)."""
+    cut = idx.size > 32 * len(L["wr"])
     xd = R.dequant_rows(*R.quantize(L["x"].double().numpy()))
     T, k = idx.shape
 
@@ -275,12 +276,12 @@ def layer_ref(L, idx, w, n_shared):
 
     y, err, mag = np.zeros((T, L["x"].shape[1])), 0.0, 0.0
     if n_shared:
-        y, err = R.expert(xd, *mats(0, ("s_gate", "s_up", "s_down")))
+        y, err = R.expert(xd, *mats(0, ("s_gate", "s_up", "s_down")), cut)
         mag = np.abs(y)
     err, mag = np.zeros_like(y) + err, np.zeros_like(y) + mag
     for e in np.unique(idx):
         t, j = np.nonzero(idx == e)
-        r, re = R.expert(xd[t], *mats(e, ("gate", "up", "down")))
+        r, re = R.expert(xd[t], *mats(e, ("gate", "up", "down")), cut)
         wt = w[t, j][:, None].astype(np.float64)
         y[t] += wt * r
         err[t] += np.abs(wt) * re
@@ -482,7 +483,7 @@ def test_run_together(dev):
     moe.moe_expert_ffn(c, x, moe.make_weights(W), off, perm, w, slot, sh, ws)
     moe.moe_combine(c, slot, sh, y)
     torch.cuda.synchronize()
-    ref, err = R.matmul(R.dequant_rows(*R.quantize(L["x"].double().numpy())), R.dequant_weight(pv, ps.astype(np.float64)))
+    ref, err = R.matmul(R.dequant_rows(*R.quantize(L["x"].double().numpy())), R.dequant_weight(pv, ps.astype(np.float64)), cut=True)
     assert (np.abs(x.double().cpu().numpy() - ref) <= R.bf16_bound(ref, err)).all()
     ri, rw = R.select(lg.cpu().numpy(), L["bias"], k, "softmax", 1.5, 4, 2, 2, True)
     assert np.array_equal(idx.cpu().numpy(), ri)
