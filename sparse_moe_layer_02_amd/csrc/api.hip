@@ -4,6 +4,7 @@
 // MFMA GEMMs).  All device work is enqueued on the caller's stream; nothing
 // here allocates, frees or synchronises.
 #include <math.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include <mutex>
@@ -76,6 +77,7 @@ int gemm_bm(const moe_config* c) {
     const long n = (long)c->n_tokens * c->top_k;
     if (c->w_dtype == MOE_DT_F8B128) {
         const long e = c->n_expert;
+        if (const char* v = getenv("F8BM")) return atoi(v);
         return n <= 4 * e ? 16 : n <= 20 * e ? 32 : n <= 48 * e ? 64 : n <= 96 * e ? 128 : 256;
     }
     return n >= 96L * c->n_expert ? 256 : 64;

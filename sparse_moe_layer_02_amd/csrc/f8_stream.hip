@@ -131,125 +131,6 @@ __device__ __forceinline__ void f8_stream(const uint8_t* const (&wp)[NR], const 
     }
 }
 
-// Activation row of tile row r (rows past the tile repeat its first; their
-// results are not stored): the token in gate/up.
-__device__ __forceinline__ int f8_token(const FfnArgs& a, const TileRows& tr, int r) {
-    r = r < tr.nrows ? r : 0;
-    if (tr.g == a.E) return tr.rbeg - a.T * a.k + r;
-    const int f = a.perm_rows[tr.rbeg + r];
-    return f >= 0 && f < a.T * a.k ? f / a.k : 0;
-}
-
-// ---------------------------------------------------------------------------
-// gate/up: a workgroup takes the 128 h columns of one scale block for a tile
-// of 16 NT rows, 16 columns per wavefront.
-// ---------------------------------------------------------------------------
-template <int NT>
-__global__ __launch_bounds__(64 * SW) void f8_gateup_stream_kernel(F8Ffn a) {
-    __shared__ uint32_t red[SW][16 * NT];
-    int tile, ntile;
-    if (!work_item<16>(tile_count(a.f), tile, ntile)) return;
-    TileRows tr;
-    if (!tile_rows<16 * NT>(a.f, tile, tr)) return;
-    const bool shared = tr.g == a.f.E;
-    const int F = shared ? a.f.Fs : a.f.F, d = a.f.d, n0 = ntile * F8_BLK;
-    if (n0 >= F) return;
-    const int lane = lane_id(), wave = wave_index(), KB = f8_blocks(d);
-    const MatRef& G = shared ? a.f.s_gate : a.f.gate;
-    const MatRef& U = shared ? a.f.s_up : a.f.up;
-    const int e = shared ? 0 : tr.g, c0 = n0 + 16 * wave;
-    const size_t wrow = ((size_t)e * F + min(c0 + lane % 16, F - 1)) * d;
-    const size_t srow = ((size_t)e * f8_blocks(F) + ntile) * KB;
-    const uint8_t* wp[2] = {static_cast<const uint8_t*>(G.q) + wrow, static_cast<const uint8_t*>(U.q) + wrow};
-    const float* sp[2] = {reinterpret_cast<const float*>(G.scale) + srow, reinterpret_cast<const float*>(U.scale) + srow};
-    const uint8_t *xp[NT], *ep[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int tok = f8_token(a.f, tr, 16 * t + lane % 16);
-        xp[t] = a.xq + (size_t)tok * d;
-        ep[t] = a.xe + (size_t)tok * f8_scale_ld(d);
-    }
-    f8_f4 acc[2][NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = f8_f4{0.f, 0.f, 0.f, 0.f};
-    f8_stream<2, NT, NT <= 2 ? 2 : 1>(wp, sp, xp, ep, 0, KB, d, acc);
-    // h, then its scale over the workgroup's 128 columns
-    const bool in = c0 < F;  // (F is a multiple of 64: a wavefront's columns are all in or all out)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            acc[0][t][v] = silu_f32(acc[0][t][v]) * acc[1][t][v];
-            m = max(m, f8_abs_bits(acc[0][t][v]));
-        }
-        m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-        if (lane < 16) red[wave][16 * t + lane] = in ? m : 0u;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int r = 16 * t + lane % 16;
-        uint32_t m = 0;
-#pragma unroll
-        for (int w = 0; w < SW; ++w) m = max(m, red[w][r]);
-        const uint32_t byte = f8_scale_byte(m);
-        const f8_f4 h = acc[0][t];
-        if (r >= tr.nrows) continue;
-        const size_t hrow = (size_t)(tr.rbeg + r);
-        if (in)
-            *reinterpret_cast<uint32_t*>(a.hq + hrow * a.f.ldh + c0 + 4 * (lane / 16)) =
-                f8_pack4(h[0], h[1], h[2], h[3], f8_inv_scale(byte), byte);
-        if (wave == 0 && lane < 16) a.he[hrow * f8_scale_ld(a.f.ldh) + ntile] = (uint8_t)byte;
-    }
-}
-
-// ---------------------------------------------------------------------------
-// down: 128 output columns per workgroup, 16 per wavefront.
-// ---------------------------------------------------------------------------
-template <int NT>
-__global__ __launch_bounds__(64 * SW) void f8_down_stream_kernel(F8Ffn a) {
-    int tile, ntile;
-    if (!work_item<16>(tile_count(a.f), tile, ntile)) return;
-    TileRows tr;
-    if (!tile_rows<16 * NT>(a.f, tile, tr)) return;
-    const bool shared = tr.g == a.f.E;
-    const int F = shared ? a.f.Fs : a.f.F, d = a.f.d;
-    const int lane = lane_id(), wave = wave_index(), KB = f8_blocks(F), c0 = ntile * F8_BLK + 16 * wave;
-    if (c0 >= d) return;  // (d is a multiple of 64)
-    const MatRef& D = shared ? a.f.s_down : a.f.down;
-    const int e = shared ? 0 : tr.g;
-    const uint8_t* wp[1] = {static_cast<const uint8_t*>(D.q) + ((size_t)e * d + c0 + lane % 16) * F};
-    const float* sp[1] = {reinterpret_cast<const float*>(D.scale) + ((size_t)e * f8_blocks(d) + ntile) * KB};
-    const uint8_t *xp[NT], *ep[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int r = 16 * t + lane % 16;
-        const size_t hrow = (size_t)(tr.rbeg + (r < tr.nrows ? r : 0));
-        xp[t] = a.hq + hrow * a.f.ldh;
-        ep[t] = a.he + hrow * f8_scale_ld(a.f.ldh);
-    }
-    f8_f4 acc[1][NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[0][t] = f8_f4{0.f, 0.f, 0.f, 0.f};
-    f8_stream<1, NT, NT <= 2 ? 4 : 2>(wp, sp, xp, ep, 0, KB, F, acc);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int r = 16 * t + lane % 16;
-        if (r >= tr.nrows) continue;
-        int dst = tr.rbeg - a.f.T * a.f.k + r;
-        float w = 1.0f;
-        if (!shared) {
-            dst = a.f.perm_rows[tr.rbeg + r];
-            if (dst < 0 || dst >= a.f.T * a.f.k) continue;
-            w = a.f.topk_w[dst];
-        }
-        float* out = (shared ? a.f.shared_out : a.f.slot_out) + (size_t)dst * d + c0 + 4 * (lane / 16);
-        st_stream16(out, make_float4(w * acc[0][t][0], w * acc[0][t][1], w * acc[0][t][2], w * acc[0][t][3]));
-    }
-}
-
 // ---------------------------------------------------------------------------
 // dense: 16 RB output columns per workgroup, K split over KS = SW / RB
 // wavefronts whose partial sums are added in LDS in a fixed order.
@@ -308,25 +189,6 @@ hipError_t dense_launch(const BlockArgs& a, hipStream_t st) {
 }
 
 }  // namespace
-
-hipError_t launch_f8_gateup(const F8Ffn& a, hipStream_t st, const KTime& kt) {
-    if (a.f.bm >= 128) return launch_f8_gateup_tile(a, st, kt);
-    const int fmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F;
-    const dim3 grid(a.f.max_tiles, f8_blocks(fmax));
-    if (a.f.bm == 16) launch_kernel(f8_gateup_stream_kernel<1>, grid, 64 * SW, st, kt, a);
-    else if (a.f.bm == 32) launch_kernel(f8_gateup_stream_kernel<2>, grid, 64 * SW, st, kt, a);
-    else launch_kernel(f8_gateup_stream_kernel<4>, grid, 64 * SW, st, kt, a);
-    return hipGetLastError();
-}
-
-hipError_t launch_f8_down(const F8Ffn& a, hipStream_t st, const KTime& kt) {
-    if (a.f.bm >= 128) return launch_f8_down_tile(a, st, kt);
-    const dim3 grid(a.f.max_tiles, f8_blocks(a.f.d));
-    if (a.f.bm == 16) launch_kernel(f8_down_stream_kernel<1>, grid, 64 * SW, st, kt, a);
-    else if (a.f.bm == 32) launch_kernel(f8_down_stream_kernel<2>, grid, 64 * SW, st, kt, a);
-    else launch_kernel(f8_down_stream_kernel<4>, grid, 64 * SW, st, kt, a);
-    return hipGetLastError();
-}
 
 hipError_t launch_block_matmul(const BlockArgs& a, hipStream_t st) {
     if (a.m > 128) return launch_block_matmul_tile(a, st);

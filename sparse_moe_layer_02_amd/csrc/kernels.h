@@ -165,8 +165,6 @@ struct F8Ffn {
 };
 hipError_t launch_f8_gateup(const F8Ffn& a, hipStream_t st, const KTime& kt = KTime());
 hipError_t launch_f8_down(const F8Ffn& a, hipStream_t st, const KTime& kt = KTime());
-hipError_t launch_f8_gateup_tile(const F8Ffn& a, hipStream_t st, const KTime& kt = KTime());  // bm 128 and 256
-hipError_t launch_f8_down_tile(const F8Ffn& a, hipStream_t st, const KTime& kt = KTime());
 
 // The decode path (T <= MOE_DECODE_MAX_TOKENS) in four launches: router;
 // selection + grouping beside the shared gate/up; routed gate/up; down +

@@ -266,8 +266,8 @@ def upload(L):
 
 
 def layer_ref(L, idx, w, n_shared):
-    """(y, bound) of the layer for a given routing (many rows per expert: the 8-bit instruction's bound)."""
-    cut = idx.size > 32 * len(L["wr"])
+    """(y, bound) of the layer for a given routing (its products may come from the 8-bit instruction)."""
+    cut = True
     xd = R.dequant_rows(*R.quantize(L["x"].double().numpy()))
     T, k = idx.shape
 
