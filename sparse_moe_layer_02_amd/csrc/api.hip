@@ -4,7 +4,6 @@
 // MFMA GEMMs).  All device work is enqueued on the caller's stream; nothing
 // here allocates, frees or synchronises.
 #include <math.h>
-#include <stdlib.h>
 #include <string.h>
 
 #include <mutex>
@@ -70,16 +69,15 @@ int ldh_of(const moe_config* c) {
 // 256-row product.  Fewer rows per expert: 64-row tiles (every expert
 // bandwidth-bound; the register-staged kernels keep more loads in flight per
 // CU).  int8 weights always take 64-row tiles (grouped_gemm_q8.hip).  e4m3
-// weights: the rows one pass over an expert's weights serves (f8_stream.hip).
-constexpr int F8_BM_MIN = 16;
+// weights: the tile shapes of f8_tile.hip (rows of a tile against LDS stages:
+// fewer rows, deeper weight ring), by the rows an expert averages.  Measured,
+// gate/up + down: 16 rows (512 tokens) 32-row tiles 2.04, 64-row 2.01 ms; 128
+// rows, unevenly spread (4096 tokens): 64-row 4.72, 128-row 3.90, 256-row 3.67 ms.
+constexpr int F8_BM_MIN = 32;
 int gemm_bm(const moe_config* c) {
     if (c->w_dtype == MOE_DT_Q8B32) return 64;
-    const long n = (long)c->n_tokens * c->top_k;
-    if (c->w_dtype == MOE_DT_F8B128) {
-        const long e = c->n_expert;
-        if (const char* v = getenv("F8BM")) return atoi(v);
-        return n <= 4 * e ? 16 : n <= 20 * e ? 32 : n <= 48 * e ? 64 : n <= 96 * e ? 128 : 256;
-    }
+    const long n = (long)c->n_tokens * c->top_k, e = c->n_expert;
+    if (c->w_dtype == MOE_DT_F8B128) return n <= 12 * e ? 32 : n <= 48 * e ? 64 : n <= 96 * e ? 128 : 256;
     return n >= 96L * c->n_expert ? 256 : 64;
 }
 

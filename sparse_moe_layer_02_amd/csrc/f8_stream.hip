@@ -1,21 +1,17 @@
-// f8_stream.hip - e4m3 products for few activation rows per weight matrix.
+// f8_stream.hip - e4m3 products for few activation rows: out[m, n] = x_m W_n.
 //
-//   gate/up:  h[r, c] = silu(x_r Wg_c) (x_r Wu_c), quantised per 128 columns
-//   down:     slot_out[f, :] = w_f (h_r Wd^T)
-//   dense:    out[m, n] = x_m W_n
-//
-// Bound by the weight bytes, each read once.  The weights go from memory
-// straight into the registers of the wavefront that uses them, in the order
-// the matrix instruction takes them, so neither LDS nor a barrier stands
-// between HBM and the multiply.  A wavefront owns 16 weight rows (16 gate and
-// 16 up rows); the 128 columns that share a scale are one step, whose codes
+// Bound by the weight bytes, each read once, and at these sizes by latency.
+// The weights go from memory straight into the registers of the wavefront
+// that uses them, in the order the matrix instruction takes them, so neither
+// LDS nor a barrier stands between HBM and the multiply.  A wavefront owns 16
+// NR weight rows; the 128 columns that share a scale are one step, whose codes
 // are widened to bf16 (exact) and multiplied on the matrix cores with fp32
 // sums (f8_dev.h: why not the 8-bit instruction; its rate is not needed
 // here).  A step's sum is multiplied by the activation row's power-of-two scale
-// (exact) and added with the weight block's fp32 scale.  Lane l reads columns 16 (l / 16) .. +15 of both
-// 64-column halves, so a load touches 64 consecutive bytes of 16 rows; the
-// activation rows are read the same way (their order in K is free as long as
-// both operands agree).
+// (exact) and added with the weight block's fp32 scale.  Lane l reads columns
+// 16 (l / 16) .. +15 of both 64-column halves, so a load touches 64 consecutive
+// bytes of 16 rows; the activation rows are read the same way (their order in
+// K is free as long as both operands agree).
 #include "common.h"
 #include "dma_dev.h"
 #include "f8_dev.h"
