@@ -47,8 +47,13 @@
  *    weight = scale * code.
  *  - Products with F8B128 weights are products of e4m3 operands: activations
  *    are quantised per row and 128 columns as moe_quantize_rows does (x, and
- *    the SwiGLU intermediate from its fp32 values), and sums are fp32.  Softmax
- *    scores are taken over all n_expert logits of a token.
+ *    the SwiGLU intermediate from its fp32 values).  Sums are fp32, except that
+ *    results that are rounded to 16 or 8 bits next (and the layer's, whose
+ *    intermediate is) may come from the 8-bit matrix instruction, which cuts
+ *    the products of 8 consecutive columns 13 bits below the largest of them
+ *    (1.5e-5 of a result; moe_block_matmul to fp32 never uses it).  Layers with
+ *    F8B128 weights need n_tokens * d_model < 2^32.  Softmax scores are taken
+ *    over all n_expert logits of a token.
  *  - Results: expert indices and the permutation are exact and do not depend
  *    on the path taken; logits and scores are accumulated in fp64 and rounded
  *    once to fp32; the SwiGLU intermediate is rounded to the activation format
@@ -270,7 +275,7 @@ int moe_quantize_rows(const void *x, int32_t x_dtype, int32_t rows, int32_t cols
 
 /* out [m, n] = x [m, k] w[n, k]^T with e4m3 operands:
  *   out[i, j] = sum_b s_x[i, b] * s_w[j / 128, b] * sum_{c in block b} q_x[i, c] * q_w[j, c]
- * (b: the blocks of 128 columns; fp32 sums).  x is MOE_DT_F8B128 codes with
+ * (b: the blocks of 128 columns; sums as above).  x is MOE_DT_F8B128 codes with
  * x_scale [m, MOE_F8_SCALE_LD(k)] as moe_quantize_rows writes them, or
  * MOE_DT_BF16 / MOE_DT_F32 rows, which are quantised that way first (x_scale
  * NULL, workspace needed).  w [n, k] codes, w_scale [ceil(n/128), ceil(k/128)]

@@ -54,6 +54,8 @@ int validate_config(const moe_config* c) {
     if ((size_t)c->d_model > (1u << 20) || (size_t)c->d_ff > (1u << 20) ||
         (c->n_shared && (size_t)c->d_ff_shared > (1u << 20)))
         return MOE_ERR_UNSUPPORTED;
+    // e4m3 layers address the quantised rows with 32-bit offsets (f8_tile.hip)
+    if (c->w_dtype == MOE_DT_F8B128 && (int64_t)c->n_tokens * c->d_model > 0xFFFFFFFFll) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
@@ -69,15 +71,13 @@ int ldh_of(const moe_config* c) {
 // 256-row product.  Fewer rows per expert: 64-row tiles (every expert
 // bandwidth-bound; the register-staged kernels keep more loads in flight per
 // CU).  int8 weights always take 64-row tiles (grouped_gemm_q8.hip).  e4m3
-// weights: the tile shapes of f8_tile.hip (rows of a tile against LDS stages:
-// fewer rows, deeper weight ring), by the rows an expert averages.  Measured,
-// gate/up + down: 16 rows (512 tokens) 32-row tiles 2.04, 64-row 2.01 ms; 128
-// rows, unevenly spread (4096 tokens): 64-row 4.72, 128-row 3.90, 256-row 3.67 ms.
-constexpr int F8_BM_MIN = 32;
+// weights: 64 rows, or 256 where experts average more than 192 (f8_tile.hip;
+// gate/up + down at d 6144, F 2048: 128 rows per expert, unevenly spread, 64-row
+// tiles 2.99, 256-row 3.00 ms; 512 rows 2.25 / 2.12 ms).
 int gemm_bm(const moe_config* c) {
     if (c->w_dtype == MOE_DT_Q8B32) return 64;
     const long n = (long)c->n_tokens * c->top_k, e = c->n_expert;
-    if (c->w_dtype == MOE_DT_F8B128) return n <= 12 * e ? 32 : n <= 48 * e ? 64 : n <= 96 * e ? 128 : 256;
+    if (c->w_dtype == MOE_DT_F8B128) return n > 192 * e ? 256 : 64;
     return n >= 96L * c->n_expert ? 256 : 64;
 }
 
@@ -104,7 +104,7 @@ Layout make_layout(const moe_config* c) {
     const size_t hsz = c->act_dtype == MOE_DT_BF16 ? 2 : 4;
     L.n_blk = (int)((n + PERM_BLOCK - 1) / PERM_BLOCK);
     const bool f8 = c->w_dtype == MOE_DT_F8B128;
-    L.max_tiles = max_tiles_of(c, f8 ? F8_BM_MIN : GEMM_BM);  // the smallest tile: capacity for any bm
+    L.max_tiles = max_tiles_of(c, GEMM_BM);  // the smallest tile: capacity for any bm
     size_t o = 0;
     auto take = [&](size_t bytes) {
         size_t at = o;

@@ -127,70 +127,67 @@ __device__ __forceinline__ void f8_stream(const uint8_t* const (&wp)[NR], const 
     }
 }
 
-// ---------------------------------------------------------------------------
-// dense: 16 RB output columns per workgroup, K split over KS = SW / RB
-// wavefronts whose partial sums are added in LDS in a fixed order.
-// ---------------------------------------------------------------------------
-template <int NT, int RB, int OF>
+// 16 NR output columns per workgroup, K split over its SW wavefronts, whose
+// partial sums are added in LDS in a fixed order.
+template <int NT, int NR, int OF>
 __global__ __launch_bounds__(64 * SW) void f8_dense_stream_kernel(BlockArgs a) {
-    constexpr int KS = SW / RB;
-    __shared__ f8_f4 part[KS > 1 ? KS - 1 : 1][RB][NT][WAVE];
-    const int lane = lane_id(), wave = wave_index(), rb = wave % RB, ks = wave / RB;
-    const int c0 = (blockIdx.x * RB + rb) * 16, m0 = blockIdx.y * 16 * NT, KB = f8_blocks(a.k);
-    const bool live = c0 < a.n;
-    f8_f4 acc[1][NT];
+    __shared__ f8_f4 part[SW][NR][NT][WAVE];
+    const int lane = lane_id(), wave = wave_index();
+    const int c0 = blockIdx.x * 16 * NR, m0 = blockIdx.y * 16 * NT, KB = f8_blocks(a.k);
+    f8_f4 acc[NR][NT];
+    const uint8_t* wp[NR];
+    const float* sp[NR];
+    const uint8_t *xp[NT], *ep[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[0][t] = f8_f4{0.f, 0.f, 0.f, 0.f};
-    if (live) {
-        const uint8_t* wp[1] = {a.wq + (size_t)min(c0 + lane % 16, a.n - 1) * a.k};
-        const float* sp[1] = {a.ws + (size_t)(c0 / F8_BLK) * KB};
-        const uint8_t *xp[NT], *ep[NT];
+    for (int r = 0; r < NR; ++r) {
+        wp[r] = a.wq + (size_t)min(c0 + 16 * r + lane % 16, a.n - 1) * a.k;
+        sp[r] = a.ws + (size_t)(min(c0 + 16 * r, a.n - 1) / F8_BLK) * KB;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const size_t r = (size_t)min(m0 + 16 * t + lane % 16, a.m - 1);
-            xp[t] = a.xq + r * a.k;
-            ep[t] = a.xe + r * f8_scale_ld(a.k);
-        }
-        const int per = (KB + KS - 1) / KS;
-        f8_stream<1, NT, NT <= 2 ? 4 : 2>(wp, sp, xp, ep, ks * per, min(KB, (ks + 1) * per), a.k, acc);
+        for (int t = 0; t < NT; ++t) acc[r][t] = f8_f4{0.f, 0.f, 0.f, 0.f};
     }
-    if constexpr (KS > 1) {
-        if (ks > 0)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) part[ks - 1][rb][t][lane] = acc[0][t];
-        __syncthreads();
-        if (ks > 0) return;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int s = 0; s < KS - 1; ++s) acc[0][t] += part[s][rb][t][lane];
-    }
-    const int c = c0 + 4 * (lane / 16);
-    if (c >= a.n) return;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int r = m0 + 16 * t + lane % 16;
-        if (r >= a.m) continue;
-        const float v[4] = {acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3]};
-        f8_store4<OF>(a.out, (size_t)r * a.n + c, a.n - c, v, a.n % 4 == 0);
+        const size_t r = (size_t)min(m0 + 16 * t + lane % 16, a.m - 1);
+        xp[t] = a.xq + r * a.k;
+        ep[t] = a.xe + r * f8_scale_ld(a.k);
+    }
+    const int per = (KB + SW - 1) / SW;
+    f8_stream<NR, NT, 4 / NR>(wp, sp, xp, ep, wave * per, min(KB, (wave + 1) * per), a.k, acc);
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) part[wave][r][t][lane] = acc[r][t];
+    __syncthreads();
+    // wavefront w adds the partial sums of the (r, t) tiles w, w + SW, ...
+    for (int q = wave; q < NR * NT; q += SW) {
+        const int r = q / NT, t = q % NT;
+        f8_f4 s = part[0][r][t][lane];
+#pragma unroll
+        for (int w = 1; w < SW; ++w) s += part[w][r][t][lane];
+        const int c = c0 + 16 * r + 4 * (lane / 16), row = m0 + 16 * t + lane % 16;
+        if (c >= a.n || row >= a.m) continue;
+        const float v[4] = {s[0], s[1], s[2], s[3]};
+        f8_store4<OF>(a.out, (size_t)row * a.n + c, a.n - c, v, a.n % 4 == 0);
     }
 }
 
-template <int NT, int RB>
+template <int NT, int NR>
 hipError_t dense_launch(const BlockArgs& a, hipStream_t st) {
-    const dim3 grid((a.n + 16 * RB - 1) / (16 * RB), (a.m + 16 * NT - 1) / (16 * NT));
-    if (a.odt == MOE_DT_BF16) f8_dense_stream_kernel<NT, RB, MOE_DT_BF16><<<grid, 64 * SW, 0, st>>>(a);
-    else f8_dense_stream_kernel<NT, RB, MOE_DT_F32><<<grid, 64 * SW, 0, st>>>(a);
+    const dim3 grid((a.n + 16 * NR - 1) / (16 * NR), (a.m + 16 * NT - 1) / (16 * NT));
+    if (a.odt == MOE_DT_BF16) f8_dense_stream_kernel<NT, NR, MOE_DT_BF16><<<grid, 64 * SW, 0, st>>>(a);
+    else f8_dense_stream_kernel<NT, NR, MOE_DT_F32><<<grid, 64 * SW, 0, st>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// Up to 48 rows here, more in LDS tiles (us at n x k 4096 x 6144: 1 row 9.1
+// against 20.8 for the smallest tiles, 24 rows 16.7 / 21.2, 128 rows 24.8 / 23.1;
+// 48 rows of 4096 x 4096 13.0 / 16.4, 77 rows of 6144 x 2048 16.4 / 10.1).
 hipError_t launch_block_matmul(const BlockArgs& a, hipStream_t st) {
-    if (a.m > 128) return launch_block_matmul_tile(a, st);
     if (a.m <= 16) return dense_launch<1, 1>(a, st);
-    if (a.m <= 32) return dense_launch<2, 2>(a, st);
-    return dense_launch<4, 4>(a, st);
+    if (a.m <= 48) return dense_launch<2, 2>(a, st);
+    return launch_block_matmul_tile(a, st);
 }
 
 }  // namespace moe

@@ -4,17 +4,16 @@
 //   down:     slot_out[f, :] = w_f (h_r Wd^T)
 //   dense:    out[m, n] = x_m W_n
 //
-// A workgroup of eight wavefronts computes 32 NB GM activation rows x 256
-// weight rows (gate/up: 128 gate and the same 128 up rows, so that a tile holds
-// whole scale blocks of h); GM wavefronts along the activation rows, 8 / GM
-// along the weight rows, each NB x GM blocks of 32 x 32.  A stage is one step of 128
-// columns, the width of a scale block: 128-byte rows, copied straight from
-// global memory into LDS (eight whole cache lines per copy instruction, 16-byte
-// chunks swizzled by row as dma_dev.h describes), in a ring of NST stages behind
-// one barrier per stage.  A block's partial sum over the stage starts from zero
-// on the matrix cores and is added with the weight block's fp32 scale, which is
-// uniform over the block (one v_fma per 16 x 64 results, an SGPR operand); the
-// activation rows' e8m0 scales are applied by the matrix instruction.
+// A workgroup computes a tile of activation rows x weight rows (gate/up: 128
+// gate and the same 128 up rows, so that a tile holds whole scale blocks of h),
+// each wavefront blocks of 32 x 32 of it.  A stage is one step of 128 columns,
+// the width of a scale block: 128-byte rows, copied straight from global
+// memory into LDS (eight whole cache lines per copy instruction, 16-byte
+// chunks swizzled by row as dma_dev.h describes), in a ring of stages behind
+// one barrier per stage.  A block's sum over the stage starts from zero on the
+// matrix cores and is added with the weight block's fp32 scale, uniform over
+// the block (one FMA per lane's result, an SGPR operand); the activation rows'
+// e8m0 scales are applied by the matrix instruction.
 //
 // WIDE: the codes are widened to bf16 and the sums are fp32 (f8_dev.h); taken
 // for fp32 results.  Otherwise the 8-bit instruction, twice the rate, for
@@ -23,6 +22,8 @@
 // A tile computes only the 32-row blocks that hold rows: blocks are dealt to the
 // two wavefront rows in turn, and each wavefront runs the K loop built for its
 // number of live blocks.
+#include <utility>
+
 #include "common.h"
 #include "dma_dev.h"
 #include "f8_dev.h"
@@ -32,92 +33,187 @@
 namespace moe {
 namespace {
 
-constexpr int TW = 8;              // wavefronts
-constexpr int TN = 256;            // weight rows per tile
-constexpr int TWB = TN * F8_BLK;   // bytes of one stage's weight rows
-constexpr int TWC = TWB / 1024 / TW;  // 1 KB weight copies per wavefront and stage
-
-// Tile shapes: NB blocks of 32 activation rows per wavefront, GM wavefronts
-// along them, NST stages in LDS (what 160 KB hold).
-template <int NB_, int GM_, int NST_>
+// Tile shapes: GM x GN wavefronts (GM along the activation rows, GN along the
+// weight rows), each NB x NJ blocks of 32 x 32, NST stages in LDS.
+template <int NB_, int NJ_, int GM_, int GN_, int NST_>
 struct Shape {
-    static constexpr int NB = NB_, GM = GM_, NST = NST_;
+    static constexpr int NB = NB_, NJ = NJ_, GM = GM_, GN = GN_, NST = NST_;
+    static constexpr int W = GM * GN;              // wavefronts
     static constexpr int BM = 32 * NB * GM;        // activation rows
-    static constexpr int GN = TW / GM;             // wavefronts along the weight rows
-    static constexpr int WR = TN / GN;             // weight rows per wavefront: GM blocks of 32
-    static constexpr int XB = BM * F8_BLK;         // bytes of one stage's activation rows
-    static constexpr int XCP = XB / 1024;          // 1 KB copies of them
-    static constexpr int XQ = (XCP + TW - 1) / TW; // at most, per wavefront
+    static constexpr int WR = 32 * NJ, TN = WR * GN;         // weight rows per wavefront, per tile
+    static constexpr int WB = TN * F8_BLK, XB = BM * F8_BLK; // bytes of a stage
+    static constexpr int WQ = WB / 1024 / W;                 // 1 KB copies per wavefront and stage
+    static constexpr int XQ = (XB / 1024 + W - 1) / W;       // (at most)
+    static_assert(WQ * 1024 * W == WB, "weight copies");
 };
-typedef Shape<1, 1, 4> Rows32;
-typedef Shape<2, 1, 3> Rows64;
-typedef Shape<2, 2, 3> Rows128;
-typedef Shape<4, 2, 2> Rows256;
+// Expert tiles (256 weight rows, the two scale blocks of a 128-column h block).
+// Up to 64 activation rows: two workgroups per compute unit, each with two
+// stages, so that one's start and end lie under the other's loop (gate/up of
+// 512 tokens, 16 rows per expert: 1.06 ms, 6.1 TB/s of weights; one workgroup
+// with four stages 1.35 ms).  More: the matrix work sets the pace, and a
+// larger tile reads LDS less per product.
+typedef Shape<1, 2, 2, 4, 2> Rows64;
+typedef Shape<4, 2, 2, 4, 2> Rows256;
+// Further tiles of the dense product, for sizes whose largest tiles would leave
+// compute units idle, and for fp32 results (whose widened operands do not fit
+// beside the accumulators of the largest tile).
+typedef Shape<2, 2, 2, 4, 3> Rows128;
+typedef Shape<2, 2, 2, 2, 2> Square128;
+typedef Shape<1, 1, 2, 2, 4> Square64;
 
-// Per-lane sources of one tile.
+// Sources of one tile: wave-uniform buffers and 32-bit lane offsets (64-bit lane
+// pointers of the largest shape did not fit the register file, and a buffer load
+// adds the step's offset without a vector instruction).
 template <class S>
 struct F8Tile {
-    static constexpr int NB = S::NB;
-    const uint8_t* wsrc[TWC];  // weight row bytes this copy lane fetches at K = 0
-    const uint8_t* xsrc[S::XQ];// activation row bytes
-    int wch, xch;              // the lane's 16-byte chunk in a stage row (weights, activations), in bytes
-    const uint8_t* ep[NB];     // scale bytes of the lane's activation row in each live block
-    const float* sp[2];        // block scales of the wavefront's weight rows (gate/up: of gate, of up)
+    const uint8_t *wbase, *xbase, *ebase;  // weight rows (of gate or of up), activation rows, scale bytes
+    uint32_t woff[S::WQ];         // the copy lane's bytes of weight copy q, at K = 0
+    uint32_t xoff[S::XQ];
+    uint32_t eoff[S::NB];         // scale bytes of the lane's activation row in each block
+    int ch;                       // the copy lane's 16-byte chunk in a stage row, in bytes
+    const float* sp[2];           // block scales of the wavefront's weight rows (gate/up: of gate, of up)
     int K, nst;
 };
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_buffer(const uint8_t* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, 0xFFFFFFFF, 0x00020000);
+}
+__device__ __forceinline__ void buffer_copy16(__amdgpu_buffer_rsrc_t r, uint32_t off, int k0, uint8_t* dst) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst), 16, (int)off, k0, 0, 0);
+}
 
 // Copy lane l of copy c fills row 8 c + l / 8, slot l % 8.
 __device__ __forceinline__ int copy_row(int c, int lane) { return 8 * c + (lane >> 3); }
 __device__ __forceinline__ int copy_chunk(int row, int lane) { return 16 * ((lane & 7) ^ pair_swz(row)); }
 
-// 32 codes of row r: columns 64 h + 32 (lane / 32) .. + 31 of the stage.
+// 32 codes of a lane's row: columns 64 h + 32 (lane / 32) .. + 31 of the stage.
 struct F8Row {
     f8_u4 a, b;
 };
-__device__ __forceinline__ F8Row tile_row(const uint8_t* S, int r, int h) {
-    const int c = 4 * h + 2 * (lane_id() >> 5), sw = pair_swz(r);
-    const uint8_t* p = S + r * F8_BLK;
-    return F8Row{*reinterpret_cast<const f8_u4*>(p + ((c ^ sw) << 4)), *reinterpret_cast<const f8_u4*>(p + (((c + 1) ^ sw) << 4))};
+// Byte offsets of those chunks from the first row of a block of 32 rows (the
+// swizzle repeats every 16 rows, so they serve every block).
+struct F8Lane {
+    uint32_t o[4];
+};
+__device__ __forceinline__ F8Lane tile_lane(int lane) {
+    F8Lane f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        f.o[k] = (lane & 31) * F8_BLK + (((4 * (k >> 1) + 2 * (lane >> 5) + (k & 1)) ^ pair_swz(lane & 31)) << 4);
+    return f;
+}
+__device__ __forceinline__ F8Row tile_row(const uint8_t* S, const F8Lane& f, uint32_t block, int h) {
+    return F8Row{*reinterpret_cast<const f8_u4*>(S + (f.o[2 * h] + block)),
+                 *reinterpret_cast<const f8_u4*>(S + (f.o[2 * h + 1] + block))};
+}
+
+// f(ic<0>()), ..., f(ic<N - 1>()): indices that are constants from the start.
+template <class F, int... I>
+__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>) {
+    (f(ic<I>()), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F f) {
+    each_of(f, std::make_integer_sequence<int, N>());
 }
 
 // The K loop of one wavefront with L live blocks and XC activation copies per
 // stage; acc[i][j]: block i (activation rows) x weight row block j.  SPLIT: the
 // wavefront's one weight block holds 16 gate rows and 16 up rows.
 template <class S, int L, int XC, bool WIDE, bool SPLIT>
-__device__ __forceinline__ void tile_loop(const F8Tile<S>& g, uint8_t* const (&W)[S::NST], uint8_t* const (&X)[S::NST],
-                                          f8_f16 (&acc)[S::NB][S::GM]) {
-    constexpr int NST = S::NST, NB = S::NB, NJ = S::GM;
-    const int lane = lane_id(), wave = wave_index(), mh = wave / S::GN, wn = wave % S::GN, l32 = lane & 31;
+__device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NST], uint8_t* const (&X)[S::NST],
+                                          f8_f16 (&out)[S::NB][S::NJ]) {
+    constexpr int NST = S::NST, NB = S::NB, NJ = S::NJ, TW = S::W, TWC = S::WQ;
+    const int wave = wave_index(), mh = wave / S::GN, wn = wave % S::GN;
+    const F8Lane fl = tile_lane(lane_id());
     constexpr int NC = TWC + XC;
-    const int last = g.nst - 1, ktail = g.K & (F8_BLK - 1);
+    const int nfull = g.K / F8_BLK, last = nfull - 1;  // whole stages
+    // (opaque: single registers, not parts of vectors or of 64-bit values)
+#pragma unroll
+    for (int q = 0; q < TWC; ++q) __asm__ volatile("" : "+v"(g.woff[q]));
+#pragma unroll
+    for (int q = 0; q < XC; ++q) __asm__ volatile("" : "+v"(g.xoff[q]));
+#pragma unroll
+    for (int i = 0; i < L; ++i) __asm__ volatile("" : "+v"(g.eoff[i]));
+    const __amdgpu_buffer_rsrc_t wr = tile_buffer(g.wbase), xr = tile_buffer(g.xbase), er = tile_buffer(g.ebase);
     auto issue = [&](uint8_t* w, uint8_t* x, int kb) {
-        kb = min(kb, last);  // (stages past the end re-read the last; not used)
-        const int k0 = kb * F8_BLK;
-        if (kb == last && ktail) {  // columns past K come from a row of zeros
+        const int k0 = min(kb, last) * F8_BLK;  // (stages past the end re-read the last; not used)
 #pragma unroll
-            for (int q = 0; q < TWC; ++q)
-                copy16(g.wch < ktail ? g.wsrc[q] + k0 : reinterpret_cast<const uint8_t*>(f8_zeros), w + (q * TW + wave) * 1024);
+        for (int q = 0; q < TWC; ++q) buffer_copy16(wr, g.woff[q], k0, w + (q * TW + wave) * 1024);
 #pragma unroll
-            for (int q = 0; q < XC; ++q)
-                copy16(g.xch < ktail ? g.xsrc[q] + k0 : reinterpret_cast<const uint8_t*>(f8_zeros), x + (q * TW + wave) * 1024);
-            return;
-        }
-#pragma unroll
-        for (int q = 0; q < TWC; ++q) copy16(g.wsrc[q] + k0, w + (q * TW + wave) * 1024);
-#pragma unroll
-        for (int q = 0; q < XC; ++q) copy16(g.xsrc[q] + k0, x + (q * TW + wave) * 1024);
+        for (int q = 0; q < XC; ++q) buffer_copy16(xr, g.xoff[q], k0, x + (q * TW + wave) * 1024);
     };
     uint32_t ev[NB], en[NB];
 #pragma unroll
-    for (int i = 0; i < L; ++i) en[i] = *reinterpret_cast<const uint32_t*>(g.ep[i]);
+    for (int i = 0; i < L; ++i) en[i] = __builtin_amdgcn_raw_buffer_load_b32(er, (int)g.eoff[i], 0, 0);
+    if (nfull > 0) {
 #pragma unroll
-    for (int s = 0; s < NST - 1; ++s) issue(W[s], X[s], s);
-    float sw[2];
-    sw[0] = f8_uniform(g.sp[0], 0);
-    sw[1] = f8_uniform(g.sp[1], 0);
-    auto stage = [&](auto bb, auto ss, int kb) {
-        constexpr int B = decltype(bb)::value;    // LDS stage
-        constexpr int SEL = decltype(ss)::value;  // kb % 4: byte of the activation scales
+        for (int s = 0; s < NST - 1; ++s) issue(W[s], X[s], s);
+    }
+    // Weight scales: at the top of a round lane l holds those of the round's
+    // stage l.  (Scalar loads count with the LDS reads, out of order, and every
+    // partial wait for LDS data became a full one.)
+    float sl[2], sn[2];
+    auto scales = [&](int kb) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) sn[j] = g.sp[j][min(kb + lane_id(), g.nst - 1)];
+    };
+    scales(0);
+    f8_f16 acc[NB][NJ];
+    each<NB * NJ>([&](auto b) { acc[decltype(b)::value / NJ][decltype(b)::value % NJ] = f8_f16{}; });
+    // the products of LDS stage B; byte SEL of ev scales the activation rows,
+    // lane LN of sl the weight rows
+    auto products = [&](auto bb, auto ss, auto ll) {
+        constexpr int B = decltype(bb)::value, SEL = decltype(ss)::value, LN = decltype(ll)::value;
+        const float s0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sl[0]), LN));
+        const float s1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sl[1]), LN));
+        // (opaque: addresses formed from them are not kept over the loop, where
+        // they would take registers the accumulators need)
+        uint32_t wo = S::WR * wn * F8_BLK, xo = 32 * mh * F8_BLK;
+        __asm__ volatile("" : "+s"(wo), "+s"(xo));
+        F8Row w[NJ][2];
+        each<NJ>([&](auto jj) {
+            constexpr int j = decltype(jj)::value;
+            w[j][0] = tile_row(W[B] + 32 * j * F8_BLK, fl, wo, 0);
+            w[j][1] = tile_row(W[B] + 32 * j * F8_BLK, fl, wo, 1);
+        });
+        F8Wide ww[NJ][2];
+        if constexpr (WIDE) {
+            each<NJ * 2>([&](auto q) {
+                constexpr int j = decltype(q)::value / 2, h = decltype(q)::value % 2;
+                ww[j][h] = f8_widen(w[j][h].a, w[j][h].b);
+            });
+        }
+        each<L>([&](auto ii) {
+            constexpr int i = decltype(ii)::value;
+            const F8Row x0 = tile_row(X[B] + 32 * S::GM * i * F8_BLK, fl, xo, 0);
+            const F8Row x1 = tile_row(X[B] + 32 * S::GM * i * F8_BLK, fl, xo, 1);
+            F8Wide v0, v1;
+            if constexpr (WIDE) {
+                v0 = f8_widen(x0.a, x0.b);
+                v1 = f8_widen(x1.a, x1.b);
+            }
+            each<NJ>([&](auto jj) {
+                constexpr int j = decltype(jj)::value;
+                f8_f16 p;
+                if constexpr (WIDE) {
+                    p = f8_dot32(ww[j][1], v1, f8_dot32(ww[j][0], v0, f8_f16{})) *
+                        f8_scale_value((ev[i] >> (8 * SEL)) & 255u);
+                } else {
+                    p = f8_mfma32<SEL>(f8_join(w[j][0].a, w[j][0].b), f8_join(x0.a, x0.b), f8_f16{}, ev[i]);
+                    p = f8_mfma32<SEL>(f8_join(w[j][1].a, w[j][1].b), f8_join(x1.a, x1.b), p, ev[i]);
+                }
+                // (whole-vector operations: accumulators written element by
+                // element in a loop went to scratch memory)
+                const float a = j > 0 ? s1 : s0, b = SPLIT ? s1 : a;
+                const f8_f16 s = f8_f16{a, a, a, a, a, a, a, a, b, b, b, b, b, b, b, b};
+                acc[i][j] = __builtin_elementwise_fma(s, p, acc[i][j]);
+            });
+            if constexpr (NB * NJ == 8) pin();  // (more blocks' sums in flight than the registers hold, otherwise)
+        });
+        wait_lgkm0();  // this stage's reads are done before the next barrier releases its refill
+    };
+    auto stage = [&](auto nn, int kb) {
+        constexpr int n = decltype(nn)::value, B = n % NST, SEL = n % 4;
         wait_vm<(NST - 2) * NC>();
         barrier_nofence();
         issue(W[(B + NST - 1) % NST], X[(B + NST - 1) % NST], kb + NST - 1);
@@ -125,91 +221,82 @@ __device__ __forceinline__ void tile_loop(const F8Tile<S>& g, uint8_t* const (&W
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 ev[i] = en[i];
-                en[i] = *reinterpret_cast<const uint32_t*>(g.ep[i] + (kb + 4 <= last ? kb + 4 : 0));
+                en[i] = __builtin_amdgcn_raw_buffer_load_b32(er, (int)g.eoff[i], kb + 4 < g.nst ? kb + 4 : 0, 0);
             }
         }
-        const float s0 = sw[0], s1 = sw[1];
-        sw[0] = f8_uniform(g.sp[0], min(kb + 1, last));
-        sw[1] = f8_uniform(g.sp[1], min(kb + 1, last));
-        if constexpr (L > 0) {
-            F8Row w[NJ][2];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) w[j][h] = tile_row(W[B], S::WR * wn + 32 * j + l32, h);
-            F8Wide ww[NJ][2];
-            if constexpr (WIDE) {
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) ww[j][h] = f8_widen(w[j][h].a, w[j][h].b);
-            }
-#pragma unroll
-            for (int i = 0; i < L; ++i) {
-                const int xr = 32 * (mh + S::GM * i) + l32;
-                const F8Row x0 = tile_row(X[B], xr, 0), x1 = tile_row(X[B], xr, 1);
-                auto add = [&](const f8_f16& p, int j) {
-#pragma unroll
-                    for (int v = 0; v < 16; ++v)
-                        acc[i][j][v] = fmaf((SPLIT ? v >= 8 : j > 0) ? s1 : s0, p[v], acc[i][j][v]);
-                };
-                if constexpr (WIDE) {
-                    const F8Wide v0 = f8_widen(x0.a, x0.b), v1 = f8_widen(x1.a, x1.b);
-                    const float sx = f8_scale_value((ev[i] >> (8 * SEL)) & 255u);
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) add(f8_dot32(ww[j][1], v1, f8_dot32(ww[j][0], v0, f8_f16{})) * sx, j);
-                } else {
-                    const i32x8_t v0 = f8_join(x0.a, x0.b), v1 = f8_join(x1.a, x1.b);
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        const f8_f16 p = f8_mfma32<SEL>(f8_join(w[j][0].a, w[j][0].b), v0, f8_f16{}, ev[i]);
-                        add(f8_mfma32<SEL>(f8_join(w[j][1].a, w[j][1].b), v1, p, ev[i]), j);
-                    }
-                }
-            }
-            wait_lgkm0();  // this stage's reads are done before the next barrier releases its refill
-        }
+        if constexpr (L > 0) products(ic<B>(), ic<SEL>(), nn);
     };
     // twelve (four) stages run through every pair of LDS stage and scale byte
     constexpr int CYC = NST == 3 ? 12 : 4;
-    for (int kb = 0; kb < g.nst; kb += CYC) {
+    for (int kb = 0; kb < nfull; kb += CYC) {
+        sl[0] = sn[0];
+        sl[1] = sn[1];
+        scales(kb + CYC);
 #define F8_STAGE(n) \
-    if constexpr (n < CYC) { if (kb + n < g.nst) stage(ic<(n) % NST>(), ic<(n) % 4>(), kb + n); }
+    if constexpr (n < CYC) { if (kb + n < nfull) stage(ic<n>(), kb + n); }
         F8_STAGE(0) F8_STAGE(1) F8_STAGE(2) F8_STAGE(3) F8_STAGE(4) F8_STAGE(5)
         F8_STAGE(6) F8_STAGE(7) F8_STAGE(8) F8_STAGE(9) F8_STAGE(10) F8_STAGE(11)
 #undef F8_STAGE
     }
+    if (g.nst > nfull) {  // the step that K ends in: columns past K come from a row of zeros
+        wait_vm<0>();
+        barrier_nofence();  // every stage has landed and been read
+        const bool in = g.ch < g.K - nfull * F8_BLK;
+        const uint8_t* zero = reinterpret_cast<const uint8_t*>(f8_zeros);
+        // (opaque: or the 64-bit forms of the offsets would be kept over the loop)
+        auto from = [&](const uint8_t* base, uint32_t off) {
+            __asm__ volatile("" : "+v"(off));
+            return in ? base + nfull * F8_BLK + off : zero;
+        };
+#pragma unroll
+        for (int q = 0; q < TWC; ++q) copy16(from(g.wbase, g.woff[q]), W[0] + (q * TW + wave) * 1024);
+#pragma unroll
+        for (int q = 0; q < XC; ++q) copy16(from(g.xbase, g.xoff[q]), X[0] + (q * TW + wave) * 1024);
+#pragma unroll
+        for (int i = 0; i < L; ++i) ev[i] = __builtin_amdgcn_raw_buffer_load_b8(er, (int)g.eoff[i], nfull, 0);
+        wait_vm<0>();
+        barrier_nofence();
+        if constexpr (L > 0) {
+            sl[0] = g.sp[0][nfull];
+            sl[1] = g.sp[1][nfull];
+            products(ic<0>(), ic<0>(), ic<0>());
+        }
+    }
     wait_vm<0>();  // no copy may still be writing LDS when the workgroup ends
+    each<NB * NJ>([&](auto b) {
+        constexpr int i = decltype(b)::value / NJ, j = decltype(b)::value % NJ;
+        out[i][j] = acc[i][j];
+    });
 }
 
 // Runs the loop built for this wavefront's live blocks (rows of the tile: nrows).
-// A round of activation copies of the eight wavefronts covers 64 rows.
 template <class S, bool WIDE, bool SPLIT>
 __device__ __forceinline__ void tile_run(const F8Tile<S>& g, int nrows, uint8_t* const (&W)[S::NST],
-                                         uint8_t* const (&X)[S::NST], f8_f16 (&acc)[S::NB][S::GM]) {
+                                         uint8_t* const (&X)[S::NST], f8_f16 (&acc)[S::NB][S::NJ]) {
     const int wave = wave_index(), nblk = (nrows + 31) / 32, live = (nblk - wave / S::GN + S::GM - 1) / S::GM;
     auto run = [&](auto l, auto xc) { tile_loop<S, decltype(l)::value, decltype(xc)::value, WIDE, SPLIT>(g, W, X, acc); };
-    if constexpr (S::GM == 2) {
+    static_assert(S::GM == 2, "two wavefronts along the activation rows");
+    {  // a round of activation copies covers W / 4 blocks
+        constexpr int RB = S::W / 4;
         if constexpr (S::NB == 4) {
+            static_assert(RB == 2 && S::GM == 2, "eight wavefronts");
             if (nblk > 6) return live == 4 ? run(ic<4>(), ic<4>()) : run(ic<3>(), ic<4>());
             if (nblk > 4) return live == 3 ? run(ic<3>(), ic<3>()) : run(ic<2>(), ic<3>());
         }
-        if (nblk > 2) return live == 2 ? run(ic<2>(), ic<2>()) : run(ic<1>(), ic<2>());
-        return live == 1 ? run(ic<1>(), ic<1>()) : run(ic<0>(), ic<1>());
-    } else if constexpr (S::NB == 2) {
-        return live == 2 ? run(ic<2>(), ic<1>()) : run(ic<1>(), ic<1>());
-    } else {  // four copies of 8 rows: the first four wavefronts
-        return wave < 4 ? run(ic<1>(), ic<1>()) : run(ic<1>(), ic<0>());
+        if constexpr (S::NB >= 2) {
+            if (nblk > 2) return live == 2 ? run(ic<2>(), ic<4 / RB>()) : run(ic<1>(), ic<4 / RB>());
+        }
+        return live == 1 ? run(ic<1>(), ic<2 / RB>()) : run(ic<0>(), ic<2 / RB>());
     }
 }
 
 // The ring's stages as separate objects: the compiler then knows that reading
 // one does not wait for the copies into another.
 #define F8_TILE_LDS(S)                                                                         \
-    __shared__ __attribute__((aligned(1024))) uint8_t W0[TWB];                                 \
-    __shared__ __attribute__((aligned(1024))) uint8_t W1[TWB];                                 \
-    __shared__ __attribute__((aligned(1024))) uint8_t W2[S::NST > 2 ? TWB : 16];               \
-    __shared__ __attribute__((aligned(1024))) uint8_t W3[S::NST > 3 ? TWB : 16];               \
+    __shared__ __attribute__((aligned(1024))) uint8_t W0[S::WB];                               \
+    __shared__ __attribute__((aligned(1024))) uint8_t W1[S::WB];                               \
+    __shared__ __attribute__((aligned(1024))) uint8_t W2[S::NST > 2 ? S::WB : 16];             \
+    __shared__ __attribute__((aligned(1024))) uint8_t W3[S::NST > 3 ? S::WB : 16];             \
     __shared__ __attribute__((aligned(1024))) uint8_t X0[S::XB];                               \
     __shared__ __attribute__((aligned(1024))) uint8_t X1[S::XB];                               \
     __shared__ __attribute__((aligned(1024))) uint8_t X2[S::NST > 2 ? S::XB : 16];             \
@@ -219,11 +306,7 @@ __device__ __forceinline__ void tile_run(const F8Tile<S>& g, int nrows, uint8_t*
 
 template <class S, bool WIDE, bool SPLIT>
 __device__ __forceinline__ void tile_go(const F8Tile<S>& g, int nrows, uint8_t* const (&WS)[4], uint8_t* const (&XS)[4],
-                                        f8_f16 (&acc)[S::NB][S::GM]) {
-#pragma unroll
-    for (int i = 0; i < S::NB; ++i)
-#pragma unroll
-        for (int j = 0; j < S::GM; ++j) acc[i][j] = f8_f16{};
+                                        f8_f16 (&acc)[S::NB][S::NJ]) {
     if constexpr (S::NST == 2) {
         uint8_t* const W[2] = {WS[0], WS[1]};
         uint8_t* const X[2] = {XS[0], XS[1]};
@@ -238,10 +321,12 @@ __device__ __forceinline__ void tile_go(const F8Tile<S>& g, int nrows, uint8_t* 
 }
 
 template <class S>
-__global__ __launch_bounds__(64 * TW) void f8_gateup_tile_kernel(F8Ffn a) {
-    constexpr int NB = S::NB, BM = S::BM, HC = S::WR / 2;  // h columns per wavefront
+__global__ __launch_bounds__(64 * S::W) void f8_gateup_tile_kernel(F8Ffn a) {
+    constexpr int NB = S::NB, BM = S::BM, HC = S::WR / 2, TW = S::W, TWC = S::WQ;  // h columns per wavefront
     F8_TILE_LDS(S);
-    __shared__ uint32_t red[S::GN][BM];
+    // per-row maxima of the wavefronts, over the first activation stage once the K loop is done
+    static_assert(S::GN * S::BM * 4 <= S::XB, "room for the maxima");
+    uint32_t(*red)[BM] = reinterpret_cast<uint32_t(*)[BM]>(X0);
     int tile, ntile;
     if (!work_item<4>(tile_count(a.f), tile, ntile)) return;
     TileRows tr;
@@ -256,12 +341,16 @@ __global__ __launch_bounds__(64 * TW) void f8_gateup_tile_kernel(F8Ffn a) {
     F8Tile<S> g;
     g.K = d;
     g.nst = f8_blocks(d);
-    // stage rows 2 HC m .. + HC - 1: gate rows n0 + HC m .., the HC rows after them: the same up rows
+    // stage rows 2 HC m .. + HC - 1: gate rows n0 + HC m .., the HC rows after
+    // them: the same up rows (a wavefront's copies are 64 rows apart: all of
+    // them gate, or all up)
+    static_assert(64 % (2 * HC) == 0 && TW == 8, "gate and up copies");
+    g.wbase = static_cast<const uint8_t*>((8 * wave & HC) ? U.q : G.q) + (e * F + n0) * d;
 #pragma unroll
     for (int q = 0; q < TWC; ++q) {
-        const int sr = copy_row(q * TW + wave, lane), n = min(n0 + HC * (sr / (2 * HC)) + sr % HC, F - 1);
-        g.wch = copy_chunk(sr, lane);
-        g.wsrc[q] = static_cast<const uint8_t*>((sr & HC) ? U.q : G.q) + (e * F + n) * d + g.wch;
+        const int r8 = 8 * (q * TW + wave), n = HC * (r8 / (2 * HC)) + r8 % HC + (lane >> 3);
+        g.ch = copy_chunk(r8 + (lane >> 3), lane);
+        g.woff[q] = (uint32_t)(min(n, F - 1 - n0) * d + g.ch);
     }
     auto token = [&](int r) {  // rows past the tile repeat its first; their results are not stored
         r = r < tr.nrows ? r : 0;
@@ -269,41 +358,43 @@ __global__ __launch_bounds__(64 * TW) void f8_gateup_tile_kernel(F8Ffn a) {
         const int f = a.f.perm_rows[tr.rbeg + r];
         return f >= 0 && f < a.f.T * a.f.k ? f / a.f.k : 0;
     };
+    g.xbase = a.xq;  // (T * d is below 2^32)
+    g.ebase = a.xe;
 #pragma unroll
-    for (int q = 0; q < S::XQ; ++q) {
-        const int sr = copy_row(q * TW + wave, lane);
-        g.xch = copy_chunk(sr, lane);
-        g.xsrc[q] = a.xq + (size_t)token(sr) * d + g.xch;
-    }
+    for (int q = 0; q < S::XQ; ++q) g.xoff[q] = (uint32_t)token(copy_row(q * TW + wave, lane)) * d + g.ch;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) g.ep[i] = a.xe + (size_t)token(32 * (mh + S::GM * i) + l32) * f8_scale_ld(d);
+    for (int i = 0; i < NB; ++i) g.eoff[i] = (uint32_t)token(32 * (mh + S::GM * i) + l32) * f8_scale_ld(d);
     const size_t srow = (e * f8_blocks(F) + ntile) * g.nst;
     g.sp[0] = reinterpret_cast<const float*>(G.scale) + srow;
     g.sp[1] = reinterpret_cast<const float*>(U.scale) + srow;
-    f8_f16 acc[NB][S::GM];
-    tile_go<S, false, S::GM == 1>(g, tr.nrows, WS, XS, acc);
+    f8_f16 acc[NB][S::NJ];
+    tile_go<S, false, S::NJ == 1>(g, tr.nrows, WS, XS, acc);
     // h and its largest magnitude per row over the tile's 128 columns
-    // (a wavefront of GM = 2 has gate and up in its two blocks, of GM = 1 in the
-    // lower and upper half of one)
+    // (a wavefront has gate and up in its two blocks, or in the lower and upper
+    // half of its one)
     constexpr int NV = HC / 2;  // h values per lane
     const int c0 = n0 + HC * wn;
     const bool in = c0 < F;  // (F is a multiple of 64)
-    float h[NB][NV];
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
+    __syncthreads();  // every wavefront has read its last stage
+    each<NB>([&](auto ii) {  // h takes the place of gate in acc[i][0]
+        constexpr int i = decltype(ii)::value;
+        const f8_f16 ga = acc[i][0], up = acc[i][S::NJ - 1];
+        f8_f16 h = ga;
         uint32_t m = 0;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            h[i][v] = silu_f32(acc[i][0][v]) * (S::GM == 2 ? acc[i][S::GM - 1][v] : acc[i][0][(v + NV) & 15]);
-            m = max(m, f8_abs_bits(h[i][v]));
+            h[v] = silu_f32(ga[v]) * up[S::NJ == 2 ? v : v + 8];
+            m = max(m, f8_abs_bits(h[v]));
         }
+        acc[i][0] = h;
         m = max(m, (uint32_t)__shfl_xor((int)m, 32));
         if (lane < 32) red[wn][32 * (mh + S::GM * i) + l32] = in ? m : 0u;
-    }
+    });
     __syncthreads();
     const int hi = lane >> 5;
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
+    each<NB>([&](auto ii) {
+        constexpr int i = decltype(ii)::value;
+        const f8_f16 h = acc[i][0];
         const int r = 32 * (mh + S::GM * i) + l32;
         uint32_t m = 0;
 #pragma unroll
@@ -313,12 +404,12 @@ __global__ __launch_bounds__(64 * TW) void f8_gateup_tile_kernel(F8Ffn a) {
         uint32_t c[NV / 4];
 #pragma unroll
         for (int j = 0; j < NV / 4; ++j)
-            c[j] = f8_pack4(h[i][4 * j], h[i][4 * j + 1], h[i][4 * j + 2], h[i][4 * j + 3], inv, byte);
+            c[j] = f8_pack4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3], inv, byte);
         // lanes l and l + 32 hold alternate 4-column runs of a row: each takes NV adjacent columns
         uint32_t o[NV / 8];
 #pragma unroll
         for (int j = 0; j < NV / 8; ++j) o[j] = (uint32_t)__shfl_xor((int)(hi ? c[j] : c[j + NV / 8]), 32);
-        if (r >= tr.nrows) continue;
+        if (r >= tr.nrows) return;
         const size_t hrow = (size_t)(tr.rbeg + r);
         uint8_t* dst = a.hq + hrow * a.f.ldh + c0 + NV * hi;
         if constexpr (NV == 16) {
@@ -327,12 +418,12 @@ __global__ __launch_bounds__(64 * TW) void f8_gateup_tile_kernel(F8Ffn a) {
             if (in) *reinterpret_cast<uint2*>(dst) = hi ? make_uint2(o[0], c[1]) : make_uint2(c[0], o[0]);
         }
         if (wn == 0 && hi == 0) a.he[hrow * f8_scale_ld(a.f.ldh) + ntile] = (uint8_t)byte;
-    }
+    });
 }
 
 template <class S>
-__global__ __launch_bounds__(64 * TW) void f8_down_tile_kernel(F8Ffn a) {
-    constexpr int NB = S::NB, BM = S::BM;
+__global__ __launch_bounds__(64 * S::W) void f8_down_tile_kernel(F8Ffn a) {
+    constexpr int NB = S::NB, BM = S::BM, TN = S::TN, TW = S::W, TWC = S::WQ;
     F8_TILE_LDS(S);
     int tile, ntile;
     if (!work_item<4>(tile_count(a.f), tile, ntile)) return;
@@ -349,54 +440,59 @@ __global__ __launch_bounds__(64 * TW) void f8_down_tile_kernel(F8Ffn a) {
 #pragma unroll
     for (int q = 0; q < TWC; ++q) {
         const int sr = copy_row(q * TW + wave, lane);
-        g.wch = copy_chunk(sr, lane);
-        g.wsrc[q] = static_cast<const uint8_t*>(D.q) + (e * d + min(n0 + sr, d - 1)) * F + g.wch;
+        g.ch = copy_chunk(sr, lane);
+        g.woff[q] = (uint32_t)(min(sr, d - 1 - n0) * F + g.ch);
     }
+    g.wbase = static_cast<const uint8_t*>(D.q) + (e * d + n0) * F;
+    g.xbase = a.hq + (size_t)tr.rbeg * a.f.ldh;
+    g.ebase = a.he + (size_t)tr.rbeg * f8_scale_ld(a.f.ldh);
 #pragma unroll
     for (int q = 0; q < S::XQ; ++q) {
         const int sr = copy_row(q * TW + wave, lane);
-        g.xch = copy_chunk(sr, lane);
-        g.xsrc[q] = a.hq + (size_t)(tr.rbeg + (sr < tr.nrows ? sr : 0)) * a.f.ldh + g.xch;
+        g.xoff[q] = (uint32_t)((sr < tr.nrows ? sr : 0) * a.f.ldh + g.ch);
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
         const int r = 32 * (mh + S::GM * i) + l32;
-        g.ep[i] = a.he + (size_t)(tr.rbeg + (r < tr.nrows ? r : 0)) * f8_scale_ld(a.f.ldh);
+        g.eoff[i] = (uint32_t)((r < tr.nrows ? r : 0) * f8_scale_ld(a.f.ldh));
     }
     const int c0 = n0 + S::WR * wn;
 #pragma unroll
     for (int j = 0; j < 2; ++j)  // (one block: both the same)
         g.sp[j] = reinterpret_cast<const float*>(D.scale) + (e * f8_blocks(d) + min(c0 + 32 * j % S::WR, d - 1) / F8_BLK) * g.nst;
-    f8_f16 acc[NB][S::GM];
+    f8_f16 acc[NB][S::NJ];
     tile_go<S, false, false>(g, tr.nrows, WS, XS, acc);
+    // (stores that the caches join: a lane's 16 bytes are an eighth of a cache
+    // line, and written past the caches the 4096-token case took 1.64 ms, not 1.08)
     float* out = shared ? a.f.shared_out : a.f.slot_out;
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
+    each<NB>([&](auto ii) {
+        constexpr int i = decltype(ii)::value;
         const int r = 32 * (mh + S::GM * i) + l32;
-        if (r >= tr.nrows) continue;
+        if (r >= tr.nrows) return;
         int dst = tr.rbeg - a.f.T * a.f.k + r;
         float w = 1.0f;
         if (!shared) {
             dst = a.f.perm_rows[tr.rbeg + r];
-            if (dst < 0 || dst >= a.f.T * a.f.k) continue;
+            if (dst < 0 || dst >= a.f.T * a.f.k) return;
             w = a.f.topk_w[dst];
         }
-#pragma unroll
-        for (int j = 0; j < S::GM; ++j)
+        each<S::NJ>([&](auto jj) {
+            constexpr int j = decltype(jj)::value;
+            const f8_f16 p = acc[i][j] * w;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int c = c0 + 32 * j + 8 * q + 4 * (lane >> 5);
-                const f8_f16& p = acc[i][j];
                 if (c < d)
-                    st_stream16(out + (size_t)dst * d + c,
-                                make_float4(w * p[4 * q], w * p[4 * q + 1], w * p[4 * q + 2], w * p[4 * q + 3]));
+                    *reinterpret_cast<float4*>(out + (size_t)dst * d + c) =
+                        make_float4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
             }
-    }
+        });
+    });
 }
 
 template <class S, int OF>
-__global__ __launch_bounds__(64 * TW) void f8_dense_tile_kernel(BlockArgs a) {
-    constexpr int NB = S::NB, BM = S::BM;
+__global__ __launch_bounds__(64 * S::W) void f8_dense_tile_kernel(BlockArgs a) {
+    constexpr int NB = S::NB, BM = S::BM, TN = S::TN, TW = S::W, TWC = S::WQ;
     F8_TILE_LDS(S);
     // consecutive workgroups go to the 8 XCDs in turn: give each a contiguous
     // range of the tiles, walked in groups of 4 weight tiles (gemm_dev.h)
@@ -412,37 +508,38 @@ __global__ __launch_bounds__(64 * TW) void f8_dense_tile_kernel(BlockArgs a) {
 #pragma unroll
     for (int q = 0; q < TWC; ++q) {
         const int sr = copy_row(q * TW + wave, lane);
-        g.wch = copy_chunk(sr, lane);
-        g.wsrc[q] = a.wq + (size_t)min(n0 + sr, a.n - 1) * a.k + g.wch;
+        g.ch = copy_chunk(sr, lane);
+        g.woff[q] = (uint32_t)(min(sr, a.n - 1 - n0) * a.k + g.ch);
     }
+    g.wbase = a.wq + (size_t)n0 * a.k;
+    g.xbase = a.xq + (size_t)m0 * a.k;
+    g.ebase = a.xe + (size_t)m0 * f8_scale_ld(a.k);
 #pragma unroll
-    for (int q = 0; q < S::XQ; ++q) {
-        const int sr = copy_row(q * TW + wave, lane);
-        g.xch = copy_chunk(sr, lane);
-        g.xsrc[q] = a.xq + (size_t)(m0 + min(sr, nrows - 1)) * a.k + g.xch;
-    }
+    for (int q = 0; q < S::XQ; ++q) g.xoff[q] = (uint32_t)(min(copy_row(q * TW + wave, lane), nrows - 1) * a.k + g.ch);
 #pragma unroll
     for (int i = 0; i < NB; ++i)
-        g.ep[i] = a.xe + (size_t)(m0 + min(32 * (mh + S::GM * i) + l32, nrows - 1)) * f8_scale_ld(a.k);
+        g.eoff[i] = (uint32_t)(min(32 * (mh + S::GM * i) + l32, nrows - 1) * f8_scale_ld(a.k));
     const int c0 = n0 + S::WR * wn;
 #pragma unroll
     for (int j = 0; j < 2; ++j) g.sp[j] = a.ws + (size_t)(min(c0 + 32 * j % S::WR, a.n - 1) / F8_BLK) * g.nst;
-    f8_f16 acc[NB][S::GM];
+    f8_f16 acc[NB][S::NJ];
     tile_go<S, OF == MOE_DT_F32, false>(g, nrows, WS, XS, acc);
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
+    each<NB>([&](auto ii) {
+        constexpr int i = decltype(ii)::value;
         const int r = 32 * (mh + S::GM * i) + l32;
-        if (r >= nrows) continue;
-#pragma unroll
-        for (int j = 0; j < S::GM; ++j)
+        if (r >= nrows) return;
+        each<S::NJ>([&](auto jj) {
+            constexpr int j = decltype(jj)::value;
+            const f8_f16 p = acc[i][j];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int c = c0 + 32 * j + 8 * q + 4 * (lane >> 5);
                 if (c >= a.n) continue;
-                const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                const float v[4] = {p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]};
                 f8_store4<OF>(a.out, (size_t)(m0 + r) * a.n + c, a.n - c, v, a.n % 4 == 0);
             }
-    }
+        });
+    });
 }
 
 }  // namespace
@@ -450,31 +547,42 @@ __global__ __launch_bounds__(64 * TW) void f8_dense_tile_kernel(BlockArgs a) {
 hipError_t launch_f8_gateup(const F8Ffn& a, hipStream_t st, const KTime& kt) {
     const int fmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F;
     const dim3 grid(a.f.max_tiles, f8_blocks(fmax));
-    if (a.f.bm == 32) launch_kernel(f8_gateup_tile_kernel<Rows32>, grid, 64 * TW, st, kt, a);
-    else if (a.f.bm == 64) launch_kernel(f8_gateup_tile_kernel<Rows64>, grid, 64 * TW, st, kt, a);
-    else if (a.f.bm == 128) launch_kernel(f8_gateup_tile_kernel<Rows128>, grid, 64 * TW, st, kt, a);
-    else launch_kernel(f8_gateup_tile_kernel<Rows256>, grid, 64 * TW, st, kt, a);
+    if (a.f.bm == 64) launch_kernel(f8_gateup_tile_kernel<Rows64>, grid, 64 * Rows64::W, st, kt, a);
+    else launch_kernel(f8_gateup_tile_kernel<Rows256>, grid, 64 * Rows256::W, st, kt, a);
     return hipGetLastError();
 }
 
 hipError_t launch_f8_down(const F8Ffn& a, hipStream_t st, const KTime& kt) {
-    const dim3 grid(a.f.max_tiles, (a.f.d + TN - 1) / TN);
-    if (a.f.bm == 32) launch_kernel(f8_down_tile_kernel<Rows32>, grid, 64 * TW, st, kt, a);
-    else if (a.f.bm == 64) launch_kernel(f8_down_tile_kernel<Rows64>, grid, 64 * TW, st, kt, a);
-    else if (a.f.bm == 128) launch_kernel(f8_down_tile_kernel<Rows128>, grid, 64 * TW, st, kt, a);
-    else launch_kernel(f8_down_tile_kernel<Rows256>, grid, 64 * TW, st, kt, a);
+    static_assert(Rows64::TN == Rows256::TN, "one grid");
+    const dim3 grid(a.f.max_tiles, (a.f.d + Rows64::TN - 1) / Rows64::TN);
+    if (a.f.bm == 64) launch_kernel(f8_down_tile_kernel<Rows64>, grid, 64 * Rows64::W, st, kt, a);
+    else launch_kernel(f8_down_tile_kernel<Rows256>, grid, 64 * Rows256::W, st, kt, a);
     return hipGetLastError();
 }
 
+template <class S, int OF>
+static void dense_tile_launch(const BlockArgs& a, hipStream_t st) {
+    const dim3 grid((a.m + S::BM - 1) / S::BM, (a.n + S::TN - 1) / S::TN);
+    f8_dense_tile_kernel<S, OF><<<grid, 64 * S::W, 0, st>>>(a);
+}
+template <class S>
+static void dense_tile_launch_out(const BlockArgs& a, hipStream_t st) {
+    if (a.odt == MOE_DT_F32) dense_tile_launch<S, MOE_DT_F32>(a, st);
+    else dense_tile_launch<S, MOE_DT_BF16>(a, st);
+}
+
+// The largest tiles that still give most compute units one (us, 256 x 256 /
+// 128 x 128 / 64 x 64 tiles, bf16 results; n x k 4096 x 6144: 300 rows 93 / 41 /
+// 25, 1000 rows 94 / 44 / 50, 4096 rows 118 / 124 / 199; 4096 x 2048: 2048 rows
+// 40 / 26 / 41; 700 x 1024: 4096 rows 24 / 12.2 / 12.9).  fp32 results double
+// the matrix work: 128 x 256 tiles pay from 256 of them (2048 rows of 4096 x
+// 2048 46 against 54 us for 128 x 128).
 hipError_t launch_block_matmul_tile(const BlockArgs& a, hipStream_t st) {
-    const int nt = (a.n + TN - 1) / TN;
-    if (a.odt == MOE_DT_F32) {
-        f8_dense_tile_kernel<Rows128, MOE_DT_F32><<<dim3((a.m + 127) / 128, nt), 64 * TW, 0, st>>>(a);
-    } else if ((long)((a.m + 255) / 256) * nt >= 192) {
-        f8_dense_tile_kernel<Rows256, MOE_DT_BF16><<<dim3((a.m + 255) / 256, nt), 64 * TW, 0, st>>>(a);
-    } else {
-        f8_dense_tile_kernel<Rows128, MOE_DT_BF16><<<dim3((a.m + 127) / 128, nt), 64 * TW, 0, st>>>(a);
-    }
+    auto tiles = [&](int bm, int tn) { return (long)((a.m + bm - 1) / bm) * ((a.n + tn - 1) / tn); };
+    if (a.odt == MOE_DT_F32 && tiles(128, 256) >= 256) dense_tile_launch<Rows128, MOE_DT_F32>(a, st);
+    else if (a.odt == MOE_DT_BF16 && tiles(256, 256) >= 192) dense_tile_launch<Rows256, MOE_DT_BF16>(a, st);
+    else if (tiles(128, 128) >= 192) dense_tile_launch_out<Square128>(a, st);
+    else dense_tile_launch_out<Square64>(a, st);
     return hipGetLastError();
 }
 
