@@ -123,8 +123,10 @@ typedef struct {
  * projection, 5 combine.  The decode path (n_tokens <= MOE_DECODE_MAX_TOKENS)
  * builds the permutation inside the selection kernel and the combine inside
  * the down kernel: it launches no kernel for stages 2 and 5 and leaves their
- * events unrecorded (F8B128 layers run the same launches at every n_tokens,
- * stages 2 and 5 included; the quantisation of x counts to stage 3). */
+ * events unrecorded.  F8B128 layers have one path: stages 0 to 5 at every
+ * n_tokens, but up to 16 tokens stage 1 includes the permutation (stage 2's
+ * events stay unrecorded), and the quantisation of x is in stage 1 there and
+ * in none beyond. */
 #define MOE_STAGES 6
 #define MOE_STAGE_EVENTS (2 * MOE_STAGES)
 

@@ -249,15 +249,16 @@ hipError_t run_bf16_experts(const FfnArgs& f, hipStream_t st, const KTime& kg = 
     return launch_down_mfma(f, st, kd);
 }
 
-// e4m3 experts: x quantised once per token, then gate/up (which quantises h)
-// and down.
+// e4m3 experts over the quantised rows of x: gate/up (which quantises h), down.
+QuantArgs f8_quant_args(const moe_config* c, const Layout& L, void* ws, const void* x) {
+    return QuantArgs{x, MOE_DT_BF16, c->n_tokens, c->d_model, c->d_model, at<uint8_t>(ws, L.xq), at<uint8_t>(ws, L.xe)};
+}
+
 hipError_t run_f8_experts(const FfnArgs& f, const Layout& L, void* ws, hipStream_t st, const KTime& kg = KTime(),
                           const KTime& kd = KTime()) {
-    F8Ffn a{f, at<uint8_t>(ws, L.xq), at<uint8_t>(ws, L.xe), at<uint8_t>(ws, L.hq), at<uint8_t>(ws, L.he)};
-    hipError_t e = launch_quantize_rows(QuantArgs{f.x, MOE_DT_BF16, f.T, f.d, f.d, a.xq, a.xe}, st, kg.first());
-    if (e != hipSuccess) return e;
-    if ((e = launch_f8_gateup(a, st, kg.last())) != hipSuccess) return e;
-    return launch_f8_down(a, st, kd);
+    const F8Ffn a{f, at<uint8_t>(ws, L.xq), at<uint8_t>(ws, L.xe), at<uint8_t>(ws, L.hq), at<uint8_t>(ws, L.he)};
+    const hipError_t e = launch_f8_gateup(a, st, kg);
+    return e == hipSuccess ? launch_f8_down(a, st, kd) : e;
 }
 
 hipError_t run_expert_kernels(const FfnArgs& f, const Layout& L, void* ws, hipStream_t st,
@@ -576,6 +577,7 @@ int moe_expert_ffn(const moe_config* cfg, const void* x, const moe_weights* w, c
     FfnArgs f = ffn_args(cfg, L, ws, x, w, offsets, perm_rows, topk_w);
     f.slot_out = slot_out;
     f.shared_out = cfg->n_shared ? shared_out : nullptr;
+    if (f.wdt == MOE_DT_F8B128 && launch_quantize_rows(f8_quant_args(cfg, L, ws, x), st) != hipSuccess) return MOE_ERR_DEVICE;
     return device_status(run_expert_kernels(f, L, ws, st));
 }
 
@@ -654,9 +656,20 @@ int enqueue_layer(const moe_config* cfg, const GroupArgs& g, const void* x, cons
         dr.grouped = is_grouped(cfg, g);
         return device_status(launch_decode(dr, kt, st));
     }
-    hipError_t e = launch_router_logits(r, st, kt[0]);
-    if (e == hipSuccess) e = run_select(cfg, g, select_args(cfg, logits, w->bias, idx, wts), st, kt[1]);
-    if (e == hipSuccess) e = launch_permute(perm_args(cfg, L, ws, idx, off, perm, inv), st, kt[2]);
+    const SelectArgs sel = select_args(cfg, logits, w->bias, idx, wts);
+    const PermArgs pa = perm_args(cfg, L, ws, idx, off, perm, inv);
+    const bool f8 = cfg->w_dtype == MOE_DT_F8B128;
+    hipError_t e;
+    if (f8 && cfg->n_tokens <= F8_ROUTE_MAX_T) {
+        e = launch_f8_router(r, st, kt[0]);
+        if (e == hipSuccess)
+            e = launch_f8_route(sel, g, is_grouped(cfg, g), pa, f8_quant_args(cfg, L, ws, x), st, kt[1]);
+    } else {
+        e = launch_router_logits(r, st, kt[0]);
+        if (e == hipSuccess) e = run_select(cfg, g, sel, st, kt[1]);
+        if (e == hipSuccess) e = launch_permute(pa, st, kt[2]);
+        if (e == hipSuccess && f8) e = launch_quantize_rows(f8_quant_args(cfg, L, ws, x), st);
+    }
     if (e != hipSuccess) return MOE_ERR_DEVICE;
     FfnArgs f = ffn_args(cfg, L, ws, x, w, off, perm, wts);
     e = run_expert_kernels(f, L, ws, st, kt[3], kt[4]);

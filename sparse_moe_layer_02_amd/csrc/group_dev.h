@@ -10,7 +10,14 @@
 //
 // Lane l holds experts l, l + 64, ... as route_dev.h's selection does, and
 // the k rounds are the same.  The group scores need a group's keys side by
-// side: the wavefront lays its keys out in LDS and lane g scans group g.
+// side: the wavefront lays its keys out in LDS and as many lanes as there are
+// for each group scan it together.
+//
+// Bound by instruction issue: a wavefront per token, 64 of them in turn on each
+// SIMD for 65536 tokens (256 experts, 8 groups, top-8: 96 us with the library
+// exponential and division and one lane scanning each group, 80 us here, about
+// 600 vector instructions a token; a bitwise search for the k-th key over
+// ballots in place of the k rounds took as many).
 #pragma once
 #include "common.h"
 #include "kernels.h"
@@ -24,6 +31,36 @@ namespace moe {
 __device__ __forceinline__ float unpack_ord(uint32_t ord) {
     if (ord == 0u) return __uint_as_float(0x7FC00000u);
     return __uint_as_float((ord & 0x80000000u) ? ord & 0x7FFFFFFFu : ~ord);
+}
+
+// e^x for |x| up to 708 (further out: as at 708) to about one unit in the last
+// place: x = n ln2 + r, the Taylor series of e^r to r^12 (|r| <= ln2 / 2: the next
+// term is below 2^-52), scaled by 2^n.  NaN is the caller's.
+__device__ __forceinline__ double exp_f64(double x) {
+    x = fmin(fmax(x, -708.0), 708.0);
+    const double n = rint(x * 1.4426950408889634);
+    double r = __fma_rn(-n, 0x1.62e42fefa39efp-1, x);  // ln2 in two parts; the fused product is exact
+    r = __fma_rn(-n, 0x1.abc9e3b39803fp-56, r);
+    double p = 1.0 / 479001600.0;
+    p = __fma_rn(p, r, 1.0 / 39916800.0);
+    p = __fma_rn(p, r, 1.0 / 3628800.0);
+    p = __fma_rn(p, r, 1.0 / 362880.0);
+    p = __fma_rn(p, r, 1.0 / 40320.0);
+    p = __fma_rn(p, r, 1.0 / 5040.0);
+    p = __fma_rn(p, r, 1.0 / 720.0);
+    p = __fma_rn(p, r, 1.0 / 120.0);
+    p = __fma_rn(p, r, 1.0 / 24.0);
+    p = __fma_rn(p, r, 1.0 / 6.0);
+    p = __fma_rn(p, r, 0.5);
+    p = __fma_rn(p, r, 1.0);
+    p = __fma_rn(p, r, 1.0);
+    return ldexp(p, (int)n);
+}
+// 1 / d for finite normal d: the hardware's estimate and two Newton steps.
+__device__ __forceinline__ double rcp_f64(double d) {
+    double r = __builtin_amdgcn_rcp(d);
+    r = __fma_rn(__fma_rn(-d, r, 1.0), r, r);
+    return __fma_rn(__fma_rn(-d, r, 1.0), r, r);
 }
 
 // keys: E words of LDS of this wavefront's own.  Returns the expert of rank
@@ -50,12 +87,20 @@ __device__ __forceinline__ int group_topk_token(const float* __restrict__ lrow, 
         double ex[KPL], sum = 0.0;
 #pragma unroll
         for (int j = 0; j < KPL; ++j) {
-            ex[j] = lane + WAVE * j < E ? exp((double)sc[j] - (double)m) : 0.0;
+            const double x = (double)sc[j] - (double)m;  // NaN for a NaN logit, and for all if m is infinite
+            ex[j] = lane + WAVE * j < E ? (x != x ? x : exp_f64(x)) : 0.0;
             sum += ex[j];
         }
         sum = wave_sum_f64(sum);
+        const double inv = sum != sum ? sum : rcp_f64(sum);  // sum >= 1
 #pragma unroll
-        for (int j = 0; j < KPL; ++j) sc[j] = (float)(ex[j] / sum);
+        for (int j = 0; j < KPL; ++j) sc[j] = (float)(ex[j] * inv);
+    } else if (score_kind == MOE_SCORE_SIGMOID) {
+#pragma unroll
+        for (int j = 0; j < KPL; ++j) {
+            const float s = (float)rcp_f64(1.0 + exp_f64(-(double)sc[j]));
+            sc[j] = sc[j] != sc[j] ? sc[j] : s;
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < KPL; ++j) sc[j] = router_score(score_kind, sc[j]);
@@ -72,31 +117,39 @@ __device__ __forceinline__ int group_topk_token(const float* __restrict__ lrow, 
             if (lane + WAVE * j < E) keys[lane + WAVE * j] = (uint32_t)(key[j] >> 32);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the wavefront's own writes before its reads
         __builtin_amdgcn_wave_barrier();
-        uint64_t mine = 0;  // group `lane`: orderable score, then the lower index
-        if (lane < g.n_group) {
-            uint32_t b0 = 0, b1 = 0;
-            int s = lane % S;  // staggered starts: the lanes' reads spread over the banks
-            for (int i = 0; i < S; ++i) {
-                const uint32_t v = keys[lane * S + s];
+        // lpg lanes (a power of two) scan each group: lane g lpg + i its keys i, i + lpg, ...
+        int lpg = 1;
+        while (2 * lpg * g.n_group <= WAVE) lpg *= 2;
+        const int grp_l = lane / lpg;
+        uint32_t b0 = 0, b1 = 0;
+        if (grp_l < g.n_group) {
+            const uint32_t* kg = keys + grp_l * S;
+            for (int i = lane % lpg; i < S; i += lpg) {
+                const uint32_t v = kg[i];
                 b1 = max(b1, min(b0, v));
                 b0 = max(b0, v);
-                s = s + 1 == S ? 0 : s + 1;
             }
-            const float best = unpack_ord(b0);
-            mine = pack_key(g.group_top == 2 && S > 1 ? best + unpack_ord(b1) : best, lane);
         }
+        for (int o = 1; o < lpg; o *= 2) {
+            const uint32_t c0 = (uint32_t)__shfl_xor((int)b0, o), c1 = (uint32_t)__shfl_xor((int)b1, o);
+            b1 = max(min(b0, c0), max(b1, c1));
+            b0 = max(b0, c0);
+        }
+        const float best = unpack_ord(b0);
+        const uint64_t mine =  // orderable score, then the lower group
+            grp_l < g.n_group ? pack_key(g.group_top == 2 && S > 1 ? best + unpack_ord(b1) : best, grp_l) : 0ull;
         int rank = 0;
         for (int q = 0; q < g.n_group; ++q) {
-            const uint64_t o = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(mine >> 32), q) << 32) |
-                               (uint32_t)__builtin_amdgcn_readlane((uint32_t)mine, q);
+            const uint64_t o = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(mine >> 32), q * lpg) << 32) |
+                               (uint32_t)__builtin_amdgcn_readlane((uint32_t)mine, q * lpg);
             rank += o > mine;
         }
-        const uint64_t keep = __ballot(lane < g.n_group && rank < g.topk_group);
+        const uint64_t keep = __ballot(grp_l < g.n_group && rank < g.topk_group);
 #pragma unroll
         for (int j = 0; j < KPL; ++j) {
             const int e = lane + WAVE * j;
             const int grp = (int)(((float)e + 0.5f) * g.inv_size);  // e / S (exact: E <= 1024)
-            if (e < E && !((keep >> grp) & 1)) key[j] = 0ull;
+            if (e < E && !((keep >> (grp * lpg)) & 1)) key[j] = 0ull;
         }
     }
     // descending within the lane, then k rounds of wave maxima (route_dev.h)

@@ -163,6 +163,12 @@ struct F8Ffn {
     uint8_t *xq, *xe;        // [T, d], [T, f8_scale_ld(d)]
     uint8_t *hq, *he;        // [T*k + T*n_shared, ldh], [.., f8_scale_ld(ldh)]
 };
+// Selection, grouping and quantisation of x (bf16) in one launch, for up to
+// F8_ROUTE_MAX_T tokens.
+constexpr int F8_ROUTE_MAX_T = 16;
+hipError_t launch_f8_router(const RouteArgs& a, hipStream_t st, const KTime& kt = KTime());  // their logits (bf16 x)
+hipError_t launch_f8_route(const SelectArgs& s, const GroupArgs& g, bool grouped, const PermArgs& p, const QuantArgs& q,
+                           hipStream_t st, const KTime& kt = KTime());
 hipError_t launch_f8_gateup(const F8Ffn& a, hipStream_t st, const KTime& kt = KTime());
 hipError_t launch_f8_down(const F8Ffn& a, hipStream_t st, const KTime& kt = KTime());
 

@@ -319,6 +319,8 @@ def test_layer(dev, spec):
         torch.cuda.synchronize()
         assert (y[T] == 77.0).all()
         ys.append(y[:T].double().cpu().numpy())
+    want = (L["x"].double() @ torch.from_numpy(L["wr"]).double().t()).float().numpy()
+    assert H.ulp_diff_f32(lg.cpu().numpy(), want).max() <= 1  # one rounding of an fp64 sum
     ref_idx, _ = R.select(lg.cpu().numpy(), L["bias"], k, "sigmoid", 1.5)
     assert np.array_equal(idx.cpu().numpy(), ref_idx)
     ref, err = layer_ref(L, ref_idx, w.cpu().numpy(), n_shared)
