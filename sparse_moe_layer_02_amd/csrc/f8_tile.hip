@@ -74,6 +74,13 @@ struct F8Tile {
     const float* sp[2];           // block scales of the wavefront's weight rows (gate/up: of gate, of up)
     int K, nst;
 };
+// A wave-uniform pointer in scalar registers (where the compiler cannot see it).
+template <class P>
+__device__ __forceinline__ const P* uniform_ptr(const P* p) {
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u), hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
+    return reinterpret_cast<const P*>(((uint64_t)hi << 32) | lo);
+}
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_buffer(const uint8_t* p) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, 0xFFFFFFFF, 0x00020000);
 }
@@ -126,6 +133,11 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
     const int wave = wave_index(), mh = wave / S::GN, wn = wave % S::GN;
     const F8Lane fl = tile_lane(lane_id());
     constexpr int NC = TWC + XC;
+    g.wbase = uniform_ptr(g.wbase);
+    g.xbase = uniform_ptr(g.xbase);
+    g.ebase = uniform_ptr(g.ebase);
+    g.sp[0] = uniform_ptr(g.sp[0]);
+    g.sp[1] = uniform_ptr(g.sp[1]);
     const int nfull = g.K / F8_BLK, last = nfull - 1;  // whole stages
     // (opaque: single registers, not parts of vectors or of 64-bit values)
 #pragma unroll
@@ -157,7 +169,7 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
 #pragma unroll
         for (int j = 0; j < 2; ++j) sn[j] = g.sp[j][min(kb + lane_id(), g.nst - 1)];
     };
-    scales(0);
+    if constexpr (NB * NJ < 8) scales(0);
     f8_f16 acc[NB][NJ];
     each<NB * NJ>([&](auto b) { acc[decltype(b)::value / NJ][decltype(b)::value % NJ] = f8_f16{}; });
     // the products of LDS stage B; byte SEL of ev scales the activation rows,
@@ -208,30 +220,107 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
                 const f8_f16 s = f8_f16{a, a, a, a, a, a, a, a, b, b, b, b, b, b, b, b};
                 acc[i][j] = __builtin_elementwise_fma(s, p, acc[i][j]);
             });
-            if constexpr (NB * NJ == 8) pin();  // (more blocks' sums in flight than the registers hold, otherwise)
         });
         wait_lgkm0();  // this stage's reads are done before the next barrier releases its refill
+    };
+    // The same for the largest shape, in a fixed order: a block's products are
+    // issued before the FMAs of the block before it, which then run beside the
+    // matrix unit; the last block of a stage waits for the first products of the
+    // next; the copies go out behind the first products.  (Its registers are
+    // all taken: left to the compiler the sums of several blocks are in flight
+    // at once and offsets are reloaded from scratch memory behind the copies;
+    // 4096 x 4096 x 6144 131 us, in this order 106.)
+    constexpr bool PIPE = NB * NJ == 8;
+    f8_f16 pend = f8_f16{};
+    float q0 = 0.0f, q1 = 0.0f, t0 = 0.0f, t1 = 0.0f;  // scales of the block that waits, of the next stage
+    if constexpr (PIPE) {
+        t0 = f8_uniform(g.sp[0], 0);
+        t1 = f8_uniform(g.sp[1], 0);
+    }
+    auto retire = [&](auto bb, float s0, float s1) {  // block b = i NJ + j
+        constexpr int i = decltype(bb)::value / NJ, j = decltype(bb)::value % NJ;
+        const float a = j > 0 ? s1 : s0;
+        const f8_f16 s = f8_f16{a, a, a, a, a, a, a, a, a, a, a, a, a, a, a, a};
+        acc[i][j] = __builtin_elementwise_fma(s, pend, acc[i][j]);
+    };
+    auto products_pipe = [&](auto bb, auto ss, auto more, int kb) {
+        constexpr int B = decltype(bb)::value, SEL = decltype(ss)::value;
+        constexpr bool MORE = decltype(more)::value != 0;  // a stage of the loop, which sends for a later one
+        static_assert(!PIPE || (!WIDE && !SPLIT), "the largest shape");
+        uint32_t wo = S::WR * wn * F8_BLK, xo = 32 * mh * F8_BLK;
+        __asm__ volatile("" : "+s"(wo), "+s"(xo));
+        F8Row w[NJ][2], x[2];
+        each<2>([&](auto hh) {  // in the order of use
+            constexpr int h = decltype(hh)::value;
+            w[0][h] = tile_row(W[B], fl, wo, h);
+            x[h] = tile_row(X[B], fl, xo, h);
+        });
+        each<2 * (NJ - 1)>([&](auto q) {
+            constexpr int j = 1 + decltype(q)::value / 2, h = decltype(q)::value % 2;
+            w[j][h] = tile_row(W[B] + 32 * j * F8_BLK, fl, wo, h);
+        });
+        if constexpr (MORE && SEL == 0) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) ev[i] = en[i];
+        }
+        const float s0 = t0, s1 = t1;
+        each<L * NJ>([&](auto b2) {
+            constexpr int b = decltype(b2)::value, i = b / NJ, j = b % NJ;
+            f8_f16 p = f8_mfma32<SEL>(f8_join(w[j][0].a, w[j][0].b), f8_join(x[0].a, x[0].b), f8_f16{}, ev[i]);
+            p = f8_mfma32<SEL>(f8_join(w[j][1].a, w[j][1].b), f8_join(x[1].a, x[1].b), p, ev[i]);
+            pin();
+            if constexpr (j == NJ - 1 && i + 1 < L) {  // the next activation block's rows
+                x[0] = tile_row(X[B] + 32 * S::GM * (i + 1) * F8_BLK, fl, xo, 0);
+                x[1] = tile_row(X[B] + 32 * S::GM * (i + 1) * F8_BLK, fl, xo, 1);
+            }
+            if constexpr (b == 0) {
+                if constexpr (MORE) issue(W[(B + NST - 1) % NST], X[(B + NST - 1) % NST], kb + NST - 1);
+                retire(ic<(L > 0 ? L * NJ - 1 : 0)>(), q0, q1);
+                if constexpr (MORE) {
+                    t0 = f8_uniform(g.sp[0], min(kb + 1, g.nst - 1));
+                    t1 = f8_uniform(g.sp[1], min(kb + 1, g.nst - 1));
+                    if constexpr (SEL == 0) {
+#pragma unroll
+                        for (int t = 0; t < L; ++t)
+                            en[t] = __builtin_amdgcn_raw_buffer_load_b32(er, (int)g.eoff[t], kb + 4 < g.nst ? kb + 4 : 0, 0);
+                    }
+                }
+            } else {
+                retire(ic<(b > 0 ? b - 1 : 0)>(), s0, s1);
+            }
+            pin();
+            pend = p;
+        });
+        q0 = s0;
+        q1 = s1;
+        wait_lgkm0();
     };
     auto stage = [&](auto nn, int kb) {
         constexpr int n = decltype(nn)::value, B = n % NST, SEL = n % 4;
         wait_vm<(NST - 2) * NC>();
         barrier_nofence();
-        issue(W[(B + NST - 1) % NST], X[(B + NST - 1) % NST], kb + NST - 1);
-        if constexpr (SEL == 0) {
+        if constexpr (PIPE && L > 0) {
+            products_pipe(ic<B>(), ic<SEL>(), ic<1>(), kb);
+        } else {
+            issue(W[(B + NST - 1) % NST], X[(B + NST - 1) % NST], kb + NST - 1);
+            if constexpr (SEL == 0) {
 #pragma unroll
-            for (int i = 0; i < L; ++i) {
-                ev[i] = en[i];
-                en[i] = __builtin_amdgcn_raw_buffer_load_b32(er, (int)g.eoff[i], kb + 4 < g.nst ? kb + 4 : 0, 0);
+                for (int i = 0; i < L; ++i) {
+                    ev[i] = en[i];
+                    en[i] = __builtin_amdgcn_raw_buffer_load_b32(er, (int)g.eoff[i], kb + 4 < g.nst ? kb + 4 : 0, 0);
+                }
             }
+            if constexpr (L > 0) products(ic<B>(), ic<SEL>(), nn);
         }
-        if constexpr (L > 0) products(ic<B>(), ic<SEL>(), nn);
     };
     // twelve (four) stages run through every pair of LDS stage and scale byte
     constexpr int CYC = NST == 3 ? 12 : 4;
     for (int kb = 0; kb < nfull; kb += CYC) {
-        sl[0] = sn[0];
-        sl[1] = sn[1];
-        scales(kb + CYC);
+        if constexpr (!PIPE) {
+            sl[0] = sn[0];
+            sl[1] = sn[1];
+            scales(kb + CYC);
+        }
 #define F8_STAGE(n) \
     if constexpr (n < CYC) { if (kb + n < nfull) stage(ic<n>(), kb + n); }
         F8_STAGE(0) F8_STAGE(1) F8_STAGE(2) F8_STAGE(3) F8_STAGE(4) F8_STAGE(5)
@@ -256,12 +345,15 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         for (int i = 0; i < L; ++i) ev[i] = __builtin_amdgcn_raw_buffer_load_b8(er, (int)g.eoff[i], nfull, 0);
         wait_vm<0>();
         barrier_nofence();
-        if constexpr (L > 0) {
+        if constexpr (PIPE && L > 0) {
+            products_pipe(ic<0>(), ic<0>(), ic<0>(), nfull);
+        } else if constexpr (L > 0) {
             sl[0] = g.sp[0][nfull];
             sl[1] = g.sp[1][nfull];
             products(ic<0>(), ic<0>(), ic<0>());
         }
     }
+    if constexpr (PIPE && L > 0) retire(ic<(L > 0 ? L * NJ - 1 : 0)>(), q0, q1);
     wait_vm<0>();  // no copy may still be writing LDS when the workgroup ends
     each<NB * NJ>([&](auto b) {
         constexpr int i = decltype(b)::value / NJ, j = decltype(b)::value % NJ;
