@@ -124,9 +124,8 @@ __device__ __forceinline__ void each(F f) {
 }
 
 // The K loop of one wavefront with L live blocks and XC activation copies per
-// stage; acc[i][j]: block i (activation rows) x weight row block j.  SPLIT: the
-// wavefront's one weight block holds 16 gate rows and 16 up rows.
-template <class S, int L, int XC, bool WIDE, bool SPLIT>
+// stage; acc[i][j]: block i (activation rows) x weight row block j.
+template <class S, int L, int XC, bool WIDE>
 __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NST], uint8_t* const (&X)[S::NST],
                                           f8_f16 (&out)[S::NB][S::NJ]) {
     constexpr int NST = S::NST, NB = S::NB, NJ = S::NJ, TW = S::W, TWC = S::WQ;
@@ -161,20 +160,20 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
 #pragma unroll
         for (int s = 0; s < NST - 1; ++s) issue(W[s], X[s], s);
     }
-    // Weight scales: at the top of a round lane l holds those of the round's
-    // stage l.  (Scalar loads count with the LDS reads, out of order, and every
-    // partial wait for LDS data became a full one.)
+    // Weight scales of the WIDE loop: at the top of a round lane l holds those of
+    // the round's stage l.  (Scalar loads count with the LDS reads, out of order,
+    // and every partial wait for LDS data became a full one.)
     float sl[2], sn[2];
     auto scales = [&](int kb) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) sn[j] = g.sp[j][min(kb + lane_id(), g.nst - 1)];
     };
-    if constexpr (NB * NJ < 8) scales(0);
+    if constexpr (WIDE) scales(0);
     f8_f16 acc[NB][NJ];
     each<NB * NJ>([&](auto b) { acc[decltype(b)::value / NJ][decltype(b)::value % NJ] = f8_f16{}; });
-    // the products of LDS stage B; byte SEL of ev scales the activation rows,
-    // lane LN of sl the weight rows
-    auto products = [&](auto bb, auto ss, auto ll) {
+    // WIDE: the products of LDS stage B; byte SEL of ev scales the activation
+    // rows, lane LN of sl the weight rows
+    auto products_wide = [&](auto bb, auto ss, auto ll) {
         constexpr int B = decltype(bb)::value, SEL = decltype(ss)::value, LN = decltype(ll)::value;
         const float s0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sl[0]), LN));
         const float s1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sl[1]), LN));
@@ -189,51 +188,39 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
             w[j][1] = tile_row(W[B] + 32 * j * F8_BLK, fl, wo, 1);
         });
         F8Wide ww[NJ][2];
-        if constexpr (WIDE) {
-            each<NJ * 2>([&](auto q) {
-                constexpr int j = decltype(q)::value / 2, h = decltype(q)::value % 2;
-                ww[j][h] = f8_widen(w[j][h].a, w[j][h].b);
-            });
-        }
+        each<NJ * 2>([&](auto q) {
+            constexpr int j = decltype(q)::value / 2, h = decltype(q)::value % 2;
+            ww[j][h] = f8_widen(w[j][h].a, w[j][h].b);
+        });
         each<L>([&](auto ii) {
             constexpr int i = decltype(ii)::value;
             const F8Row x0 = tile_row(X[B] + 32 * S::GM * i * F8_BLK, fl, xo, 0);
             const F8Row x1 = tile_row(X[B] + 32 * S::GM * i * F8_BLK, fl, xo, 1);
-            F8Wide v0, v1;
-            if constexpr (WIDE) {
-                v0 = f8_widen(x0.a, x0.b);
-                v1 = f8_widen(x1.a, x1.b);
-            }
+            const F8Wide v0 = f8_widen(x0.a, x0.b), v1 = f8_widen(x1.a, x1.b);
+            const float sx = f8_scale_value((ev[i] >> (8 * SEL)) & 255u);
             each<NJ>([&](auto jj) {
                 constexpr int j = decltype(jj)::value;
-                f8_f16 p;
-                if constexpr (WIDE) {
-                    p = f8_dot32(ww[j][1], v1, f8_dot32(ww[j][0], v0, f8_f16{})) *
-                        f8_scale_value((ev[i] >> (8 * SEL)) & 255u);
-                } else {
-                    p = f8_mfma32<SEL>(f8_join(w[j][0].a, w[j][0].b), f8_join(x0.a, x0.b), f8_f16{}, ev[i]);
-                    p = f8_mfma32<SEL>(f8_join(w[j][1].a, w[j][1].b), f8_join(x1.a, x1.b), p, ev[i]);
-                }
+                const f8_f16 p = f8_dot32(ww[j][1], v1, f8_dot32(ww[j][0], v0, f8_f16{})) * sx;
                 // (whole-vector operations: accumulators written element by
                 // element in a loop went to scratch memory)
-                const float a = j > 0 ? s1 : s0, b = SPLIT ? s1 : a;
-                const f8_f16 s = f8_f16{a, a, a, a, a, a, a, a, b, b, b, b, b, b, b, b};
+                const float a = j > 0 ? s1 : s0;
+                const f8_f16 s = f8_f16{a, a, a, a, a, a, a, a, a, a, a, a, a, a, a, a};
                 acc[i][j] = __builtin_elementwise_fma(s, p, acc[i][j]);
             });
         });
         wait_lgkm0();  // this stage's reads are done before the next barrier releases its refill
     };
-    // The same for the largest shape, in a fixed order: a block's products are
-    // issued before the FMAs of the block before it, which then run beside the
-    // matrix unit; the last block of a stage waits for the first products of the
-    // next; the copies go out behind the first products.  (Its registers are
-    // all taken: left to the compiler the sums of several blocks are in flight
-    // at once and offsets are reloaded from scratch memory behind the copies;
-    // 4096 x 4096 x 6144 131 us, in this order 106.)
-    constexpr bool PIPE = NB * NJ == 8;
+    // The 8-bit products, in a fixed order: a block's products are issued before
+    // the FMAs of the block before it, which then run beside the matrix unit; the
+    // last block of a stage waits for the first products of the next; the copies
+    // go out behind the first products.  (Left to the compiler the sums of
+    // several blocks are in flight at once; in the largest shape, whose registers
+    // are all taken, offsets were then reloaded from scratch memory behind the
+    // copies: 4096 x 4096 x 6144 131 us, in this order 106.  The smaller shapes
+    // gain little: 300 x 4096 x 6144 in 64 x 64 tiles 25.0, now 24.5.)
     f8_f16 pend = f8_f16{};
     float q0 = 0.0f, q1 = 0.0f, t0 = 0.0f, t1 = 0.0f;  // scales of the block that waits, of the next stage
-    if constexpr (PIPE) {
+    if constexpr (!WIDE) {
         t0 = f8_uniform(g.sp[0], 0);
         t1 = f8_uniform(g.sp[1], 0);
     }
@@ -243,10 +230,9 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         const f8_f16 s = f8_f16{a, a, a, a, a, a, a, a, a, a, a, a, a, a, a, a};
         acc[i][j] = __builtin_elementwise_fma(s, pend, acc[i][j]);
     };
-    auto products_pipe = [&](auto bb, auto ss, auto more, int kb) {
+    auto products = [&](auto bb, auto ss, auto more, int kb) {
         constexpr int B = decltype(bb)::value, SEL = decltype(ss)::value;
         constexpr bool MORE = decltype(more)::value != 0;  // a stage of the loop, which sends for a later one
-        static_assert(!PIPE || (!WIDE && !SPLIT), "the largest shape");
         uint32_t wo = S::WR * wn * F8_BLK, xo = 32 * mh * F8_BLK;
         __asm__ volatile("" : "+s"(wo), "+s"(xo));
         F8Row w[NJ][2], x[2];
@@ -299,8 +285,8 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         constexpr int n = decltype(nn)::value, B = n % NST, SEL = n % 4;
         wait_vm<(NST - 2) * NC>();
         barrier_nofence();
-        if constexpr (PIPE && L > 0) {
-            products_pipe(ic<B>(), ic<SEL>(), ic<1>(), kb);
+        if constexpr (!WIDE && L > 0) {
+            products(ic<B>(), ic<SEL>(), ic<1>(), kb);
         } else {
             issue(W[(B + NST - 1) % NST], X[(B + NST - 1) % NST], kb + NST - 1);
             if constexpr (SEL == 0) {
@@ -310,13 +296,13 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
                     en[i] = __builtin_amdgcn_raw_buffer_load_b32(er, (int)g.eoff[i], kb + 4 < g.nst ? kb + 4 : 0, 0);
                 }
             }
-            if constexpr (L > 0) products(ic<B>(), ic<SEL>(), nn);
+            if constexpr (L > 0) products_wide(ic<B>(), ic<SEL>(), nn);
         }
     };
     // twelve (four) stages run through every pair of LDS stage and scale byte
     constexpr int CYC = NST == 3 ? 12 : 4;
     for (int kb = 0; kb < nfull; kb += CYC) {
-        if constexpr (!PIPE) {
+        if constexpr (WIDE) {
             sl[0] = sn[0];
             sl[1] = sn[1];
             scales(kb + CYC);
@@ -345,15 +331,15 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         for (int i = 0; i < L; ++i) ev[i] = __builtin_amdgcn_raw_buffer_load_b8(er, (int)g.eoff[i], nfull, 0);
         wait_vm<0>();
         barrier_nofence();
-        if constexpr (PIPE && L > 0) {
-            products_pipe(ic<0>(), ic<0>(), ic<0>(), nfull);
+        if constexpr (!WIDE && L > 0) {
+            products(ic<0>(), ic<0>(), ic<0>(), nfull);
         } else if constexpr (L > 0) {
             sl[0] = g.sp[0][nfull];
             sl[1] = g.sp[1][nfull];
-            products(ic<0>(), ic<0>(), ic<0>());
+            products_wide(ic<0>(), ic<0>(), ic<0>());
         }
     }
-    if constexpr (PIPE && L > 0) retire(ic<(L > 0 ? L * NJ - 1 : 0)>(), q0, q1);
+    if constexpr (!WIDE && L > 0) retire(ic<(L > 0 ? L * NJ - 1 : 0)>(), q0, q1);
     wait_vm<0>();  // no copy may still be writing LDS when the workgroup ends
     each<NB * NJ>([&](auto b) {
         constexpr int i = decltype(b)::value / NJ, j = decltype(b)::value % NJ;
@@ -362,11 +348,11 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
 }
 
 // Runs the loop built for this wavefront's live blocks (rows of the tile: nrows).
-template <class S, bool WIDE, bool SPLIT>
+template <class S, bool WIDE>
 __device__ __forceinline__ void tile_run(const F8Tile<S>& g, int nrows, uint8_t* const (&W)[S::NST],
                                          uint8_t* const (&X)[S::NST], f8_f16 (&acc)[S::NB][S::NJ]) {
     const int wave = wave_index(), nblk = (nrows + 31) / 32, live = (nblk - wave / S::GN + S::GM - 1) / S::GM;
-    auto run = [&](auto l, auto xc) { tile_loop<S, decltype(l)::value, decltype(xc)::value, WIDE, SPLIT>(g, W, X, acc); };
+    auto run = [&](auto l, auto xc) { tile_loop<S, decltype(l)::value, decltype(xc)::value, WIDE>(g, W, X, acc); };
     static_assert(S::GM == 2, "two wavefronts along the activation rows");
     {  // a round of activation copies covers W / 4 blocks
         constexpr int RB = S::W / 4;
@@ -396,19 +382,19 @@ __device__ __forceinline__ void tile_run(const F8Tile<S>& g, int nrows, uint8_t*
     uint8_t* const WS[4] = {W0, W1, W2, W3};                                                   \
     uint8_t* const XS[4] = {X0, X1, X2, X3}
 
-template <class S, bool WIDE, bool SPLIT>
+template <class S, bool WIDE>
 __device__ __forceinline__ void tile_go(const F8Tile<S>& g, int nrows, uint8_t* const (&WS)[4], uint8_t* const (&XS)[4],
                                         f8_f16 (&acc)[S::NB][S::NJ]) {
     if constexpr (S::NST == 2) {
         uint8_t* const W[2] = {WS[0], WS[1]};
         uint8_t* const X[2] = {XS[0], XS[1]};
-        tile_run<S, WIDE, SPLIT>(g, nrows, W, X, acc);
+        tile_run<S, WIDE>(g, nrows, W, X, acc);
     } else if constexpr (S::NST == 3) {
         uint8_t* const W[3] = {WS[0], WS[1], WS[2]};
         uint8_t* const X[3] = {XS[0], XS[1], XS[2]};
-        tile_run<S, WIDE, SPLIT>(g, nrows, W, X, acc);
+        tile_run<S, WIDE>(g, nrows, W, X, acc);
     } else {
-        tile_run<S, WIDE, SPLIT>(g, nrows, WS, XS, acc);
+        tile_run<S, WIDE>(g, nrows, WS, XS, acc);
     }
 }
 
@@ -460,22 +446,22 @@ __global__ __launch_bounds__(64 * S::W) void f8_gateup_tile_kernel(F8Ffn a) {
     g.sp[0] = reinterpret_cast<const float*>(G.scale) + srow;
     g.sp[1] = reinterpret_cast<const float*>(U.scale) + srow;
     f8_f16 acc[NB][S::NJ];
-    tile_go<S, false, S::NJ == 1>(g, tr.nrows, WS, XS, acc);
+    tile_go<S, false>(g, tr.nrows, WS, XS, acc);
     // h and its largest magnitude per row over the tile's 128 columns
-    // (a wavefront has gate and up in its two blocks, or in the lower and upper
-    // half of its one)
-    constexpr int NV = HC / 2;  // h values per lane
+    // (a wavefront has gate and up in its two blocks)
+    static_assert(S::NJ == 2 && HC == 32, "a block of gate, a block of up");
+    constexpr int NV = 16;  // h values per lane
     const int c0 = n0 + HC * wn;
     const bool in = c0 < F;  // (F is a multiple of 64)
     __syncthreads();  // every wavefront has read its last stage
     each<NB>([&](auto ii) {  // h takes the place of gate in acc[i][0]
         constexpr int i = decltype(ii)::value;
-        const f8_f16 ga = acc[i][0], up = acc[i][S::NJ - 1];
+        const f8_f16 ga = acc[i][0], up = acc[i][1];
         f8_f16 h = ga;
         uint32_t m = 0;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            h[v] = silu_f32(ga[v]) * up[S::NJ == 2 ? v : v + 8];
+            h[v] = silu_f32(ga[v]) * up[v];
             m = max(m, f8_abs_bits(h[v]));
         }
         acc[i][0] = h;
@@ -493,22 +479,19 @@ __global__ __launch_bounds__(64 * S::W) void f8_gateup_tile_kernel(F8Ffn a) {
         for (int w = 0; w < S::GN; ++w) m = max(m, red[w][r]);
         const uint32_t byte = f8_scale_byte(m);
         const float inv = f8_inv_scale(byte);
-        uint32_t c[NV / 4];
+        uint32_t c[4];
 #pragma unroll
-        for (int j = 0; j < NV / 4; ++j)
+        for (int j = 0; j < 4; ++j)
             c[j] = f8_pack4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3], inv, byte);
-        // lanes l and l + 32 hold alternate 4-column runs of a row: each takes NV adjacent columns
-        uint32_t o[NV / 8];
+        // lanes l and l + 32 hold alternate 4-column runs of a row: each takes 16 adjacent columns
+        uint32_t o[2];
 #pragma unroll
-        for (int j = 0; j < NV / 8; ++j) o[j] = (uint32_t)__shfl_xor((int)(hi ? c[j] : c[j + NV / 8]), 32);
+        for (int j = 0; j < 2; ++j) o[j] = (uint32_t)__shfl_xor((int)(hi ? c[j] : c[j + 2]), 32);
         if (r >= tr.nrows) return;
         const size_t hrow = (size_t)(tr.rbeg + r);
-        uint8_t* dst = a.hq + hrow * a.f.ldh + c0 + NV * hi;
-        if constexpr (NV == 16) {
-            if (in) *reinterpret_cast<uint4*>(dst) = hi ? make_uint4(o[0], c[2], o[1], c[3]) : make_uint4(c[0], o[0], c[1], o[1]);
-        } else {
-            if (in) *reinterpret_cast<uint2*>(dst) = hi ? make_uint2(o[0], c[1]) : make_uint2(c[0], o[0]);
-        }
+        if (in)
+            *reinterpret_cast<uint4*>(a.hq + hrow * a.f.ldh + c0 + 16 * hi) =
+                hi ? make_uint4(o[0], c[2], o[1], c[3]) : make_uint4(c[0], o[0], c[1], o[1]);
         if (wn == 0 && hi == 0) a.he[hrow * f8_scale_ld(a.f.ldh) + ntile] = (uint8_t)byte;
     });
 }
@@ -553,7 +536,7 @@ __global__ __launch_bounds__(64 * S::W) void f8_down_tile_kernel(F8Ffn a) {
     for (int j = 0; j < 2; ++j)  // (one block: both the same)
         g.sp[j] = reinterpret_cast<const float*>(D.scale) + (e * f8_blocks(d) + min(c0 + 32 * j % S::WR, d - 1) / F8_BLK) * g.nst;
     f8_f16 acc[NB][S::NJ];
-    tile_go<S, false, false>(g, tr.nrows, WS, XS, acc);
+    tile_go<S, false>(g, tr.nrows, WS, XS, acc);
     // (stores that the caches join: a lane's 16 bytes are an eighth of a cache
     // line, and written past the caches the 4096-token case took 1.64 ms, not 1.08)
     float* out = shared ? a.f.shared_out : a.f.slot_out;
@@ -615,7 +598,7 @@ __global__ __launch_bounds__(64 * S::W) void f8_dense_tile_kernel(BlockArgs a) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) g.sp[j] = a.ws + (size_t)(min(c0 + 32 * j % S::WR, a.n - 1) / F8_BLK) * g.nst;
     f8_f16 acc[NB][S::NJ];
-    tile_go<S, OF == MOE_DT_F32, false>(g, nrows, WS, XS, acc);
+    tile_go<S, OF == MOE_DT_F32>(g, nrows, WS, XS, acc);
     each<NB>([&](auto ii) {
         constexpr int i = decltype(ii)::value;
         const int r = 32 * (mh + S::GM * i) + l32;
