@@ -474,8 +474,13 @@ int moe_block_matmul(const void* x, int32_t x_dtype, const uint8_t* x_scale, con
     hipStream_t st = static_cast<hipStream_t>(stream);
     BlockArgs a{static_cast<const uint8_t*>(x), x_scale, w, w_scale, m, n, k, out, out_dtype};
     if (!codes) {
-        if (!ptr_ok(ws)) return MOE_ERR_INVALID;
+        if (!ptr_ok(ws)) return MOE_ERR_INVALID;  // (asked for at every m, though few rows do not use it)
         if (ws_bytes < moe_block_matmul_workspace_bytes(x_dtype, m, k)) return MOE_ERR_WORKSPACE;
+        if (block_matmul_takes(x_dtype, m, n)) {
+            a.xe = nullptr;
+            a.xdt = x_dtype;
+            return device_status(launch_block_matmul(a, st));
+        }
         uint8_t* q = static_cast<uint8_t*>(ws);
         uint8_t* e = q + align256((size_t)m * k);
         const hipError_t err = launch_quantize_rows(QuantArgs{x, x_dtype, m, k, k, q, e}, st);

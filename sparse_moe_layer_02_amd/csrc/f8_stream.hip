@@ -29,22 +29,81 @@ __device__ __forceinline__ f8_u4 f8_ld(const uint8_t* p) {
     else return *reinterpret_cast<const f8_u4*>(p);
 }
 
+// A lane's 32 columns of one activation row: 16 from each 64-column half, as
+// codes, or as bf16 or fp32 values that are quantised here (few rows: the
+// launch that would do it first costs more than every workgroup doing it).
+template <int XF>
+struct F8Act {
+    static constexpr int N = XF == MOE_DT_F8B128 ? 1 : XF == MOE_DT_BF16 ? 2 : 4;  // 16-byte pieces per half
+    static constexpr int SIZE = XF == MOE_DT_F8B128 ? 1 : XF == MOE_DT_BF16 ? 2 : 4;
+    f8_u4 v[2][N];
+    uint32_t e;  // scale byte (codes)
+
+    __device__ __forceinline__ void load(const uint8_t* row, const uint8_t* scales, int kb, int lo, int K) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = kb * F8_BLK + 64 * h + lo;
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+                v[h][q] = f8_u4{0, 0, 0, 0};
+                if (c < K) v[h][q] = f8_ld<false>(row + (size_t)c * SIZE + 16 * q);  // K is a multiple of 16
+            }
+        }
+        if constexpr (XF == MOE_DT_F8B128) e = scales[kb];
+    }
+    // codes of both halves; their scale in s
+    __device__ __forceinline__ F8Wide widen(float& s) const {
+        if constexpr (XF == MOE_DT_F8B128) {
+            s = f8_scale_value(e);
+            return f8_widen(v[0][0], v[1][0]);
+        } else {
+            float x[2][16];
+            uint32_t m = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    if constexpr (XF == MOE_DT_BF16) {
+                        const uint32_t p = v[h][j / 8][j / 2 % 4];
+                        x[h][j] = j % 2 ? bf16_hi(p) : bf16_lo(p);
+                    } else {
+                        x[h][j] = __uint_as_float(v[h][j / 4][j % 4]);
+                    }
+                    m = max(m, f8_abs_bits(x[h][j]));
+                }
+            // the block's other columns are in the lanes 16, 32 and 48 away
+            m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+            m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+            const uint32_t byte = f8_scale_byte(m);
+            const float inv = f8_inv_scale(byte);
+            f8_u4 c[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    c[h][q] = f8_pack4(x[h][4 * q], x[h][4 * q + 1], x[h][4 * q + 2], x[h][4 * q + 3], inv, byte);
+            s = f8_scale_value(byte);
+            return f8_widen(c[0], c[1]);
+        }
+    }
+};
+
 // Fragments of U steps of 128 columns: NR weight row tiles, NT activation row tiles.
-template <int NR, int NT, int U>
+template <int NR, int NT, int U, int XF>
 struct F8Frag {
-    f8_u4 w[U][NR][2], x[U][NT][2];
-    uint32_t e[U][NT];
+    f8_u4 w[U][NR][2];
+    F8Act<XF> x[U][NT];
 };
 
 // acc[r][t] += the products over the 128-column steps [kb0, kb1).  wp, xp:
 // this lane's rows; ep: their scale bytes; sp: the weight rows' block scales
 // (wave-uniform).  kb1 may be the step that K ends in: its columns past K
 // count as zeros and are not read.
-template <int NR, int NT, int U>
+template <int NR, int NT, int U, int XF>
 __device__ __forceinline__ void f8_stream(const uint8_t* const (&wp)[NR], const float* const (&sp)[NR],
                                           const uint8_t* const (&xp)[NT], const uint8_t* const (&ep)[NT], int kb0,
                                           int kb1, int K, f8_f4 (&acc)[NR][NT]) {
-    using Frag = F8Frag<NR, NT, U>;
+    using Frag = F8Frag<NR, NT, U, XF>;
     const int lo = 16 * (lane_id() / 16), kfull = K / F8_BLK, kbe = min(kb1, kfull);
     auto load = [&](Frag& f, int kb) {
 #pragma unroll
@@ -57,15 +116,11 @@ __device__ __forceinline__ void f8_stream(const uint8_t* const (&wp)[NR], const 
                 f.w[u][r][1] = f8_ld<true>(wp[r] + o + 64);
             }
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                f.x[u][t][0] = f8_ld<false>(xp[t] + o);
-                f.x[u][t][1] = f8_ld<false>(xp[t] + o + 64);
-                f.e[u][t] = ep[t][k];
-            }
+            for (int t = 0; t < NT; ++t) f.x[u][t].load(xp[t], ep[t], k, lo, 1 << 30);
         }
         pin();
     };
-    auto step = [&](const f8_u4 (&w)[NR][2], const f8_u4 (&x)[NT][2], const uint32_t (&e)[NT], int k) {
+    auto step = [&](const f8_u4 (&w)[NR][2], const F8Act<XF> (&x)[NT], int k) {
         F8Wide ww[NR];
         float s[NR];
 #pragma unroll
@@ -75,8 +130,8 @@ __device__ __forceinline__ void f8_stream(const uint8_t* const (&wp)[NR], const 
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const F8Wide xw = f8_widen(x[t][0], x[t][1]);
-            const float sx = f8_scale_value(e[t]);
+            float sx;
+            const F8Wide xw = x[t].widen(sx);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
                 const f8_f4 p = f8_dot16(ww[r], xw, f8_f4{0.f, 0.f, 0.f, 0.f});
@@ -88,7 +143,7 @@ __device__ __forceinline__ void f8_stream(const uint8_t* const (&wp)[NR], const 
     auto compute = [&](const Frag& f, int kb) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (kb + u < kbe) step(f.w[u], f.x[u], f.e[u], kb + u);
+            if (kb + u < kbe) step(f.w[u], f.x[u], kb + u);
     };
     if (kb0 < kbe) {
         Frag a, b;
@@ -104,32 +159,24 @@ __device__ __forceinline__ void f8_stream(const uint8_t* const (&wp)[NR], const 
     }
     if (kb0 <= kfull && kfull < kb1) {  // the step that K ends in
         const int k0 = kfull * F8_BLK + lo;
-        const f8_u4 zero = f8_u4{0, 0, 0, 0};
-        f8_u4 w[NR][2], x[NT][2];
-        uint32_t e[NT];
+        f8_u4 w[NR][2];
+        F8Act<XF> x[NT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const bool in = k0 + 64 * h < K;  // K is a multiple of 16
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-                w[r][h] = zero;
-                if (in) w[r][h] = f8_ld<true>(wp[r] + k0 + 64 * h);
+                w[r][h] = f8_u4{0, 0, 0, 0};
+                if (k0 + 64 * h < K) w[r][h] = f8_ld<true>(wp[r] + k0 + 64 * h);
             }
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                x[t][h] = zero;
-                if (in) x[t][h] = f8_ld<false>(xp[t] + k0 + 64 * h);
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) e[t] = ep[t][kfull];
-        step(w, x, e, kfull);
+        for (int t = 0; t < NT; ++t) x[t].load(xp[t], ep[t], kfull, lo, K);
+        step(w, x, kfull);
     }
 }
 
 // 16 NR output columns per workgroup, K split over its SW wavefronts, whose
 // partial sums are added in LDS in a fixed order.
-template <int NT, int NR, int OF>
+template <int NT, int NR, int OF, int XF>
 __global__ __launch_bounds__(64 * SW) void f8_dense_stream_kernel(BlockArgs a) {
     __shared__ f8_f4 part[SW][NR][NT][WAVE];
     const int lane = lane_id(), wave = wave_index();
@@ -148,11 +195,12 @@ __global__ __launch_bounds__(64 * SW) void f8_dense_stream_kernel(BlockArgs a) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const size_t r = (size_t)min(m0 + 16 * t + lane % 16, a.m - 1);
-        xp[t] = a.xq + r * a.k;
-        ep[t] = a.xe + r * f8_scale_ld(a.k);
+        xp[t] = a.xq + r * a.k * F8Act<XF>::SIZE;
+        ep[t] = XF == MOE_DT_F8B128 ? a.xe + r * f8_scale_ld(a.k) : nullptr;
     }
     const int per = (KB + SW - 1) / SW;
-    f8_stream<NR, NT, 4 / NR>(wp, sp, xp, ep, wave * per, min(KB, (wave + 1) * per), a.k, acc);
+    constexpr int U = XF == MOE_DT_F8B128 ? 4 / NR : XF == MOE_DT_BF16 ? 2 : 1;  // steps in flight: what the registers hold
+    f8_stream<NR, NT, U, XF>(wp, sp, xp, ep, wave * per, min(KB, (wave + 1) * per), a.k, acc);
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -171,22 +219,33 @@ __global__ __launch_bounds__(64 * SW) void f8_dense_stream_kernel(BlockArgs a) {
     }
 }
 
-template <int NT, int NR>
+template <int NT, int NR, int XF>
 hipError_t dense_launch(const BlockArgs& a, hipStream_t st) {
     const dim3 grid((a.n + 16 * NR - 1) / (16 * NR), (a.m + 16 * NT - 1) / (16 * NT));
-    if (a.odt == MOE_DT_BF16) f8_dense_stream_kernel<NT, NR, MOE_DT_BF16><<<grid, 64 * SW, 0, st>>>(a);
-    else f8_dense_stream_kernel<NT, NR, MOE_DT_F32><<<grid, 64 * SW, 0, st>>>(a);
+    if (a.odt == MOE_DT_BF16) f8_dense_stream_kernel<NT, NR, MOE_DT_BF16, XF><<<grid, 64 * SW, 0, st>>>(a);
+    else f8_dense_stream_kernel<NT, NR, MOE_DT_F32, XF><<<grid, 64 * SW, 0, st>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// Rows that are quantised by the product itself: every workgroup of 16 output
+// columns does it again, so few rows and few workgroups (us against a launch of
+// its own first, bf16 rows: n x k 6144 x 2048: 1 row 7.7 / 10.5, 16 rows 10.2 /
+// 13.8; 4096 x 6144: 9.8 / 9.8, 14.3 / 14.3; 24576 x 6144: 57 / 52, 78 / 70; fp32
+// rows, twice the bytes, 4096 x 6144: 1 row 9.6 / 9.7, 8 rows 13.9 / 12.4).
+bool block_matmul_takes(int xdt, int m, int n) {
+    return n <= 8192 && m <= (xdt == MOE_DT_BF16 ? 16 : 4);
+}
+
 // Up to 48 rows here, more in LDS tiles (us at n x k 4096 x 6144: 1 row 9.1
-// against 20.8 for the smallest tiles, 24 rows 16.7 / 21.2, 128 rows 24.8 / 23.1;
-// 48 rows of 4096 x 4096 13.0 / 16.4, 77 rows of 6144 x 2048 16.4 / 10.1).
+// against 20.3 for the smallest tiles, 24 rows 16.7 / 20.3, 128 rows 33.9 / 23.1;
+// 48 rows of 4096 x 4096 13.1 / 16.2, 77 rows of 6144 x 2048 16.9 / 9.9).
 hipError_t launch_block_matmul(const BlockArgs& a, hipStream_t st) {
-    if (a.m <= 16) return dense_launch<1, 1>(a, st);
-    if (a.m <= 48) return dense_launch<2, 2>(a, st);
+    if (a.xdt == MOE_DT_BF16) return dense_launch<1, 1, MOE_DT_BF16>(a, st);
+    if (a.xdt == MOE_DT_F32) return dense_launch<1, 1, MOE_DT_F32>(a, st);
+    if (a.m <= 16) return dense_launch<1, 1, MOE_DT_F8B128>(a, st);
+    if (a.m <= 48) return dense_launch<2, 2, MOE_DT_F8B128>(a, st);
     return launch_block_matmul_tile(a, st);
 }
 

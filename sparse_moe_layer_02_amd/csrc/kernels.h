@@ -67,13 +67,15 @@ hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t st, const KTime&
 
 // Dense product out[m, n] = x[m, k] w[n, k]^T of e4m3 operands.
 struct BlockArgs {
-    const uint8_t *xq, *xe;  // [m, k] codes, [m, f8_scale_ld(k)] scale bytes
+    const uint8_t *xq, *xe;  // [m, k] codes, [m, f8_scale_ld(k)] scale bytes (or rows of xdt and null)
     const uint8_t* wq;       // [n, k]
     const float* ws;         // [ceil(n / 128), ceil(k / 128)]
     int m, n, k;
     void* out;               // [m, n]
     int odt;                 // MOE_DT_F32 or MOE_DT_BF16
+    int xdt = MOE_DT_F8B128; // where block_matmul_takes says so, MOE_DT_F32 or MOE_DT_BF16
 };
+bool block_matmul_takes(int xdt, int m, int n);
 hipError_t launch_block_matmul(const BlockArgs& a, hipStream_t st);
 hipError_t launch_block_matmul_tile(const BlockArgs& a, hipStream_t st);  // many rows
 

@@ -68,6 +68,33 @@ def test_grouped_layer_refusals(moe):
     assert call(cfg(moe), W=ctypes.byref(bad)) == 1
 
 
+def test_f8_layer_row_limit(moe):
+    """e4m3 layers address the quantised rows with 32 bits: n_tokens * d_model < 2^32."""
+    lib = moe.load()
+    m = moe.binding.moe_mat(FAKE.value, FAKE.value)
+    w = moe.binding.moe_weights(FAKE.value, None, m, m, m, m, m, m)
+
+    def call(**kw):
+        return lib.moe_layer_forward_grouped(ctypes.byref(cfg(moe, **kw)), None, FAKE, ctypes.byref(w), FAKE, F32, None,
+                                             FAKE, 1000, None)
+
+    assert call(T=4096, d=1 << 20) == 2
+    assert call(T=4095, d=1 << 20) == 3  # (the limit is passed: only the workspace is too small)
+    assert call(T=4096, d=1 << 20, w="bf16") == 3
+
+
+def test_f8_prefetch_arguments(moe):
+    """Of e4m3 experts only the codes are fetched: a scale array may start at any 4-byte address."""
+    lib = moe.load()
+    m = moe.binding.moe_mat(FAKE.value, FAKE.value + 4)
+    w = moe.binding.moe_weights(FAKE.value, None, m, m, m, m, m, m)
+    call = lambda c, w, ids, n: lib.moe_prefetch_experts(ctypes.byref(c), ctypes.byref(w), ids, n, 7, 0, 4, None, None)
+    assert call(cfg(moe), w, None, 0) == 0
+    assert call(cfg(moe), w, None, 4) == 1
+    noscale = moe.binding.moe_mat(FAKE.value, None)
+    assert call(cfg(moe), moe.binding.moe_weights(FAKE.value, None, m, m, noscale, m, m, m), None, 0) == 1
+
+
 def test_f8_workspace_monotone(moe):
     lib = moe.load()
     base = dict(T=64, d=512, E=32, k=4, F=256, Fs=256)

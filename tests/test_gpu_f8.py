@@ -151,6 +151,65 @@ def test_matmul(dev, m, n, k, xdt):
         assert (out[m] == 123.0).all()  # the row behind the last is left alone
 
 
+# sizes whose tiles are the larger ones (128 x 128; 256 x 256 and, for fp32 results, 128 x 256), with ends in
+# rows, columns and K; K below one block; K of more blocks than a wavefront has lanes
+LARGE = [(1600, 2000, 272), (3500, 3600, 400), (70, 200, 16), (300, 70, 112), (1600, 2000, 48), (3500, 3600, 80),
+         (90, 150, 8464), (1600, 2000, 8320)]
+
+
+@pytest.mark.parametrize("odt", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", LARGE)
+def test_matmul_large(dev, m, n, k, odt):
+    """On a spread of rows and columns, the first and last among them: the definition needs not every one."""
+    torch, moe = dev
+    rng = np.random.default_rng(m + n + k)
+    wv, wc, wsc = weights_of(rng, n, k)
+    xv, xc = codes_of(rng, (m, k))
+    e = np.full((m, moe.scale_ld(k)), 127, np.uint8)
+    e[:, :-(-k // 128)] = rng.integers(110, 140, (m, -(-k // 128)))
+    odt = torch.bfloat16 if odt == "bf16" else torch.float32
+    out = torch.full((m + 1, n), 123.0, dtype=odt, device="cuda")
+    say("matmul", m, n, k, odt)
+    moe.moe_block_matmul(torch.from_numpy(xc).cuda(), torch.from_numpy(e).cuda(), torch.from_numpy(wc).cuda(),
+                         torch.from_numpy(wsc).cuda(), out[:m])
+    torch.cuda.synchronize()
+    rows = np.unique(np.concatenate([np.arange(0, m, 29), np.arange(max(0, m - 40), m)]))
+    cols = np.unique(np.concatenate([np.arange(0, n, 13), np.arange(max(0, n - 40), n)]))
+    xd = R.dequant_rows(xv, np.ldexp(1.0, e[:, :-(-k // 128)].astype(int) - 127))[rows]
+    wd = R.dequant_weight(wv, wsc.astype(np.float64))[cols]
+    ref, err = R.matmul(xd, wd, cut=odt == torch.bfloat16)
+    got = out[:m].double().cpu().numpy()
+    assert np.isfinite(got).all() and (out[m] == 123.0).all()
+    lim = err if odt == torch.float32 else R.bf16_bound(ref, err)
+    assert (np.abs(got[np.ix_(rows, cols)] - ref) <= lim).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 640, 2048), (4, 33, 1040), (5, 640, 272), (16, 200, 6144), (16, 9000, 144), (17, 64, 256)])
+def test_matmul_rows_quantised_first(dev, m, n, k):
+    """Rows handed in as bf16 or fp32 give what their quantised codes give, bit for bit, with the scales
+    of zero blocks, tiny, huge and non-finite ones."""
+    torch, moe = dev
+    rng = np.random.default_rng(m * n + k)
+    _, wc, wsc = weights_of(rng, n, k)
+    w, ws = torch.from_numpy(wc).cuda(), torch.from_numpy(wsc).cuda()
+    x = torch.randn((m, k), device="cuda") * torch.exp(torch.randn((m, 1), device="cuda") * 4)
+    for i, v in enumerate((0.0, 1e-37, 2.0 ** -140, 1e30, float("inf"), float("nan"))):
+        x[i % m, min(16 * i, k - 16):][:16] = v
+    for dt in (torch.bfloat16, torch.float32):
+        xr = x.to(dt)
+        q, s = torch.empty((m, k), dtype=torch.uint8, device="cuda"), torch.empty((m, moe.scale_ld(k)), dtype=torch.uint8, device="cuda")
+        moe.moe_quantize_rows(xr, q, s)
+        for odt in (torch.bfloat16, torch.float32):
+            say("rows", m, n, k, dt, odt)
+            a, b = (torch.full((m, n), 7.0, dtype=odt, device="cuda") for _ in range(2))
+            moe.moe_block_matmul(xr, None, w, ws, a, moe.block_matmul_workspace(xr, n))
+            moe.moe_block_matmul(q, s, w, ws, b)
+            torch.cuda.synchronize()
+            ints = torch.int16 if odt == torch.bfloat16 else torch.int32
+            same = (a.view(ints) == b.view(ints)) | (torch.isnan(a) & torch.isnan(b))
+            assert same.all()
+
+
 def test_matmul_scale_range(dev):
     """Row scales over the whole e8m0 range that keeps the result finite, and
     weight scales that are not powers of two: one nonzero product per output."""
@@ -458,6 +517,28 @@ def test_layer_graph(dev, T):
             moe.moe_layer_forward_grouped(c, g, x, Wm, want, wk)
             torch.cuda.synchronize()
             assert torch.equal(y, want), (T, i)
+
+
+def test_prefetch_changes_no_result(dev):
+    """e4m3 experts fetched ahead, on the layer's stream and beside it: the layer's output is the same."""
+    torch, moe = dev
+    T, d, E, k, F = 6, 256, 16, 4, 192
+    L = make_f8_layer(T, d, E, k, F, seed=3)
+    W = upload(L)
+    c = moe.make_config(T, d, E, k, F, score="softmax", route_scale=2.0, act="bf16", w="f8b128")
+    Wm, x, ws = moe.make_weights(W), L["x"].cuda(), moe.workspace(c)
+    want, y = (torch.empty((T, d), device="cuda") for _ in range(2))
+    moe.moe_layer_forward_grouped(c, None, x, Wm, want, ws)
+    ids = torch.tensor([E - 1, 0, -1, E, 1 << 30, 5], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    for which in range(1, 8):
+        say("prefetch", which)
+        moe.moe_prefetch_experts(c, Wm, ids, which=which, rows=(0, 3, 1 << 30)[which % 3], workgroups=1 + 7 * which)
+        side.wait_stream(torch.cuda.current_stream())
+        moe.moe_prefetch_experts(c, Wm, ids, which=which, workgroups=64, stream=side.cuda_stream)
+        moe.moe_layer_forward_grouped(c, None, x, Wm, y.fill_(9.0), ws)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), which
 
 
 def test_run_together(dev):
