@@ -45,6 +45,7 @@ struct Shape {
     static constexpr int WQ = WB / 1024 / W;                 // 1 KB copies per wavefront and stage
     static constexpr int XQ = (XB / 1024 + W - 1) / W;       // (at most)
     static_assert(WQ * 1024 * W == WB, "weight copies");
+    static constexpr int WAVES = NST * (WB + XB) <= 80 * 1024 && W == 8 ? 4 : 2;  // per SIMD: two workgroups where LDS has room
 };
 // Expert tiles (256 weight rows, the two scale blocks of a 128-column h block).
 // Up to 64 activation rows: two workgroups per compute unit, each with two
@@ -398,8 +399,52 @@ __device__ __forceinline__ void tile_go(const F8Tile<S>& g, int nrows, uint8_t* 
     }
 }
 
+// Results to memory through LDS, so that eight lanes store 128 consecutive bytes
+// of a row (a lane holds four columns of a row per eight; straight from the
+// registers, 2772 x 4096 x 192 to fp32 took 32 us and now 22, to bf16 18 / 17, to
+// 4089 columns, whose rows start anywhere, 39 / 23; 4096 x 4096 x 6144 113 / 105,
+// back to back; down of 4096 tokens 1.08 / 1.03 ms).  A wavefront's region holds 32
+// rows of 128 bytes, 16-byte chunks swizzled by row.
+constexpr int OUT_REGION = 32 * 128;
 template <class S>
-__global__ __launch_bounds__(64 * S::W) void f8_gateup_tile_kernel(F8Ffn a) {
+__device__ __forceinline__ uint8_t* out_region(uint8_t* const (&WS)[4], int wave) {
+    constexpr int PER = S::WB / OUT_REGION;  // regions in a stage's weight buffer
+    static_assert(2 * PER >= S::W, "room for every wavefront");
+    if constexpr (PER >= S::W) return WS[0] + wave * OUT_REGION;
+    else return (wave < PER ? WS[0] : WS[1]) + wave % PER * OUT_REGION;
+}
+__device__ __forceinline__ int out_chunk(int row, int c) { return row * 128 + 16 * (c ^ (row & 7)); }
+// (the wavefront's own LDS accesses keep their order; this keeps the compiler to it)
+__device__ __forceinline__ void out_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+// The lane's 16 fp32 results of a block: one activation row, 32 columns with the other half's.
+__device__ __forceinline__ void out_put_f32(uint8_t* R, int lane, const f8_f16& p) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f8_f4*>(R + out_chunk(lane & 31, 2 * q + (lane >> 5))) = f8_f4{p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]};
+}
+// The same rounded to bf16, as columns 32 j .. + 31 of the region's 64.
+__device__ __forceinline__ void out_put_bf16(uint8_t* R, int lane, int j, const f8_f16& p) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint2*>(R + out_chunk(lane & 31, 4 * j + q) + 8 * (lane >> 5)) =
+            make_uint2(f32_to_bf16(p[4 * q]) | (uint32_t)f32_to_bf16(p[4 * q + 1]) << 16,
+                       f32_to_bf16(p[4 * q + 2]) | (uint32_t)f32_to_bf16(p[4 * q + 3]) << 16);
+}
+// Rows of the region (the first `rows`, `left` columns of BYTES / sizeof(E)) to
+// `out`, n elements per row, in units of U.
+template <class E, class U, int BYTES>
+__device__ __forceinline__ void out_rows(const uint8_t* R, int lane, E* out, size_t n, int rows, int left) {
+    constexpr int PER = BYTES / sizeof(U), ROWS = WAVE / PER, EU = sizeof(U) / sizeof(E);  // lanes per row, rows at once
+#pragma unroll
+    for (int s = 0; s < 32 / ROWS; ++s) {
+        const int r = ROWS * s + lane / PER, u = lane % PER;
+        const U v = *reinterpret_cast<const U*>(R + out_chunk(r, u * (int)sizeof(U) / 16) + u * sizeof(U) % 16);
+        if (r < rows && u * EU < left) *reinterpret_cast<U*>(out + r * n + u * EU) = v;
+    }
+}
+
+template <class S>
+__global__ __launch_bounds__(64 * S::W, S::WAVES) void f8_gateup_tile_kernel(F8Ffn a) {
     constexpr int NB = S::NB, BM = S::BM, HC = S::WR / 2, TW = S::W, TWC = S::WQ;  // h columns per wavefront
     F8_TILE_LDS(S);
     // per-row maxima of the wavefronts, over the first activation stage once the K loop is done
@@ -497,7 +542,7 @@ __global__ __launch_bounds__(64 * S::W) void f8_gateup_tile_kernel(F8Ffn a) {
 }
 
 template <class S>
-__global__ __launch_bounds__(64 * S::W) void f8_down_tile_kernel(F8Ffn a) {
+__global__ __launch_bounds__(64 * S::W, S::WAVES) void f8_down_tile_kernel(F8Ffn a) {
     constexpr int NB = S::NB, BM = S::BM, TN = S::TN, TW = S::W, TWC = S::WQ;
     F8_TILE_LDS(S);
     int tile, ntile;
@@ -537,30 +582,35 @@ __global__ __launch_bounds__(64 * S::W) void f8_down_tile_kernel(F8Ffn a) {
         g.sp[j] = reinterpret_cast<const float*>(D.scale) + (e * f8_blocks(d) + min(c0 + 32 * j % S::WR, d - 1) / F8_BLK) * g.nst;
     f8_f16 acc[NB][S::NJ];
     tile_go<S, false>(g, tr.nrows, WS, XS, acc);
-    // (stores that the caches join: a lane's 16 bytes are an eighth of a cache
-    // line, and written past the caches the 4096-token case took 1.64 ms, not 1.08)
     float* out = shared ? a.f.shared_out : a.f.slot_out;
+    __syncthreads();  // every wavefront has read its last stage
+    uint8_t* R = out_region<S>(WS, wave);
+    int ln = lane;  // (opaque: nothing formed from it is kept over the loop)
+    __asm__ volatile("" : "+v"(ln));
+    auto slot = [&](int r) {  // the result row of tile row r, or -1
+        if (r >= tr.nrows) return -1;
+        if (shared) return tr.rbeg - a.f.T * a.f.k + r;
+        const int f = a.f.perm_rows[tr.rbeg + r];
+        return f >= 0 && f < a.f.T * a.f.k ? f : -1;
+    };
     each<NB>([&](auto ii) {
         constexpr int i = decltype(ii)::value;
-        const int r = 32 * (mh + S::GM * i) + l32;
-        if (r >= tr.nrows) return;
-        int dst = tr.rbeg - a.f.T * a.f.k + r;
-        float w = 1.0f;
-        if (!shared) {
-            dst = a.f.perm_rows[tr.rbeg + r];
-            if (dst < 0 || dst >= a.f.T * a.f.k) return;
-            w = a.f.topk_w[dst];
-        }
+        const int r0 = 32 * (mh + S::GM * i);
+        if (r0 >= tr.nrows) return;
+        const int f = slot(r0 + (ln & 31));
+        const float w = shared ? 1.0f : f < 0 ? 0.0f : a.f.topk_w[f];
         each<S::NJ>([&](auto jj) {
             constexpr int j = decltype(jj)::value;
-            const f8_f16 p = acc[i][j] * w;
+            out_put_f32(R, ln, acc[i][j] * w);
+            out_fence();
+            const int c = c0 + 32 * j + 4 * (ln & 7);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int c = c0 + 32 * j + 8 * q + 4 * (lane >> 5);
-                if (c < d)
-                    *reinterpret_cast<float4*>(out + (size_t)dst * d + c) =
-                        make_float4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+            for (int s = 0; s < 4; ++s) {
+                const f8_f4 v = *reinterpret_cast<const f8_f4*>(R + out_chunk(8 * s + (ln >> 3), ln & 7));
+                const int dst = __shfl(f, 8 * s + (ln >> 3));
+                if (dst >= 0 && c < d) *reinterpret_cast<f8_f4*>(out + (size_t)dst * d + c) = v;
             }
+            out_fence();
         });
     });
 }
@@ -599,21 +649,34 @@ __global__ __launch_bounds__(64 * S::W) void f8_dense_tile_kernel(BlockArgs a) {
     for (int j = 0; j < 2; ++j) g.sp[j] = a.ws + (size_t)(min(c0 + 32 * j % S::WR, a.n - 1) / F8_BLK) * g.nst;
     f8_f16 acc[NB][S::NJ];
     tile_go<S, OF == MOE_DT_F32>(g, nrows, WS, XS, acc);
+    __syncthreads();  // every wavefront has read its last stage
+    uint8_t* R = out_region<S>(WS, wave);
     each<NB>([&](auto ii) {
         constexpr int i = decltype(ii)::value;
-        const int r = 32 * (mh + S::GM * i) + l32;
-        if (r >= nrows) return;
-        each<S::NJ>([&](auto jj) {
-            constexpr int j = decltype(jj)::value;
-            const f8_f16 p = acc[i][j];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int c = c0 + 32 * j + 8 * q + 4 * (lane >> 5);
-                if (c >= a.n) continue;
-                const float v[4] = {p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]};
-                f8_store4<OF>(a.out, (size_t)(m0 + r) * a.n + c, a.n - c, v, a.n % 4 == 0);
-            }
-        });
+        const int r0 = 32 * (mh + S::GM * i), rows = nrows - r0;
+        if (rows <= 0) return;
+        const size_t at = (size_t)(m0 + r0) * a.n + c0;
+        if constexpr (OF == MOE_DT_BF16) {
+            each<S::NJ>([&](auto jj) { out_put_bf16(R, lane, decltype(jj)::value, acc[i][decltype(jj)::value]); });
+            out_fence();
+            uint16_t* out = static_cast<uint16_t*>(a.out) + at;
+            constexpr int BYTES = 64 * S::NJ;
+            if (a.n % 8 == 0) out_rows<uint16_t, f8_u4, BYTES>(R, lane, out, a.n, rows, a.n - c0);
+            else if (a.n % 4 == 0) out_rows<uint16_t, uint2, BYTES>(R, lane, out, a.n, rows, a.n - c0);
+            else if (a.n % 2 == 0) out_rows<uint16_t, uint32_t, BYTES>(R, lane, out, a.n, rows, a.n - c0);
+            else out_rows<uint16_t, uint16_t, BYTES>(R, lane, out, a.n, rows, a.n - c0);
+            out_fence();
+        } else {
+            each<S::NJ>([&](auto jj) {
+                constexpr int j = decltype(jj)::value;
+                out_put_f32(R, lane, acc[i][j]);
+                out_fence();
+                float* out = static_cast<float*>(a.out) + at + 32 * j;
+                if (a.n % 4 == 0) out_rows<float, f8_u4, 128>(R, lane, out, a.n, rows, a.n - c0 - 32 * j);
+                else out_rows<float, uint32_t, 128>(R, lane, out, a.n, rows, a.n - c0 - 32 * j);
+                out_fence();
+            });
+        }
     });
 }
 
