@@ -34,10 +34,11 @@ namespace moe {
 namespace {
 
 // Tile shapes: GM x GN wavefronts (GM along the activation rows, GN along the
-// weight rows), each NB x NJ blocks of 32 x 32, NST stages in LDS.
-template <int NB_, int NJ_, int GM_, int GN_, int NST_>
+// weight rows), each NB x NJ blocks of 32 x 32, NST stages of weight rows and NSX
+// of activation rows in LDS.
+template <int NB_, int NJ_, int GM_, int GN_, int NST_, int NSX_ = NST_>
 struct Shape {
-    static constexpr int NB = NB_, NJ = NJ_, GM = GM_, GN = GN_, NST = NST_;
+    static constexpr int NB = NB_, NJ = NJ_, GM = GM_, GN = GN_, NST = NST_, NSX = NSX_;
     static constexpr int W = GM * GN;              // wavefronts
     static constexpr int BM = 32 * NB * GM;        // activation rows
     static constexpr int WR = 32 * NJ, TN = WR * GN;         // weight rows per wavefront, per tile
@@ -45,19 +46,24 @@ struct Shape {
     static constexpr int WQ = WB / 1024 / W;                 // 1 KB copies per wavefront and stage
     static constexpr int XQ = (XB / 1024 + W - 1) / W;       // (at most)
     static_assert(WQ * 1024 * W == WB, "weight copies");
-    static constexpr int WAVES = NST * (WB + XB) <= 80 * 1024 && W == 8 ? 4 : 2;  // per SIMD: two workgroups where LDS has room
+    static constexpr int WAVES = NST * WB + NSX * XB <= 80 * 1024 && W == 8 ? 4 : 2;  // per SIMD: two workgroups where LDS has room
 };
 // Expert tiles (256 weight rows, the two scale blocks of a 128-column h block).
 // Up to 64 activation rows: two workgroups per compute unit, each with two
 // stages, so that one's start and end lie under the other's loop (gate/up of
 // 512 tokens, 16 rows per expert: 1.06 ms, 6.1 TB/s of weights; one workgroup
-// with four stages 1.35 ms).  More: the matrix work sets the pace, and a
-// larger tile reads LDS less per product.
+// with four stages 1.35 ms).  More: a larger tile reads LDS less per product and
+// an expert's weights fewer times; the weights, which come from HBM, are sent for
+// a stage earlier than the activation rows, most often in L2 (128 rows per
+// expert: gate/up 1.66 ms and down 1.01, both one stage ahead 1.77 and 1.03; 128
+// rows per tile with the weights two stages further ahead 1.83 and 1.11).
 typedef Shape<1, 2, 2, 4, 2> Rows64;
-typedef Shape<4, 2, 2, 4, 2> Rows256;
-// Further tiles of the dense product, for sizes whose largest tiles would leave
-// compute units idle, and for fp32 results (whose widened operands do not fit
-// beside the accumulators of the largest tile).
+typedef Shape<4, 2, 2, 4, 3, 2> Rows256;
+// Tiles of the dense product: its weights are shared by every row tile, so one
+// stage ahead is enough (4096 x 4096 x 6144 105 us, 108 with the ring above);
+// smaller ones for sizes that would leave compute units idle, and for fp32 results
+// (whose widened operands do not fit beside the accumulators of the largest).
+typedef Shape<4, 2, 2, 4, 2> Square256;
 typedef Shape<2, 2, 2, 4, 3> Rows128;
 typedef Shape<2, 2, 2, 2, 2> Square128;
 typedef Shape<1, 1, 2, 2, 4> Square64;
@@ -127,9 +133,9 @@ __device__ __forceinline__ void each(F f) {
 // The K loop of one wavefront with L live blocks and XC activation copies per
 // stage; acc[i][j]: block i (activation rows) x weight row block j.
 template <class S, int L, int XC, bool WIDE>
-__device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NST], uint8_t* const (&X)[S::NST],
+__device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NST], uint8_t* const (&X)[S::NSX],
                                           f8_f16 (&out)[S::NB][S::NJ]) {
-    constexpr int NST = S::NST, NB = S::NB, NJ = S::NJ, TW = S::W, TWC = S::WQ;
+    constexpr int NST = S::NST, NSX = S::NSX, NB = S::NB, NJ = S::NJ, TW = S::W, TWC = S::WQ;
     const int wave = wave_index(), mh = wave / S::GN, wn = wave % S::GN;
     const F8Lane fl = tile_lane(lane_id());
     constexpr int NC = TWC + XC;
@@ -147,19 +153,32 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
 #pragma unroll
     for (int i = 0; i < L; ++i) __asm__ volatile("" : "+v"(g.eoff[i]));
     const __amdgpu_buffer_rsrc_t wr = tile_buffer(g.wbase), xr = tile_buffer(g.xbase), er = tile_buffer(g.ebase);
-    auto issue = [&](uint8_t* w, uint8_t* x, int kb) {
-        const int k0 = min(kb, last) * F8_BLK;  // (stages past the end re-read the last; not used)
+    // (stages past the end re-read the last; not used)
+    auto issue_w = [&](auto ss, int kb) {
+        uint8_t* w = W[decltype(ss)::value % NST];
 #pragma unroll
-        for (int q = 0; q < TWC; ++q) buffer_copy16(wr, g.woff[q], k0, w + (q * TW + wave) * 1024);
+        for (int q = 0; q < TWC; ++q) buffer_copy16(wr, g.woff[q], min(kb, last) * F8_BLK, w + (q * TW + wave) * 1024);
+    };
+    auto issue_x = [&](auto ss, int kb) {
+        uint8_t* x = X[decltype(ss)::value % NSX];
 #pragma unroll
-        for (int q = 0; q < XC; ++q) buffer_copy16(xr, g.xoff[q], k0, x + (q * TW + wave) * 1024);
+        for (int q = 0; q < XC; ++q) buffer_copy16(xr, g.xoff[q], min(kb, last) * F8_BLK, x + (q * TW + wave) * 1024);
+    };
+    // what stage n (at step kb) sends for
+    auto issue = [&](auto nn, int kb) {
+        constexpr int n = decltype(nn)::value;
+        issue_x(ic<n + NSX - 1>(), kb + NSX - 1);
+        issue_w(ic<n + NST - 1>(), kb + NST - 1);
     };
     uint32_t ev[NB], en[NB];
 #pragma unroll
     for (int i = 0; i < L; ++i) en[i] = __builtin_amdgcn_raw_buffer_load_b32(er, (int)g.eoff[i], 0, 0);
     if (nfull > 0) {
-#pragma unroll
-        for (int s = 0; s < NST - 1; ++s) issue(W[s], X[s], s);
+        each<NST - 1>([&](auto ww) {  // in the order of the loop
+            constexpr int w = decltype(ww)::value, x = w - (NST - NSX);
+            if constexpr (x >= 0) issue_x(ic<x>(), x);
+            issue_w(ww, w);
+        });
     }
     // Weight scales of the WIDE loop: at the top of a round lane l holds those of
     // the round's stage l.  (Scalar loads count with the LDS reads, out of order,
@@ -174,8 +193,8 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
     each<NB * NJ>([&](auto b) { acc[decltype(b)::value / NJ][decltype(b)::value % NJ] = f8_f16{}; });
     // WIDE: the products of LDS stage B; byte SEL of ev scales the activation
     // rows, lane LN of sl the weight rows
-    auto products_wide = [&](auto bb, auto ss, auto ll) {
-        constexpr int B = decltype(bb)::value, SEL = decltype(ss)::value, LN = decltype(ll)::value;
+    auto products_wide = [&](auto nn, auto ll) {
+        constexpr int n = decltype(nn)::value, B = n % NST, BX = n % NSX, SEL = n % 4, LN = decltype(ll)::value;
         const float s0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sl[0]), LN));
         const float s1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sl[1]), LN));
         // (opaque: addresses formed from them are not kept over the loop, where
@@ -195,8 +214,8 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         });
         each<L>([&](auto ii) {
             constexpr int i = decltype(ii)::value;
-            const F8Row x0 = tile_row(X[B] + 32 * S::GM * i * F8_BLK, fl, xo, 0);
-            const F8Row x1 = tile_row(X[B] + 32 * S::GM * i * F8_BLK, fl, xo, 1);
+            const F8Row x0 = tile_row(X[BX] + 32 * S::GM * i * F8_BLK, fl, xo, 0);
+            const F8Row x1 = tile_row(X[BX] + 32 * S::GM * i * F8_BLK, fl, xo, 1);
             const F8Wide v0 = f8_widen(x0.a, x0.b), v1 = f8_widen(x1.a, x1.b);
             const float sx = f8_scale_value((ev[i] >> (8 * SEL)) & 255u);
             each<NJ>([&](auto jj) {
@@ -231,8 +250,8 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         const f8_f16 s = f8_f16{a, a, a, a, a, a, a, a, a, a, a, a, a, a, a, a};
         acc[i][j] = __builtin_elementwise_fma(s, pend, acc[i][j]);
     };
-    auto products = [&](auto bb, auto ss, auto more, int kb) {
-        constexpr int B = decltype(bb)::value, SEL = decltype(ss)::value;
+    auto products = [&](auto nn, auto more, int kb) {
+        constexpr int n = decltype(nn)::value, B = n % NST, BX = n % NSX, SEL = n % 4;
         constexpr bool MORE = decltype(more)::value != 0;  // a stage of the loop, which sends for a later one
         uint32_t wo = S::WR * wn * F8_BLK, xo = 32 * mh * F8_BLK;
         __asm__ volatile("" : "+s"(wo), "+s"(xo));
@@ -240,7 +259,7 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         each<2>([&](auto hh) {  // in the order of use
             constexpr int h = decltype(hh)::value;
             w[0][h] = tile_row(W[B], fl, wo, h);
-            x[h] = tile_row(X[B], fl, xo, h);
+            x[h] = tile_row(X[BX], fl, xo, h);
         });
         each<2 * (NJ - 1)>([&](auto q) {
             constexpr int j = 1 + decltype(q)::value / 2, h = decltype(q)::value % 2;
@@ -257,11 +276,11 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
             p = f8_mfma32<SEL>(f8_join(w[j][1].a, w[j][1].b), f8_join(x[1].a, x[1].b), p, ev[i]);
             pin();
             if constexpr (j == NJ - 1 && i + 1 < L) {  // the next activation block's rows
-                x[0] = tile_row(X[B] + 32 * S::GM * (i + 1) * F8_BLK, fl, xo, 0);
-                x[1] = tile_row(X[B] + 32 * S::GM * (i + 1) * F8_BLK, fl, xo, 1);
+                x[0] = tile_row(X[BX] + 32 * S::GM * (i + 1) * F8_BLK, fl, xo, 0);
+                x[1] = tile_row(X[BX] + 32 * S::GM * (i + 1) * F8_BLK, fl, xo, 1);
             }
             if constexpr (b == 0) {
-                if constexpr (MORE) issue(W[(B + NST - 1) % NST], X[(B + NST - 1) % NST], kb + NST - 1);
+                if constexpr (MORE) issue(nn, kb);
                 retire(ic<(L > 0 ? L * NJ - 1 : 0)>(), q0, q1);
                 if constexpr (MORE) {
                     t0 = f8_uniform(g.sp[0], min(kb + 1, g.nst - 1));
@@ -283,13 +302,14 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         wait_lgkm0();
     };
     auto stage = [&](auto nn, int kb) {
-        constexpr int n = decltype(nn)::value, B = n % NST, SEL = n % 4;
-        wait_vm<(NST - 2) * NC>();
+        constexpr int n = decltype(nn)::value, SEL = n % 4;
+        // all but the copies sent after this stage's last
+        wait_vm<NSX == NST ? (NST - 2) * NC : TWC + (NSX - 2) * NC>();
         barrier_nofence();
         if constexpr (!WIDE && L > 0) {
-            products(ic<B>(), ic<SEL>(), ic<1>(), kb);
+            products(nn, ic<1>(), kb);
         } else {
-            issue(W[(B + NST - 1) % NST], X[(B + NST - 1) % NST], kb + NST - 1);
+            issue(nn, kb);
             if constexpr (SEL == 0) {
 #pragma unroll
                 for (int i = 0; i < L; ++i) {
@@ -297,7 +317,7 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
                     en[i] = __builtin_amdgcn_raw_buffer_load_b32(er, (int)g.eoff[i], kb + 4 < g.nst ? kb + 4 : 0, 0);
                 }
             }
-            if constexpr (L > 0) products_wide(ic<B>(), ic<SEL>(), nn);
+            if constexpr (L > 0) products_wide(nn, nn);
         }
     };
     // twelve (four) stages run through every pair of LDS stage and scale byte
@@ -333,11 +353,11 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         wait_vm<0>();
         barrier_nofence();
         if constexpr (!WIDE && L > 0) {
-            products(ic<0>(), ic<0>(), ic<0>(), nfull);
+            products(ic<0>(), ic<0>(), nfull);
         } else if constexpr (L > 0) {
             sl[0] = g.sp[0][nfull];
             sl[1] = g.sp[1][nfull];
-            products_wide(ic<0>(), ic<0>(), ic<0>());
+            products_wide(ic<0>(), ic<0>());
         }
     }
     if constexpr (!WIDE && L > 0) retire(ic<(L > 0 ? L * NJ - 1 : 0)>(), q0, q1);
@@ -351,7 +371,7 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
 // Runs the loop built for this wavefront's live blocks (rows of the tile: nrows).
 template <class S, bool WIDE>
 __device__ __forceinline__ void tile_run(const F8Tile<S>& g, int nrows, uint8_t* const (&W)[S::NST],
-                                         uint8_t* const (&X)[S::NST], f8_f16 (&acc)[S::NB][S::NJ]) {
+                                         uint8_t* const (&X)[S::NSX], f8_f16 (&acc)[S::NB][S::NJ]) {
     const int wave = wave_index(), nblk = (nrows + 31) / 32, live = (nblk - wave / S::GN + S::GM - 1) / S::GM;
     auto run = [&](auto l, auto xc) { tile_loop<S, decltype(l)::value, decltype(xc)::value, WIDE>(g, W, X, acc); };
     static_assert(S::GM == 2, "two wavefronts along the activation rows");
@@ -378,25 +398,29 @@ __device__ __forceinline__ void tile_run(const F8Tile<S>& g, int nrows, uint8_t*
     __shared__ __attribute__((aligned(1024))) uint8_t W3[S::NST > 3 ? S::WB : 16];             \
     __shared__ __attribute__((aligned(1024))) uint8_t X0[S::XB];                               \
     __shared__ __attribute__((aligned(1024))) uint8_t X1[S::XB];                               \
-    __shared__ __attribute__((aligned(1024))) uint8_t X2[S::NST > 2 ? S::XB : 16];             \
-    __shared__ __attribute__((aligned(1024))) uint8_t X3[S::NST > 3 ? S::XB : 16];             \
+    __shared__ __attribute__((aligned(1024))) uint8_t X2[S::NSX > 2 ? S::XB : 16];             \
+    __shared__ __attribute__((aligned(1024))) uint8_t X3[S::NSX > 3 ? S::XB : 16];             \
     uint8_t* const WS[4] = {W0, W1, W2, W3};                                                   \
     uint8_t* const XS[4] = {X0, X1, X2, X3}
+
+// f(the first N of S)
+template <int N, class F>
+__device__ __forceinline__ void ring(uint8_t* const (&S)[4], F f) {
+    if constexpr (N == 2) {
+        uint8_t* const R[2] = {S[0], S[1]};
+        f(R);
+    } else if constexpr (N == 3) {
+        uint8_t* const R[3] = {S[0], S[1], S[2]};
+        f(R);
+    } else {
+        f(S);
+    }
+}
 
 template <class S, bool WIDE>
 __device__ __forceinline__ void tile_go(const F8Tile<S>& g, int nrows, uint8_t* const (&WS)[4], uint8_t* const (&XS)[4],
                                         f8_f16 (&acc)[S::NB][S::NJ]) {
-    if constexpr (S::NST == 2) {
-        uint8_t* const W[2] = {WS[0], WS[1]};
-        uint8_t* const X[2] = {XS[0], XS[1]};
-        tile_run<S, WIDE>(g, nrows, W, X, acc);
-    } else if constexpr (S::NST == 3) {
-        uint8_t* const W[3] = {WS[0], WS[1], WS[2]};
-        uint8_t* const X[3] = {XS[0], XS[1], XS[2]};
-        tile_run<S, WIDE>(g, nrows, W, X, acc);
-    } else {
-        tile_run<S, WIDE>(g, nrows, WS, XS, acc);
-    }
+    ring<S::NST>(WS, [&](auto& W) { ring<S::NSX>(XS, [&](auto& X) { tile_run<S, WIDE>(g, nrows, W, X, acc); }); });
 }
 
 // Results to memory through LDS, so that eight lanes store 128 consecutive bytes
@@ -718,7 +742,7 @@ static void dense_tile_launch_out(const BlockArgs& a, hipStream_t st) {
 hipError_t launch_block_matmul_tile(const BlockArgs& a, hipStream_t st) {
     auto tiles = [&](int bm, int tn) { return (long)((a.m + bm - 1) / bm) * ((a.n + tn - 1) / tn); };
     if (a.odt == MOE_DT_F32 && tiles(128, 256) >= 256) dense_tile_launch<Rows128, MOE_DT_F32>(a, st);
-    else if (a.odt == MOE_DT_BF16 && tiles(256, 256) >= 192) dense_tile_launch<Rows256, MOE_DT_BF16>(a, st);
+    else if (a.odt == MOE_DT_BF16 && tiles(256, 256) >= 192) dense_tile_launch<Square256, MOE_DT_BF16>(a, st);
     else if (tiles(128, 128) >= 192) dense_tile_launch_out<Square128>(a, st);
     else dense_tile_launch_out<Square64>(a, st);
     return hipGetLastError();
