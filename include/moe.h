@@ -277,7 +277,8 @@ int moe_quantize_rows(const void *x, int32_t x_dtype, int32_t rows, int32_t cols
 
 /* out [m, n] = x [m, k] w[n, k]^T with e4m3 operands:
  *   out[i, j] = sum_b s_x[i, b] * s_w[j / 128, b] * sum_{c in block b} q_x[i, c] * q_w[j, c]
- * (b: the blocks of 128 columns; sums as above).  x is MOE_DT_F8B128 codes with
+ * (b: the blocks of 128 columns; sums as above; s_x times a block's sum must stay
+ * within fp32's range).  x is MOE_DT_F8B128 codes with
  * x_scale [m, MOE_F8_SCALE_LD(k)] as moe_quantize_rows writes them, or
  * MOE_DT_BF16 / MOE_DT_F32 rows, which are quantised that way first (x_scale
  * NULL, workspace needed).  w [n, k] codes, w_scale [ceil(n/128), ceil(k/128)]

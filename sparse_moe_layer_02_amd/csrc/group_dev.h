@@ -17,7 +17,8 @@
 // SIMD for 65536 tokens (256 experts, 8 groups, top-8: 96 us with the library
 // exponential and division and one lane scanning each group, 80 us here, about
 // 600 vector instructions a token; a bitwise search for the k-th key over
-// ballots in place of the k rounds took as many).
+// ballots in place of the k rounds took as many).  group_select.hip puts four
+// tokens into a wavefront where there are that many (54 us).
 #pragma once
 #include "common.h"
 #include "kernels.h"
@@ -63,6 +64,58 @@ __device__ __forceinline__ double rcp_f64(double d) {
     return __fma_rn(__fma_rn(-d, r, 1.0), r, r);
 }
 
+// Logits sc[j] to scores; in(j): sc[j] is a real expert's (others hold -inf).
+// rmax, rsum: maximum of an orderable word and fp64 sum over the lanes that
+// share the token.
+template <int N, class In, class Max, class Sum>
+__device__ __forceinline__ void group_scores(float (&sc)[N], int score_kind, In in, Max rmax, Sum rsum) {
+    if (score_kind == MOE_SCORE_SOFTMAX) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < N; ++j) m = fmaxf(m, sc[j]);
+        // (DPP shifts read 0 from outside a row; the maximum of the non-negative
+        // and the negative part is taken on orderable integers instead)
+        const uint32_t mu = __float_as_uint(m);
+        const uint32_t om = rmax((mu & 0x80000000u) ? ~mu : (mu | 0x80000000u));
+        m = unpack_ord(om);
+        double ex[N], sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const double x = (double)sc[j] - (double)m;  // NaN for a NaN logit, and for all if m is infinite
+            ex[j] = in(j) ? (x != x ? x : exp_f64(x)) : 0.0;
+            sum += ex[j];
+        }
+        sum = rsum(sum);
+        const double inv = sum != sum ? sum : rcp_f64(sum);  // sum >= 1
+#pragma unroll
+        for (int j = 0; j < N; ++j) sc[j] = (float)(ex[j] * inv);
+    } else if (score_kind == MOE_SCORE_SIGMOID) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float s = (float)rcp_f64(1.0 + exp_f64(-(double)sc[j]));
+            sc[j] = sc[j] != sc[j] ? sc[j] : s;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) sc[j] = router_score(score_kind, sc[j]);
+    }
+}
+
+// Orderable score of a group from its two best keys, then the lower group.
+__device__ __forceinline__ uint64_t group_key(uint32_t b0, uint32_t b1, bool two, int grp) {
+    const float best = unpack_ord(b0);
+    return pack_key(two ? best + unpack_ord(b1) : best, grp);
+}
+__device__ __forceinline__ void merge_best2(uint32_t& b0, uint32_t& b1, uint32_t c0, uint32_t c1) {
+    b1 = max(min(b0, c0), max(b1, c1));
+    b0 = max(b0, c0);
+}
+// Weight of a selected score (S: the sum of the selected ones).
+__device__ __forceinline__ float group_weight(float s, double S, float route_scale, int normalise) {
+    const double num = (double)s * (double)route_scale;
+    return !normalise ? (float)num : S > 0.0 ? (float)(((double)s / S) * (double)route_scale) : 0.0f;
+}
+
 // keys: E words of LDS of this wavefront's own.  Returns the expert of rank
 // `lane` in lanes 0..k-1, its weight in *w_lane.
 template <int KPL>
@@ -75,36 +128,8 @@ __device__ __forceinline__ int group_topk_token(const float* __restrict__ lrow, 
     uint64_t key[KPL];
 #pragma unroll
     for (int j = 0; j < KPL; ++j) sc[j] = lane + WAVE * j < E ? lrow[lane + WAVE * j] : -INFINITY;
-    if (score_kind == MOE_SCORE_SOFTMAX) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) m = fmaxf(m, sc[j]);
-        // (DPP shifts read 0 from outside a row; the maximum of the non-negative
-        // and the negative part is taken on orderable integers instead)
-        const uint32_t mu = __float_as_uint(m);
-        const uint32_t om = wave_max_u32((mu & 0x80000000u) ? ~mu : (mu | 0x80000000u));
-        m = unpack_ord(om);
-        double ex[KPL], sum = 0.0;
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) {
-            const double x = (double)sc[j] - (double)m;  // NaN for a NaN logit, and for all if m is infinite
-            ex[j] = lane + WAVE * j < E ? (x != x ? x : exp_f64(x)) : 0.0;
-            sum += ex[j];
-        }
-        sum = wave_sum_f64(sum);
-        const double inv = sum != sum ? sum : rcp_f64(sum);  // sum >= 1
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) sc[j] = (float)(ex[j] * inv);
-    } else if (score_kind == MOE_SCORE_SIGMOID) {
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) {
-            const float s = (float)rcp_f64(1.0 + exp_f64(-(double)sc[j]));
-            sc[j] = sc[j] != sc[j] ? sc[j] : s;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) sc[j] = router_score(score_kind, sc[j]);
-    }
+    group_scores<KPL>(sc, score_kind, [&](int j) { return lane + WAVE * j < E; },
+                      [](uint32_t v) { return wave_max_u32(v); }, [](double v) { return wave_sum_f64(v); });
 #pragma unroll
     for (int j = 0; j < KPL; ++j) {
         const int e = lane + WAVE * j;
@@ -132,12 +157,9 @@ __device__ __forceinline__ int group_topk_token(const float* __restrict__ lrow, 
         }
         for (int o = 1; o < lpg; o *= 2) {
             const uint32_t c0 = (uint32_t)__shfl_xor((int)b0, o), c1 = (uint32_t)__shfl_xor((int)b1, o);
-            b1 = max(min(b0, c0), max(b1, c1));
-            b0 = max(b0, c0);
+            merge_best2(b0, b1, c0, c1);
         }
-        const float best = unpack_ord(b0);
-        const uint64_t mine =  // orderable score, then the lower group
-            grp_l < g.n_group ? pack_key(g.group_top == 2 && S > 1 ? best + unpack_ord(b1) : best, grp_l) : 0ull;
+        const uint64_t mine = grp_l < g.n_group ? group_key(b0, b1, g.group_top == 2 && S > 1, grp_l) : 0ull;
         int rank = 0;
         for (int q = 0; q < g.n_group; ++q) {
             const uint64_t o = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(mine >> 32), q * lpg) << 32) |
@@ -199,8 +221,7 @@ __device__ __forceinline__ int group_topk_token(const float* __restrict__ lrow, 
             my_s = s_sel;
         }
     }
-    const double num = (double)my_s * (double)route_scale;
-    const float w = !g.normalise ? (float)num : S > 0.0 ? (float)(((double)my_s / S) * (double)route_scale) : 0.0f;
+    const float w = group_weight(my_s, S, route_scale, g.normalise);
     if (lane < k) {
         idx_out[lane] = my_idx;
         w_out[lane] = w;

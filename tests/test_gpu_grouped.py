@@ -94,6 +94,36 @@ def test_many_groups(dev, G, E):
         check(idx.cpu().numpy(), w.cpu().numpy(), *R.select(l, None, k, "sigmoid", 1.0, G, tg, top, True), "G=%d" % G)
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid", "sqrt_softplus"])
+@pytest.mark.parametrize("E,G,tg,top,k", [(64, 16, 5, 2, 16), (64, 1, 1, 1, 1), (128, 8, 3, 2, 8), (192, 4, 1, 1, 13),
+                                          (256, 8, 4, 2, 8), (256, 1, 1, 1, 16), (256, 32, 9, 2, 8), (256, 2, 1, 2, 17)])
+def test_many_tokens(dev, E, G, tg, top, k, kind):
+    """Four tokens per wavefront (and the sizes beside it), a ragged last wavefront, the selection order's
+    corners throughout, logits and bias that start 4 bytes off; the rows behind the last stay as they were."""
+    torch, moe = dev
+    rng = np.random.default_rng(E + G + k)
+    T = 8192 + 5
+    few = logits_of(400, E, rng)
+    few[200:, :] = rng.integers(-3, 4, (200, E)) / 2.0  # ties
+    pick = rng.integers(0, 400, T)
+    pick[-13:] = np.arange(13)
+    l = few[pick]
+    bias = (rng.integers(-2, 3, E) / 8.0).astype(np.float32)
+    say("many tokens", E, G, tg, top, k, kind)
+    lg, bs = torch.empty(T * E + 1, device="cuda")[1:], torch.empty(E + 1, device="cuda")[1:]
+    lg.copy_(torch.from_numpy(l.reshape(-1)))
+    bs.copy_(torch.from_numpy(bias))
+    for b, norm in ((bs, True), (None, False)):
+        c = moe.make_config(T, 64, E, k, 64, n_shared=0, score=kind, route_scale=1.5)
+        idx = torch.full((T + 4, k), -7, dtype=torch.int32, device="cuda")
+        w = torch.full((T + 4, k), -7.0, device="cuda")
+        moe.moe_select_grouped(c, moe.make_groups(G, tg, top, norm), lg.view(T, E), b, idx[:T], w[:T])
+        torch.cuda.synchronize()
+        assert (idx[T:] == -7).all() and (w[T:] == -7).all()
+        ri, rw = R.select(few, None if b is None else bias, k, kind, 1.5, G, tg, top, norm)
+        check(idx[:T].cpu().numpy(), w[:T].cpu().numpy(), ri[pick], rw[pick], "T=%d" % T)
+
+
 def test_flat_groups_equal_select(dev):
     """groups = None and {1, 1, 1, 1} are moe_select, bit for bit."""
     torch, moe = dev
