@@ -98,8 +98,13 @@ int n_dslots_of(const moe_config* c) {
     return c->n_shared + (n < c->n_expert ? n : c->n_expert);
 }
 
-Layout make_layout(const moe_config* c) {
-    Layout L;
+// With the rows of x and h as codes and scale bytes (e4m3 layers).
+struct LayerLayout : Layout {
+    size_t xq, xe, hq, he;
+};
+
+LayerLayout make_layout(const moe_config* c) {
+    LayerLayout L;
     const size_t T = (size_t)c->n_tokens, E = (size_t)c->n_expert, k = (size_t)c->top_k;
     const size_t d = (size_t)c->d_model, n = T * k;
     const size_t hsz = c->act_dtype == MOE_DT_BF16 ? 2 : 4;
@@ -169,7 +174,7 @@ int device_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_DEVI
 
 MatRef ref(const moe_mat& m) { return MatRef{m.q, static_cast<const uint16_t*>(m.scale)}; }
 
-PermArgs perm_args(const moe_config* c, const Layout& L, void* ws, const int32_t* idx, int32_t* off,
+PermArgs perm_args(const moe_config* c, const LayerLayout& L, void* ws, const int32_t* idx, int32_t* off,
                    int32_t* perm, int32_t* inv) {
     PermArgs p;
     p.topk_idx = idx;
@@ -190,7 +195,7 @@ PermArgs perm_args(const moe_config* c, const Layout& L, void* ws, const int32_t
     return p;
 }
 
-FfnArgs ffn_args(const moe_config* c, const Layout& L, void* ws, const void* x, const moe_weights* w,
+FfnArgs ffn_args(const moe_config* c, const LayerLayout& L, void* ws, const void* x, const moe_weights* w,
                  const int32_t* off, const int32_t* perm, const float* topk_w) {
     FfnArgs f;
     f.x = x;
@@ -251,18 +256,18 @@ hipError_t run_bf16_experts(const FfnArgs& f, hipStream_t st, const KTime& kg = 
 }
 
 // e4m3 experts over the quantised rows of x: gate/up (which quantises h), down.
-QuantArgs f8_quant_args(const moe_config* c, const Layout& L, void* ws, const void* x) {
+QuantArgs f8_quant_args(const moe_config* c, const LayerLayout& L, void* ws, const void* x) {
     return QuantArgs{x, MOE_DT_BF16, c->n_tokens, c->d_model, c->d_model, at<uint8_t>(ws, L.xq), at<uint8_t>(ws, L.xe)};
 }
 
-hipError_t run_f8_experts(const FfnArgs& f, const Layout& L, void* ws, hipStream_t st, const KTime& kg = KTime(),
+hipError_t run_f8_experts(const FfnArgs& f, const LayerLayout& L, void* ws, hipStream_t st, const KTime& kg = KTime(),
                           const KTime& kd = KTime()) {
     const F8Ffn a{f, at<uint8_t>(ws, L.xq), at<uint8_t>(ws, L.xe), at<uint8_t>(ws, L.hq), at<uint8_t>(ws, L.he)};
     const hipError_t e = launch_f8_gateup(a, st, kg);
     return e == hipSuccess ? launch_f8_down(a, st, kd) : e;
 }
 
-hipError_t run_expert_kernels(const FfnArgs& f, const Layout& L, void* ws, hipStream_t st,
+hipError_t run_expert_kernels(const FfnArgs& f, const LayerLayout& L, void* ws, hipStream_t st,
                               const KTime& kg = KTime(), const KTime& kd = KTime()) {
     hipError_t e;
     if (f.wdt == MOE_DT_BF16) return run_bf16_experts(f, st, kg, kd);
@@ -407,7 +412,7 @@ int moe_route_grouped(const moe_config* cfg, const moe_groups* groups, const voi
         !elt_ok(topk_w))
         return MOE_ERR_INVALID;
     if (!logits && (s = check_ws(cfg, ws, ws_bytes))) return s;
-    const Layout L = make_layout(cfg);
+    const LayerLayout L = make_layout(cfg);
     float* lg = logits ? logits : at<float>(ws, L.logits);
     hipStream_t st = static_cast<hipStream_t>(stream);
     RouteArgs r{x, w_router, cfg->n_tokens, cfg->d_model, cfg->n_expert, cfg->act_dtype, lg,
@@ -559,7 +564,7 @@ int moe_permute(const moe_config* cfg, const int32_t* topk_idx, int32_t* offsets
     if (s) return s;
     if (!elt_ok(topk_idx) || !elt_ok(offsets) || !elt_ok(perm_rows) || !elt_ok(inv_perm)) return MOE_ERR_INVALID;
     if ((s = check_ws(cfg, ws, ws_bytes))) return s;
-    const Layout L = make_layout(cfg);
+    const LayerLayout L = make_layout(cfg);
     PermArgs p = perm_args(cfg, L, ws, topk_idx, offsets, perm_rows, inv_perm);
     return device_status(launch_permute(p, static_cast<hipStream_t>(stream)));
 }
@@ -574,7 +579,7 @@ int moe_expert_ffn(const moe_config* cfg, const void* x, const moe_weights* w, c
         return MOE_ERR_INVALID;
     if (cfg->n_shared && !ptr_ok(shared_out)) return MOE_ERR_INVALID;
     if ((s = check_ws(cfg, ws, ws_bytes))) return s;
-    const Layout L = make_layout(cfg);
+    const LayerLayout L = make_layout(cfg);
     hipStream_t st = static_cast<hipStream_t>(stream);
     PermArgs p = perm_args(cfg, L, ws, nullptr, const_cast<int32_t*>(offsets), const_cast<int32_t*>(perm_rows),
                            nullptr);
@@ -635,7 +640,7 @@ int enqueue_layer(const moe_config* cfg, const GroupArgs& g, const void* x, cons
     const bool decode = cfg->w_dtype != MOE_DT_F8B128 &&  // (e4m3 layers have one path)
                         (cfg->path == MOE_PATH_DECODE ||
                          (cfg->path == MOE_PATH_AUTO && cfg->n_tokens <= MOE_DECODE_MAX_TOKENS));
-    const Layout L = make_layout(cfg);
+    const LayerLayout L = make_layout(cfg);
     hipStream_t st = static_cast<hipStream_t>(stream);
 
     float* logits = dbg && dbg->logits ? dbg->logits : at<float>(ws, L.logits);

@@ -138,7 +138,7 @@ __device__ __forceinline__ uint64_t lanemask_lt() {
 // ---------------------------------------------------------------------------
 struct Layout {
     size_t logits, topk_idx, topk_w, offsets, perm_rows, inv_perm;
-    size_t blk_hist, blk_base, meta, active, tiles, h, slot_out, shared_out, scores, dslots, xq, xe, hq, he, total;
+    size_t blk_hist, blk_base, meta, active, tiles, h, slot_out, shared_out, scores, dslots, total;
     int n_blk;       // permutation blocks of PERM_BLOCK assignments
     int max_tiles;   // capacity of the grouped-GEMM tile list
 };
