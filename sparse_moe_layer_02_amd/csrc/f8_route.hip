@@ -10,8 +10,9 @@
 // 2. Selection, token->expert grouping and the quantisation of x.  Each is
 // microseconds of latency for a single workgroup's work, and the expert
 // kernels wait for all three; in launches of their own they took 15 us of a
-// one-token layer's 96.  Workgroup 0 selects (a wavefront per token) and groups (permute_dev.h, over
-// the indices it keeps in LDS); the others quantise the rows of x.
+// one-token layer's 96.  Workgroup 0 selects (a wavefront per token) and groups
+// (permute_dev.h, over the indices it keeps in LDS); the others quantise the
+// rows of x: 8.3 us (10.1 with a scan each for offsets, experts and tiles).
 #include "common.h"
 #include "group_dev.h"
 #include "kernels.h"
@@ -65,7 +66,7 @@ __global__ __launch_bounds__(FR_WAVES * WAVE) void f8_router_kernel(const uint16
     }
 }
 
-static_assert(FR_WAVES * WAVE == 1024, "permute_dev.h's list emitter wants 1024 threads");
+static_assert(FR_WAVES * WAVE == 1024 && F8_ROUTE_MAX_T * 32 < 1024, "emit_lists_few: threads, assignments");
 
 template <int KPL>
 __global__ __launch_bounds__(FR_WAVES * WAVE) void f8_route_kernel(SelectArgs s, GroupArgs g, bool grouped, PermArgs p,
@@ -95,7 +96,7 @@ __global__ __launch_bounds__(FR_WAVES * WAVE) void f8_route_kernel(SelectArgs s,
     if (tid < n) atomicAdd(&cnt[s_idx[tid]], 1);
     __syncthreads();
     int off;
-    emit_lists(p, cnt[tid], smem, &off);
+    emit_lists_few(p, cnt[tid], smem, &off);
     cnt[tid] = off;  // becomes the scatter cursor
     __syncthreads();
     if (tid < WAVE) scatter_range(p, 0, n, cnt);

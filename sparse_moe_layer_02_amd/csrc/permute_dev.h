@@ -60,36 +60,58 @@ __device__ __forceinline__ void multisplit_rank(int e, bool valid, int nbits, in
     *leader = __ffsll((unsigned long long)peers) - 1;
 }
 
+// Where an expert's entries of the lists begin, and the lists' totals.
+struct ListPos {
+    int off, apos, tbase;           // of this thread's expert
+    int total, n_active, n_rtiles;  // of all
+};
+
 // Lists derived from the expert counts: offsets, active experts, GEMM tiles.
 // Called by all 1024 threads; thread e < E holds count c.  `own` = this call
 // produced the permutation (write offsets and the perm_rows tail), as opposed
 // to deriving the lists from a caller's offsets.
-__device__ void emit_lists(const PermArgs& a, int c, int* smem, int* off_out, bool own = true) {
-    const int e = threadIdx.x, E = a.E;
-    int total, n_active, n_rtiles;
-    const int off = block_excl_scan_1024(e < E ? c : 0, smem, &total);
-    const int act = (e < E && c > 0) ? 1 : 0;
-    const int apos = block_excl_scan_1024(act, smem, &n_active);
-    const int nt = (e < E && a.bm > 0) ? (c + a.bm - 1) / a.bm : 0;  // bm == 0: no tile list
-    const int tbase = block_excl_scan_1024(nt, smem, &n_rtiles);
+__device__ __forceinline__ int list_tiles(const PermArgs& a, int c) {  // (bm == 0: no tile list)
+    return ((int)threadIdx.x < a.E && a.bm > 0) ? (c + a.bm - 1) / a.bm : 0;
+}
+__device__ __forceinline__ void emit_lists_at(const PermArgs& a, int c, const ListPos& p, bool own) {
+    const int e = threadIdx.x, E = a.E, nt = list_tiles(a, c);
     if (e < E) {
-        if (own) a.offsets[e] = off;
-        if (act) a.active[apos] = e;
-        for (int i = 0; i < nt; ++i) a.tiles[tbase + i] = make_int2(e, i * a.bm);
+        if (own) a.offsets[e] = p.off;
+        if (c > 0) a.active[p.apos] = e;
+        for (int i = 0; i < nt; ++i) a.tiles[p.tbase + i] = make_int2(e, i * a.bm);
     }
     const int s_tiles = (a.n_shared && a.bm > 0) ? (a.T + a.bm - 1) / a.bm : 0;
-    for (int i = e; i < s_tiles; i += blockDim.x) a.tiles[n_rtiles + i] = make_int2(E, i * a.bm);
+    for (int i = e; i < s_tiles; i += blockDim.x) a.tiles[p.n_rtiles + i] = make_int2(E, i * a.bm);
     if (e == 0) {
-        if (own) a.offsets[E] = total;
-        a.meta[0] = n_active;
-        a.meta[1] = n_rtiles + s_tiles;
-        a.meta[2] = total;
+        if (own) a.offsets[E] = p.total;
+        a.meta[0] = p.n_active;
+        a.meta[1] = p.n_rtiles + s_tiles;
+        a.meta[2] = p.total;
     }
     if (own) {
         const int n = a.T * a.k;
-        for (int r = total + e; r < n; r += blockDim.x) a.perm_rows[r] = -1;
+        for (int r = p.total + e; r < n; r += blockDim.x) a.perm_rows[r] = -1;
     }
-    *off_out = off;
+}
+__device__ void emit_lists(const PermArgs& a, int c, int* smem, int* off_out, bool own = true) {
+    const int e = threadIdx.x, E = a.E;
+    ListPos p;
+    p.off = block_excl_scan_1024(e < E ? c : 0, smem, &p.total);
+    p.apos = block_excl_scan_1024((e < E && c > 0) ? 1 : 0, smem, &p.n_active);
+    p.tbase = block_excl_scan_1024(list_tiles(a, c), smem, &p.n_rtiles);
+    emit_lists_at(a, c, p, own);
+    *off_out = p.off;
+}
+// The same with one scan, for fewer than 1024 assignments (every count and sum
+// fits 10 bits).
+__device__ void emit_lists_few(const PermArgs& a, int c, int* smem, int* off_out) {
+    const int e = threadIdx.x;
+    const int v = e < a.E ? c | (c > 0) << 10 | list_tiles(a, c) << 20 : 0;
+    int sum;
+    const int at = block_excl_scan_1024(v, smem, &sum);
+    const ListPos p{at & 1023, at >> 10 & 1023, at >> 20, sum & 1023, sum >> 10 & 1023, sum >> 20};
+    emit_lists_at(a, c, p, true);
+    *off_out = p.off;
 }
 
 // Stable scatter of assignments [f0, f1) by one wave, cursors in LDS.
