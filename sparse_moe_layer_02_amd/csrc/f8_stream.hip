@@ -1,4 +1,5 @@
-// f8_stream.hip - e4m3 products for few activation rows: out[m, n] = x_m W_n.
+// f8_stream.hip - e4m3 products for few activation rows (or few results):
+// out[m, n] = x_m W_n.
 //
 // Bound by the weight bytes, each read once, and at these sizes by latency.
 // The weights go from memory straight into the registers of the wavefront
@@ -240,12 +241,17 @@ bool block_matmul_takes(int xdt, int m, int n) {
 
 // Up to 48 rows here, more in LDS tiles (us at n x k 4096 x 6144: 1 row 9.1
 // against 20.3 for the smallest tiles, 24 rows 16.7 / 20.3, 128 rows 33.9 / 23.1;
-// 48 rows of 4096 x 4096 13.1 / 16.2, 77 rows of 6144 x 2048 16.9 / 9.9).
+// 48 rows of 4096 x 4096 13.1 / 16.2, 77 rows of 6144 x 2048 16.9 / 9.9), unless
+// the sum over k is long and there are so few results that all workgroups here
+// run at once, its eight wavefronts sharing the sum: 256 rows of 512 x 2048 7.8 /
+// 8.7 (fp32 results 7.6 / 10.8), 77 of 1024 x 6144 17.6 / 18.5 (17.2 / 25.5), but
+// 512 of 1024 x 2048 13.6 / 8.9 and, at 512 columns, 128 of 1024 5.4 / 5.1.
 hipError_t launch_block_matmul(const BlockArgs& a, hipStream_t st) {
     if (a.xdt == MOE_DT_BF16) return dense_launch<1, 1, MOE_DT_BF16>(a, st);
     if (a.xdt == MOE_DT_F32) return dense_launch<1, 1, MOE_DT_F32>(a, st);
     if (a.m <= 16) return dense_launch<1, 1, MOE_DT_F8B128>(a, st);
-    if (a.m <= 48) return dense_launch<2, 2, MOE_DT_F8B128>(a, st);
+    const bool few = (long)((a.m + 31) / 32) * ((a.n + 31) / 32) <= 256 && a.k >= 1024;
+    if (a.m <= 48 || few) return dense_launch<2, 2, MOE_DT_F8B128>(a, st);
     return launch_block_matmul_tile(a, st);
 }
 

@@ -154,7 +154,7 @@ def test_matmul(dev, m, n, k, xdt):
 # sizes whose tiles are the larger ones (128 x 128; 256 x 256 and, for fp32 results, 128 x 256), with ends in
 # rows, columns and K; K below one block; K of more blocks than a wavefront has lanes
 LARGE = [(1600, 2000, 272), (3500, 3600, 400), (70, 200, 16), (300, 70, 112), (1600, 2000, 48), (3500, 3600, 80),
-         (90, 150, 8464), (1600, 2000, 8320), (70, 132, 144), (70, 133, 144), (70, 134, 144), (70, 136, 144)]
+         (90, 150, 8464), (600, 1000, 8464), (1600, 2000, 8320), (250, 1000, 2064), (8000, 20, 1040), (70, 132, 144), (70, 133, 144), (70, 134, 144), (70, 136, 144)]
 
 
 @pytest.mark.parametrize("odt", ["bf16", "f32"])
