@@ -51,8 +51,8 @@ struct Shape {
 // Expert tiles (256 weight rows, the two scale blocks of a 128-column h block).
 // Up to 64 activation rows: two workgroups per compute unit, each with two
 // stages, so that one's start and end lie under the other's loop (gate/up of
-// 512 tokens, 16 rows per expert: 1.06 ms, 6.1 TB/s of weights; one workgroup
-// with four stages 1.35 ms).  More: a larger tile reads LDS less per product and
+// 512 tokens, 16 rows per expert: 1.00 ms, 6.5 TB/s of weights; one workgroup
+// with four stages took 1.35 ms when this took 1.06).  More: a larger tile reads LDS less per product and
 // an expert's weights fewer times; the weights, which come from HBM, are sent for
 // a stage earlier than the activation rows, most often in L2 (128 rows per
 // expert: gate/up 1.66 ms and down 1.01, both one stage ahead 1.77 and 1.03; 128
@@ -80,6 +80,7 @@ struct F8Tile {
     int ch;                       // the copy lane's 16-byte chunk in a stage row, in bytes
     const float* sp[2];           // block scales of the wavefront's weight rows (gate/up: of gate, of up)
     int K, nst;
+    bool once = false;            // no other tile reads these weights
 };
 // A wave-uniform pointer in scalar registers (where the compiler cannot see it).
 template <class P>
@@ -91,8 +92,9 @@ __device__ __forceinline__ const P* uniform_ptr(const P* p) {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_buffer(const uint8_t* p) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, 0xFFFFFFFF, 0x00020000);
 }
+template <bool NT = false>  // NT: non-temporal
 __device__ __forceinline__ void buffer_copy16(__amdgpu_buffer_rsrc_t r, uint32_t off, int k0, uint8_t* dst) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst), 16, (int)off, k0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst), 16, (int)off, k0, 0, NT ? 2 : 0);
 }
 
 // Copy lane l of copy c fills row 8 c + l / 8, slot l % 8.
@@ -132,7 +134,7 @@ __device__ __forceinline__ void each(F f) {
 
 // The K loop of one wavefront with L live blocks and XC activation copies per
 // stage; acc[i][j]: block i (activation rows) x weight row block j.
-template <class S, int L, int XC, bool WIDE>
+template <class S, int L, int XC, bool WIDE, bool ONCE>
 __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NST], uint8_t* const (&X)[S::NSX],
                                           f8_f16 (&out)[S::NB][S::NJ]) {
     constexpr int NST = S::NST, NSX = S::NSX, NB = S::NB, NJ = S::NJ, TW = S::W, TWC = S::WQ;
@@ -154,10 +156,19 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
     for (int i = 0; i < L; ++i) __asm__ volatile("" : "+v"(g.eoff[i]));
     const __amdgpu_buffer_rsrc_t wr = tile_buffer(g.wbase), xr = tile_buffer(g.xbase), er = tile_buffer(g.ebase);
     // (stages past the end re-read the last; not used)
+    // ONCE: weights that no other tile reads, as g.once says, are copied
+    // non-temporal (16 rows per expert: gate/up 1.08 ms, so 1.00, down 0.64 / 0.61;
+    // all copies so, 64 rows per expert, many in two tiles: 1.33 / 1.55 ms).
+    const bool once = ONCE && __builtin_amdgcn_readfirstlane(g.once);
     auto issue_w = [&](auto ss, int kb) {
         uint8_t* w = W[decltype(ss)::value % NST];
+        auto copies = [&](auto nt) {
 #pragma unroll
-        for (int q = 0; q < TWC; ++q) buffer_copy16(wr, g.woff[q], min(kb, last) * F8_BLK, w + (q * TW + wave) * 1024);
+            for (int q = 0; q < TWC; ++q)
+                buffer_copy16<decltype(nt)::value != 0>(wr, g.woff[q], min(kb, last) * F8_BLK, w + (q * TW + wave) * 1024);
+        };
+        if (once) copies(ic<1>());
+        else copies(ic<0>());
     };
     auto issue_x = [&](auto ss, int kb) {
         uint8_t* x = X[decltype(ss)::value % NSX];
@@ -369,11 +380,11 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
 }
 
 // Runs the loop built for this wavefront's live blocks (rows of the tile: nrows).
-template <class S, bool WIDE>
+template <class S, bool WIDE, bool ONCE>
 __device__ __forceinline__ void tile_run(const F8Tile<S>& g, int nrows, uint8_t* const (&W)[S::NST],
                                          uint8_t* const (&X)[S::NSX], f8_f16 (&acc)[S::NB][S::NJ]) {
     const int wave = wave_index(), nblk = (nrows + 31) / 32, live = (nblk - wave / S::GN + S::GM - 1) / S::GM;
-    auto run = [&](auto l, auto xc) { tile_loop<S, decltype(l)::value, decltype(xc)::value, WIDE>(g, W, X, acc); };
+    auto run = [&](auto l, auto xc) { tile_loop<S, decltype(l)::value, decltype(xc)::value, WIDE, ONCE>(g, W, X, acc); };
     static_assert(S::GM == 2, "two wavefronts along the activation rows");
     {  // a round of activation copies covers W / 4 blocks
         constexpr int RB = S::W / 4;
@@ -417,10 +428,10 @@ __device__ __forceinline__ void ring(uint8_t* const (&S)[4], F f) {
     }
 }
 
-template <class S, bool WIDE>
+template <class S, bool WIDE, bool ONCE>
 __device__ __forceinline__ void tile_go(const F8Tile<S>& g, int nrows, uint8_t* const (&WS)[4], uint8_t* const (&XS)[4],
                                         f8_f16 (&acc)[S::NB][S::NJ]) {
-    ring<S::NST>(WS, [&](auto& W) { ring<S::NSX>(XS, [&](auto& X) { tile_run<S, WIDE>(g, nrows, W, X, acc); }); });
+    ring<S::NST>(WS, [&](auto& W) { ring<S::NSX>(XS, [&](auto& X) { tile_run<S, WIDE, ONCE>(g, nrows, W, X, acc); }); });
 }
 
 // Results to memory through LDS, so that eight lanes store 128 consecutive bytes
@@ -467,6 +478,12 @@ __device__ __forceinline__ void out_rows(const uint8_t* R, int lane, E* out, siz
     }
 }
 
+// Whether a tile holds all rows of its expert.
+template <int BM>
+__device__ __forceinline__ bool one_tile(const FfnArgs& f, const TileRows& tr) {
+    return tr.g == f.E ? f.T <= BM : f.offsets[tr.g + 1] - f.offsets[tr.g] <= BM;
+}
+
 template <class S>
 __global__ __launch_bounds__(64 * S::W, S::WAVES) void f8_gateup_tile_kernel(F8Ffn a) {
     constexpr int NB = S::NB, BM = S::BM, HC = S::WR / 2, TW = S::W, TWC = S::WQ;  // h columns per wavefront
@@ -511,11 +528,12 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void f8_gateup_tile_kernel(F8F
     for (int q = 0; q < S::XQ; ++q) g.xoff[q] = (uint32_t)token(copy_row(q * TW + wave, lane)) * d + g.ch;
 #pragma unroll
     for (int i = 0; i < NB; ++i) g.eoff[i] = (uint32_t)token(32 * (mh + S::GM * i) + l32) * f8_scale_ld(d);
+    g.once = one_tile<BM>(a.f, tr);
     const size_t srow = (e * f8_blocks(F) + ntile) * g.nst;
     g.sp[0] = reinterpret_cast<const float*>(G.scale) + srow;
     g.sp[1] = reinterpret_cast<const float*>(U.scale) + srow;
     f8_f16 acc[NB][S::NJ];
-    tile_go<S, false>(g, tr.nrows, WS, XS, acc);
+    tile_go<S, false, true>(g, tr.nrows, WS, XS, acc);
     // h and its largest magnitude per row over the tile's 128 columns
     // (a wavefront has gate and up in its two blocks)
     static_assert(S::NJ == 2 && HC == 32, "a block of gate, a block of up");
@@ -587,6 +605,7 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void f8_down_tile_kernel(F8Ffn
         g.ch = copy_chunk(sr, lane);
         g.woff[q] = (uint32_t)(min(sr, d - 1 - n0) * F + g.ch);
     }
+    g.once = one_tile<BM>(a.f, tr);
     g.wbase = static_cast<const uint8_t*>(D.q) + (e * d + n0) * F;
     g.xbase = a.hq + (size_t)tr.rbeg * a.f.ldh;
     g.ebase = a.he + (size_t)tr.rbeg * f8_scale_ld(a.f.ldh);
@@ -605,7 +624,7 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void f8_down_tile_kernel(F8Ffn
     for (int j = 0; j < 2; ++j)  // (one block: both the same)
         g.sp[j] = reinterpret_cast<const float*>(D.scale) + (e * f8_blocks(d) + min(c0 + 32 * j % S::WR, d - 1) / F8_BLK) * g.nst;
     f8_f16 acc[NB][S::NJ];
-    tile_go<S, false>(g, tr.nrows, WS, XS, acc);
+    tile_go<S, false, true>(g, tr.nrows, WS, XS, acc);
     float* out = shared ? a.f.shared_out : a.f.slot_out;
     __syncthreads();  // every wavefront has read its last stage
     uint8_t* R = out_region<S>(WS, wave);
@@ -672,7 +691,7 @@ __global__ __launch_bounds__(64 * S::W) void f8_dense_tile_kernel(BlockArgs a) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) g.sp[j] = a.ws + (size_t)(min(c0 + 32 * j % S::WR, a.n - 1) / F8_BLK) * g.nst;
     f8_f16 acc[NB][S::NJ];
-    tile_go<S, OF == MOE_DT_F32>(g, nrows, WS, XS, acc);
+    tile_go<S, OF == MOE_DT_F32, false>(g, nrows, WS, XS, acc);
     __syncthreads();  // every wavefront has read its last stage
     uint8_t* R = out_region<S>(WS, wave);
     each<NB>([&](auto ii) {
