@@ -16,7 +16,10 @@
 // e8m0 scales are applied by the matrix instruction.
 //
 // WIDE: the codes are widened to bf16 and the sums are fp32 (f8_dev.h); taken
-// for fp32 results.  Otherwise the 8-bit instruction, twice the rate, for
+// for fp32 results and for gate/up of 64-row tiles, where the weight bytes set
+// the pace and it costs nothing (8 tokens 122 us against 132, 16 rows per expert
+// 1.00 ms both): a sum off by 1e-5 can move a scale of h, which shows in the few
+// rows of a small layer.  Otherwise the 8-bit instruction, twice the rate, for
 // results that are rounded to bf16 or e4m3 next.
 //
 // A tile computes only the 32-row blocks that hold rows: blocks are dealt to the
@@ -212,6 +215,25 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         // they would take registers the accumulators need)
         uint32_t wo = S::WR * wn * F8_BLK, xo = 32 * mh * F8_BLK;
         __asm__ volatile("" : "+s"(wo), "+s"(xo));
+        if constexpr (NB == 1 && NJ > 1) {
+            // two workgroups per compute unit leave 128 registers: a half row at
+            // a time, the activation rows read and widened for each weight block
+            each<NJ>([&](auto jj) {
+                constexpr int j = decltype(jj)::value;
+                f8_f16 p = f8_f16{};
+                each<2>([&](auto hh) {
+                    constexpr int h = decltype(hh)::value;
+                    const F8Row w = tile_row(W[B] + 32 * j * F8_BLK, fl, wo, h), x = tile_row(X[BX], fl, xo, h);
+                    p = f8_dot32(f8_widen(w.a, w.b), f8_widen(x.a, x.b), p);
+                    pin();
+                });
+                const float a = (j > 0 ? s1 : s0);
+                const f8_f16 s = f8_f16{a, a, a, a, a, a, a, a, a, a, a, a, a, a, a, a};
+                acc[0][j] = __builtin_elementwise_fma(s, p * f8_scale_value((ev[0] >> (8 * SEL)) & 255u), acc[0][j]);
+            });
+            wait_lgkm0();
+            return;
+        }
         F8Row w[NJ][2];
         each<NJ>([&](auto jj) {
             constexpr int j = decltype(jj)::value;
@@ -533,7 +555,7 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void f8_gateup_tile_kernel(F8F
     g.sp[0] = reinterpret_cast<const float*>(G.scale) + srow;
     g.sp[1] = reinterpret_cast<const float*>(U.scale) + srow;
     f8_f16 acc[NB][S::NJ];
-    tile_go<S, false, true>(g, tr.nrows, WS, XS, acc);
+    tile_go<S, S::NB == 1, true>(g, tr.nrows, WS, XS, acc);
     // h and its largest magnitude per row over the tile's 128 columns
     // (a wavefront has gate and up in its two blocks)
     static_assert(S::NJ == 2 && HC == 32, "a block of gate, a block of up");
