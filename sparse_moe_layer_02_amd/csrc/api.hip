@@ -71,13 +71,13 @@ int ldh_of(const moe_config* c) {
 // 256-row product.  Fewer rows per expert: 64-row tiles (every expert
 // bandwidth-bound; the register-staged kernels keep more loads in flight per
 // CU).  int8 weights always take 64-row tiles (grouped_gemm_q8.hip).  e4m3
-// weights: 64 rows, or 256 where experts average 64 or more (f8_tile.hip;
-// gate/up + down at d 6144, F 2048: 32 rows per expert 1.73 against 1.92 ms, 64
-// rows 2.27 / 2.09).
+// weights: 64 rows, or 128 where experts average 64 or more (f8_tile.hip; whole
+// layers at d 6144, F 2048, 64- / 128-row tiles: 32 rows per expert 1.97 / 2.06 ms,
+// 47 rows 2.25 / 2.37, 64 rows 2.78 / 2.66, 256 rows 8.2 / 7.1).
 int gemm_bm(const moe_config* c) {
     if (c->w_dtype == MOE_DT_Q8B32) return 64;
     const long n = (long)c->n_tokens * c->top_k, e = c->n_expert;
-    if (c->w_dtype == MOE_DT_F8B128) return n >= 64 * e ? 256 : 64;
+    if (c->w_dtype == MOE_DT_F8B128) return n >= 64 * e ? 128 : 64;
     return n >= 96L * c->n_expert ? 256 : 64;
 }
 

@@ -15,12 +15,11 @@
 // the block (one FMA per lane's result, an SGPR operand); the activation rows'
 // e8m0 scales are applied by the matrix instruction.
 //
-// WIDE: the codes are widened to bf16 and the sums are fp32 (f8_dev.h); taken
-// for fp32 results and for gate/up of 64-row tiles, where the weight bytes set
-// the pace and it costs nothing (8 tokens 122 us against 132, 16 rows per expert
-// 1.00 ms both): a sum off by 1e-5 can move a scale of h, which shows in the few
-// rows of a small layer.  Otherwise the 8-bit instruction, twice the rate, for
-// results that are rounded to bf16 or e4m3 next.
+// WIDE: the codes are widened to bf16 and the sums are fp32 (f8_dev.h): every
+// product of the layers, and the dense one to fp32.  In 64-row tiles the weight
+// bytes set the pace and it costs nothing (8 tokens: gate/up 117 us, down 63 with
+// either instruction); at 128 rows per expert it costs 0.7 + 0.4 ms of 2.7.  The
+// dense product to bf16 takes the 8-bit instruction, twice the rate.
 //
 // A tile computes only the 32-row blocks that hold rows: blocks are dealt to the
 // two wavefront rows in turn, and each wavefront runs the K loop built for its
@@ -37,11 +36,10 @@ namespace moe {
 namespace {
 
 // Tile shapes: GM x GN wavefronts (GM along the activation rows, GN along the
-// weight rows), each NB x NJ blocks of 32 x 32, NST stages of weight rows and NSX
-// of activation rows in LDS.
-template <int NB_, int NJ_, int GM_, int GN_, int NST_, int NSX_ = NST_>
+// weight rows), each NB x NJ blocks of 32 x 32, NST stages in LDS.
+template <int NB_, int NJ_, int GM_, int GN_, int NST_>
 struct Shape {
-    static constexpr int NB = NB_, NJ = NJ_, GM = GM_, GN = GN_, NST = NST_, NSX = NSX_;
+    static constexpr int NB = NB_, NJ = NJ_, GM = GM_, GN = GN_, NST = NST_;
     static constexpr int W = GM * GN;              // wavefronts
     static constexpr int BM = 32 * NB * GM;        // activation rows
     static constexpr int WR = 32 * NJ, TN = WR * GN;         // weight rows per wavefront, per tile
@@ -49,25 +47,24 @@ struct Shape {
     static constexpr int WQ = WB / 1024 / W;                 // 1 KB copies per wavefront and stage
     static constexpr int XQ = (XB / 1024 + W - 1) / W;       // (at most)
     static_assert(WQ * 1024 * W == WB, "weight copies");
-    static constexpr int WAVES = NST * WB + NSX * XB <= 80 * 1024 && W == 8 ? 4 : 2;  // per SIMD: two workgroups where LDS has room
+    static constexpr int WAVES = NST * (WB + XB) <= 80 * 1024 && W == 8 ? 4 : 2;  // per SIMD: two workgroups where LDS has room
 };
 // Expert tiles (256 weight rows, the two scale blocks of a 128-column h block).
 // Up to 64 activation rows: two workgroups per compute unit, each with two
 // stages, so that one's start and end lie under the other's loop (gate/up of
 // 512 tokens, 16 rows per expert: 1.00 ms, 6.5 TB/s of weights; one workgroup
-// with four stages took 1.35 ms when this took 1.06).  More: a larger tile reads LDS less per product and
-// an expert's weights fewer times; the weights, which come from HBM, are sent for
-// a stage earlier than the activation rows, most often in L2 (128 rows per
-// expert: gate/up 1.66 ms and down 1.01, both one stage ahead 1.77 and 1.03; 128
-// rows per tile with the weights two stages further ahead 1.83 and 1.11).
+// with four stages took 1.35 ms when this took 1.06).  More: 128 rows, whose
+// widened operands (64 registers of weights) fit beside the accumulators; a larger
+// tile reads LDS less per product (128 rows per expert: gate/up 2.29 ms and down
+// 1.34; 256-row tiles, which widen half a stage at a time, 2.64 and 1.62; two
+// stages, or four of weights, in place of three: the same within 2%).
 typedef Shape<1, 2, 2, 4, 2> Rows64;
-typedef Shape<4, 2, 2, 4, 3, 2> Rows256;
+typedef Shape<2, 2, 2, 4, 3> Rows128;  // also of the dense product to fp32
 // Tiles of the dense product: its weights are shared by every row tile, so one
-// stage ahead is enough (4096 x 4096 x 6144 105 us, 108 with the ring above);
-// smaller ones for sizes that would leave compute units idle, and for fp32 results
-// (whose widened operands do not fit beside the accumulators of the largest).
+// stage ahead is enough (4096 x 4096 x 6144 105 us, 108 with weights two stages
+// ahead); smaller ones for sizes that would leave compute units idle, and for fp32
+// results (whose widened operands do not fit beside the accumulators of the largest).
 typedef Shape<4, 2, 2, 4, 2> Square256;
-typedef Shape<2, 2, 2, 4, 3> Rows128;
 typedef Shape<2, 2, 2, 2, 2> Square128;
 typedef Shape<1, 1, 2, 2, 4> Square64;
 
@@ -137,10 +134,10 @@ __device__ __forceinline__ void each(F f) {
 
 // The K loop of one wavefront with L live blocks and XC activation copies per
 // stage; acc[i][j]: block i (activation rows) x weight row block j.
-template <class S, int L, int XC, bool WIDE, bool ONCE>
-__device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NST], uint8_t* const (&X)[S::NSX],
+template <class S, int L, int XC, bool WIDE, bool EXPERT>
+__device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NST], uint8_t* const (&X)[S::NST],
                                           f8_f16 (&out)[S::NB][S::NJ]) {
-    constexpr int NST = S::NST, NSX = S::NSX, NB = S::NB, NJ = S::NJ, TW = S::W, TWC = S::WQ;
+    constexpr int NST = S::NST, NB = S::NB, NJ = S::NJ, TW = S::W, TWC = S::WQ;
     const int wave = wave_index(), mh = wave / S::GN, wn = wave % S::GN;
     const F8Lane fl = tile_lane(lane_id());
     constexpr int NC = TWC + XC;
@@ -159,12 +156,13 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
     for (int i = 0; i < L; ++i) __asm__ volatile("" : "+v"(g.eoff[i]));
     const __amdgpu_buffer_rsrc_t wr = tile_buffer(g.wbase), xr = tile_buffer(g.xbase), er = tile_buffer(g.ebase);
     // (stages past the end re-read the last; not used)
-    // ONCE: weights that no other tile reads, as g.once says, are copied
+    // Expert weights that no other tile reads, as g.once says, are copied
     // non-temporal (16 rows per expert: gate/up 1.08 ms, so 1.00, down 0.64 / 0.61;
-    // all copies so, 64 rows per expert, many in two tiles: 1.33 / 1.55 ms).
-    const bool once = ONCE && __builtin_amdgcn_readfirstlane(g.once);
-    auto issue_w = [&](auto ss, int kb) {
-        uint8_t* w = W[decltype(ss)::value % NST];
+    // all copies so, 64 rows per expert, many in two tiles: 1.33 / 1.55 ms; in the
+    // larger tiles, 128 rows per expert, gate/up 2.56 so, 2.48 plain).
+    const bool once = EXPERT && NB == 1 && __builtin_amdgcn_readfirstlane(g.once);
+    auto issue_at = [&](auto ss, int kb) {
+        uint8_t *w = W[decltype(ss)::value % NST], *x = X[decltype(ss)::value % NST];
         auto copies = [&](auto nt) {
 #pragma unroll
             for (int q = 0; q < TWC; ++q)
@@ -172,27 +170,16 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         };
         if (once) copies(ic<1>());
         else copies(ic<0>());
-    };
-    auto issue_x = [&](auto ss, int kb) {
-        uint8_t* x = X[decltype(ss)::value % NSX];
 #pragma unroll
         for (int q = 0; q < XC; ++q) buffer_copy16(xr, g.xoff[q], min(kb, last) * F8_BLK, x + (q * TW + wave) * 1024);
     };
     // what stage n (at step kb) sends for
-    auto issue = [&](auto nn, int kb) {
-        constexpr int n = decltype(nn)::value;
-        issue_x(ic<n + NSX - 1>(), kb + NSX - 1);
-        issue_w(ic<n + NST - 1>(), kb + NST - 1);
-    };
+    auto issue = [&](auto nn, int kb) { issue_at(ic<decltype(nn)::value + NST - 1>(), kb + NST - 1); };
     uint32_t ev[NB], en[NB];
 #pragma unroll
     for (int i = 0; i < L; ++i) en[i] = __builtin_amdgcn_raw_buffer_load_b32(er, (int)g.eoff[i], 0, 0);
     if (nfull > 0) {
-        each<NST - 1>([&](auto ww) {  // in the order of the loop
-            constexpr int w = decltype(ww)::value, x = w - (NST - NSX);
-            if constexpr (x >= 0) issue_x(ic<x>(), x);
-            issue_w(ww, w);
-        });
+        each<NST - 1>([&](auto ss) { issue_at(ss, decltype(ss)::value); });
     }
     // Weight scales of the WIDE loop: at the top of a round lane l holds those of
     // the round's stage l.  (Scalar loads count with the LDS reads, out of order,
@@ -208,7 +195,7 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
     // WIDE: the products of LDS stage B; byte SEL of ev scales the activation
     // rows, lane LN of sl the weight rows
     auto products_wide = [&](auto nn, auto ll) {
-        constexpr int n = decltype(nn)::value, B = n % NST, BX = n % NSX, SEL = n % 4, LN = decltype(ll)::value;
+        constexpr int n = decltype(nn)::value, B = n % NST, SEL = n % 4, LN = decltype(ll)::value;
         const float s0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sl[0]), LN));
         const float s1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sl[1]), LN));
         // (opaque: addresses formed from them are not kept over the loop, where
@@ -223,7 +210,7 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
                 f8_f16 p = f8_f16{};
                 each<2>([&](auto hh) {
                     constexpr int h = decltype(hh)::value;
-                    const F8Row w = tile_row(W[B] + 32 * j * F8_BLK, fl, wo, h), x = tile_row(X[BX], fl, xo, h);
+                    const F8Row w = tile_row(W[B] + 32 * j * F8_BLK, fl, wo, h), x = tile_row(X[B], fl, xo, h);
                     p = f8_dot32(f8_widen(w.a, w.b), f8_widen(x.a, x.b), p);
                     pin();
                 });
@@ -247,13 +234,19 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         });
         each<L>([&](auto ii) {
             constexpr int i = decltype(ii)::value;
-            const F8Row x0 = tile_row(X[BX] + 32 * S::GM * i * F8_BLK, fl, xo, 0);
-            const F8Row x1 = tile_row(X[BX] + 32 * S::GM * i * F8_BLK, fl, xo, 1);
-            const F8Wide v0 = f8_widen(x0.a, x0.b), v1 = f8_widen(x1.a, x1.b);
-            const float sx = f8_scale_value((ev[i] >> (8 * SEL)) & 255u);
+            const F8Row x0 = tile_row(X[B] + 32 * S::GM * i * F8_BLK, fl, xo, 0);
+            const F8Row x1 = tile_row(X[B] + 32 * S::GM * i * F8_BLK, fl, xo, 1);
+            // The layers' row scales multiply the widened codes: exact, as those are
+            // quantised finite fp32 values (but for parts below 2^-133), and one
+            // operation per result less (128 rows per expert: gate/up 2.29 ms, 2.48
+            // with the scale after the sum).  The dense product's scales are the
+            // caller's: any scale whose product with the sum is in range is right.
+            const float sx = f8_scale_value((ev[i] >> (8 * SEL)) & 255u), before = EXPERT ? sx : 1.0f;
+            const F8Wide v0 = f8_widen(x0.a, x0.b, before), v1 = f8_widen(x1.a, x1.b, before);
             each<NJ>([&](auto jj) {
                 constexpr int j = decltype(jj)::value;
-                const f8_f16 p = f8_dot32(ww[j][1], v1, f8_dot32(ww[j][0], v0, f8_f16{})) * sx;
+                f8_f16 p = f8_dot32(ww[j][1], v1, f8_dot32(ww[j][0], v0, f8_f16{}));
+                if constexpr (!EXPERT) p = p * sx;
                 // (whole-vector operations: accumulators written element by
                 // element in a loop went to scratch memory)
                 const float a = j > 0 ? s1 : s0;
@@ -284,7 +277,7 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         acc[i][j] = __builtin_elementwise_fma(s, pend, acc[i][j]);
     };
     auto products = [&](auto nn, auto more, int kb) {
-        constexpr int n = decltype(nn)::value, B = n % NST, BX = n % NSX, SEL = n % 4;
+        constexpr int n = decltype(nn)::value, B = n % NST, SEL = n % 4;
         constexpr bool MORE = decltype(more)::value != 0;  // a stage of the loop, which sends for a later one
         uint32_t wo = S::WR * wn * F8_BLK, xo = 32 * mh * F8_BLK;
         __asm__ volatile("" : "+s"(wo), "+s"(xo));
@@ -292,7 +285,7 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
         each<2>([&](auto hh) {  // in the order of use
             constexpr int h = decltype(hh)::value;
             w[0][h] = tile_row(W[B], fl, wo, h);
-            x[h] = tile_row(X[BX], fl, xo, h);
+            x[h] = tile_row(X[B], fl, xo, h);
         });
         each<2 * (NJ - 1)>([&](auto q) {
             constexpr int j = 1 + decltype(q)::value / 2, h = decltype(q)::value % 2;
@@ -309,8 +302,8 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
             p = f8_mfma32<SEL>(f8_join(w[j][1].a, w[j][1].b), f8_join(x[1].a, x[1].b), p, ev[i]);
             pin();
             if constexpr (j == NJ - 1 && i + 1 < L) {  // the next activation block's rows
-                x[0] = tile_row(X[BX] + 32 * S::GM * (i + 1) * F8_BLK, fl, xo, 0);
-                x[1] = tile_row(X[BX] + 32 * S::GM * (i + 1) * F8_BLK, fl, xo, 1);
+                x[0] = tile_row(X[B] + 32 * S::GM * (i + 1) * F8_BLK, fl, xo, 0);
+                x[1] = tile_row(X[B] + 32 * S::GM * (i + 1) * F8_BLK, fl, xo, 1);
             }
             if constexpr (b == 0) {
                 if constexpr (MORE) issue(nn, kb);
@@ -337,7 +330,7 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
     auto stage = [&](auto nn, int kb) {
         constexpr int n = decltype(nn)::value, SEL = n % 4;
         // all but the copies sent after this stage's last
-        wait_vm<NSX == NST ? (NST - 2) * NC : TWC + (NSX - 2) * NC>();
+        wait_vm<(NST - 2) * NC>();
         barrier_nofence();
         if constexpr (!WIDE && L > 0) {
             products(nn, ic<1>(), kb);
@@ -402,11 +395,11 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
 }
 
 // Runs the loop built for this wavefront's live blocks (rows of the tile: nrows).
-template <class S, bool WIDE, bool ONCE>
+template <class S, bool WIDE, bool EXPERT>
 __device__ __forceinline__ void tile_run(const F8Tile<S>& g, int nrows, uint8_t* const (&W)[S::NST],
-                                         uint8_t* const (&X)[S::NSX], f8_f16 (&acc)[S::NB][S::NJ]) {
+                                         uint8_t* const (&X)[S::NST], f8_f16 (&acc)[S::NB][S::NJ]) {
     const int wave = wave_index(), nblk = (nrows + 31) / 32, live = (nblk - wave / S::GN + S::GM - 1) / S::GM;
-    auto run = [&](auto l, auto xc) { tile_loop<S, decltype(l)::value, decltype(xc)::value, WIDE, ONCE>(g, W, X, acc); };
+    auto run = [&](auto l, auto xc) { tile_loop<S, decltype(l)::value, decltype(xc)::value, WIDE, EXPERT>(g, W, X, acc); };
     static_assert(S::GM == 2, "two wavefronts along the activation rows");
     {  // a round of activation copies covers W / 4 blocks
         constexpr int RB = S::W / 4;
@@ -431,8 +424,8 @@ __device__ __forceinline__ void tile_run(const F8Tile<S>& g, int nrows, uint8_t*
     __shared__ __attribute__((aligned(1024))) uint8_t W3[S::NST > 3 ? S::WB : 16];             \
     __shared__ __attribute__((aligned(1024))) uint8_t X0[S::XB];                               \
     __shared__ __attribute__((aligned(1024))) uint8_t X1[S::XB];                               \
-    __shared__ __attribute__((aligned(1024))) uint8_t X2[S::NSX > 2 ? S::XB : 16];             \
-    __shared__ __attribute__((aligned(1024))) uint8_t X3[S::NSX > 3 ? S::XB : 16];             \
+    __shared__ __attribute__((aligned(1024))) uint8_t X2[S::NST > 2 ? S::XB : 16];             \
+    __shared__ __attribute__((aligned(1024))) uint8_t X3[S::NST > 3 ? S::XB : 16];             \
     uint8_t* const WS[4] = {W0, W1, W2, W3};                                                   \
     uint8_t* const XS[4] = {X0, X1, X2, X3}
 
@@ -450,10 +443,10 @@ __device__ __forceinline__ void ring(uint8_t* const (&S)[4], F f) {
     }
 }
 
-template <class S, bool WIDE, bool ONCE>
+template <class S, bool WIDE, bool EXPERT>
 __device__ __forceinline__ void tile_go(const F8Tile<S>& g, int nrows, uint8_t* const (&WS)[4], uint8_t* const (&XS)[4],
                                         f8_f16 (&acc)[S::NB][S::NJ]) {
-    ring<S::NST>(WS, [&](auto& W) { ring<S::NSX>(XS, [&](auto& X) { tile_run<S, WIDE, ONCE>(g, nrows, W, X, acc); }); });
+    ring<S::NST>(WS, [&](auto& W) { ring<S::NST>(XS, [&](auto& X) { tile_run<S, WIDE, EXPERT>(g, nrows, W, X, acc); }); });
 }
 
 // Results to memory through LDS, so that eight lanes store 128 consecutive bytes
@@ -555,7 +548,7 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void f8_gateup_tile_kernel(F8F
     g.sp[0] = reinterpret_cast<const float*>(G.scale) + srow;
     g.sp[1] = reinterpret_cast<const float*>(U.scale) + srow;
     f8_f16 acc[NB][S::NJ];
-    tile_go<S, S::NB == 1, true>(g, tr.nrows, WS, XS, acc);
+    tile_go<S, true, true>(g, tr.nrows, WS, XS, acc);
     // h and its largest magnitude per row over the tile's 128 columns
     // (a wavefront has gate and up in its two blocks)
     static_assert(S::NJ == 2 && HC == 32, "a block of gate, a block of up");
@@ -646,7 +639,7 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void f8_down_tile_kernel(F8Ffn
     for (int j = 0; j < 2; ++j)  // (one block: both the same)
         g.sp[j] = reinterpret_cast<const float*>(D.scale) + (e * f8_blocks(d) + min(c0 + 32 * j % S::WR, d - 1) / F8_BLK) * g.nst;
     f8_f16 acc[NB][S::NJ];
-    tile_go<S, false, true>(g, tr.nrows, WS, XS, acc);
+    tile_go<S, true, true>(g, tr.nrows, WS, XS, acc);
     float* out = shared ? a.f.shared_out : a.f.slot_out;
     __syncthreads();  // every wavefront has read its last stage
     uint8_t* R = out_region<S>(WS, wave);
@@ -751,15 +744,15 @@ hipError_t launch_f8_gateup(const F8Ffn& a, hipStream_t st, const KTime& kt) {
     const int fmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F;
     const dim3 grid(a.f.max_tiles, f8_blocks(fmax));
     if (a.f.bm == 64) launch_kernel(f8_gateup_tile_kernel<Rows64>, grid, 64 * Rows64::W, st, kt, a);
-    else launch_kernel(f8_gateup_tile_kernel<Rows256>, grid, 64 * Rows256::W, st, kt, a);
+    else launch_kernel(f8_gateup_tile_kernel<Rows128>, grid, 64 * Rows128::W, st, kt, a);
     return hipGetLastError();
 }
 
 hipError_t launch_f8_down(const F8Ffn& a, hipStream_t st, const KTime& kt) {
-    static_assert(Rows64::TN == Rows256::TN, "one grid");
+    static_assert(Rows64::TN == Rows128::TN, "one grid");
     const dim3 grid(a.f.max_tiles, (a.f.d + Rows64::TN - 1) / Rows64::TN);
     if (a.f.bm == 64) launch_kernel(f8_down_tile_kernel<Rows64>, grid, 64 * Rows64::W, st, kt, a);
-    else launch_kernel(f8_down_tile_kernel<Rows256>, grid, 64 * Rows256::W, st, kt, a);
+    else launch_kernel(f8_down_tile_kernel<Rows128>, grid, 64 * Rows128::W, st, kt, a);
     return hipGetLastError();
 }
 
