@@ -171,7 +171,7 @@ int check_weights(const moe_config* c, const moe_weights* w, bool router) {
 
 int device_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_DEVICE; }
 
-MatRef ref(const moe_mat& m) { return MatRef{m.q, static_cast<const uint16_t*>(m.scale)}; }
+MatRef ref(const moe_mat& m) { return MatRef{m.q, m.scale}; }
 
 PermArgs perm_args(const moe_config* c, const LayerLayout& L, void* ws, const int32_t* idx, int32_t* off,
                    int32_t* perm, int32_t* inv) {
