@@ -103,11 +103,9 @@ typedef struct {
 } moe_config;
 
 typedef struct {
-    const void *q;  /* [n, rows, cols] elements of w_dtype (int8 for Q8B32, e4m3 for F8B128) */
-    union {         /* 4-byte aligned; ignored for the other weight types */
-        const uint16_t *scale;   /* Q8B32: fp16 bits [n, rows, cols/32] */
-        const float *scale_f32;  /* F8B128: [n, ceil(rows/128), ceil(cols/128)] */
-    };
+    const void *q;          /* [n, rows, cols] elements of w_dtype (int8 for Q8B32, e4m3 for F8B128) */
+    const uint16_t *scale;  /* Q8B32: fp16 bits [n, rows, cols/32]; F8B128: the address of fp32 [n,
+                               ceil(rows/128), ceil(cols/128)], cast; 4-byte aligned; else ignored */
 } moe_mat;
 
 typedef struct {
