@@ -237,7 +237,9 @@ int moe_layer_forward_grouped(const moe_config *cfg, const moe_groups *groups, c
  * at zero: each call writes every word before reading it), so calls that
  * overlap on one GPU - on two streams, or from two host threads without
  * ordering - race and must not be issued.  MOE_ERR_DEVICE if the array's
- * device address cannot be obtained. */
+ * device address cannot be obtained.
+ * Like moe_layer_forward it takes no expert groups: a grouped layer brings its
+ * own workspace (moe_layer_forward_grouped). */
 #define MOE_STATIC_SCRATCH_BYTES (64u << 20)
 int moe_layer_forward_noalloc(const moe_config *cfg, const void *x, const moe_weights *w, float *y,
                               moe_debug *dbg, void *stream);
