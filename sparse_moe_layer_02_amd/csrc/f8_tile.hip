@@ -52,7 +52,7 @@ struct Shape {
 // Expert tiles (256 weight rows, the two scale blocks of a 128-column h block).
 // Up to 64 activation rows: two workgroups per compute unit, each with two
 // stages, so that one's start and end lie under the other's loop (gate/up of
-// 512 tokens, 16 rows per expert: 1.00 ms, 6.5 TB/s of weights; one workgroup
+// 512 tokens, 16 rows per expert: 1.00 ms, 6.6 TB/s of weights; one workgroup
 // with four stages took 1.35 ms when this took 1.06).  More: 128 rows, whose
 // widened operands (64 registers of weights) fit beside the accumulators; a larger
 // tile reads LDS less per product (128 rows per expert: gate/up 2.29 ms and down
@@ -61,8 +61,8 @@ struct Shape {
 typedef Shape<1, 2, 2, 4, 2> Rows64;
 typedef Shape<2, 2, 2, 4, 3> Rows128;  // also of the dense product to fp32
 // Tiles of the dense product: its weights are shared by every row tile, so one
-// stage ahead is enough (4096 x 4096 x 6144 105 us, 108 with weights two stages
-// ahead); smaller ones for sizes that would leave compute units idle, and for fp32
+// stage ahead is enough (weights two stages ahead: 4096 x 4096 x 6144 3% longer);
+// smaller ones for sizes that would leave compute units idle, and for fp32
 // results (whose widened operands do not fit beside the accumulators of the largest).
 typedef Shape<4, 2, 2, 4, 2> Square256;
 typedef Shape<2, 2, 2, 2, 2> Square128;
@@ -262,8 +262,8 @@ __device__ __forceinline__ void tile_loop(F8Tile<S> g, uint8_t* const (&W)[S::NS
     // go out behind the first products.  (Left to the compiler the sums of
     // several blocks are in flight at once; in the largest shape, whose registers
     // are all taken, offsets were then reloaded from scratch memory behind the
-    // copies: 4096 x 4096 x 6144 131 us, in this order 106.  The smaller shapes
-    // gain little: 300 x 4096 x 6144 in 64 x 64 tiles 25.0, now 24.5.)
+    // copies: 4096 x 4096 x 6144 took a quarter longer.  The smaller shapes gain
+    // little: 300 x 4096 x 6144 in 64 x 64 tiles 2%.)
     f8_f16 pend = f8_f16{};
     float q0 = 0.0f, q1 = 0.0f, t0 = 0.0f, t1 = 0.0f;  // scales of the block that waits, of the next stage
     if constexpr (!WIDE) {
@@ -452,8 +452,8 @@ __device__ __forceinline__ void tile_go(const F8Tile<S>& g, int nrows, uint8_t* 
 // Results to memory through LDS, so that eight lanes store 128 consecutive bytes
 // of a row (a lane holds four columns of a row per eight; straight from the
 // registers, 2772 x 4096 x 192 to fp32 took 32 us and now 22, to bf16 18 / 17, to
-// 4089 columns, whose rows start anywhere, 39 / 23; 4096 x 4096 x 6144 113 / 105,
-// back to back; down of 4096 tokens 1.08 / 1.03 ms).  A wavefront's region holds 32
+// 4089 columns, whose rows start anywhere, 39 / 23; 4096 x 4096 x 6144 7% less, the
+// down product of 4096 tokens 5%).  A wavefront's region holds 32
 // rows of 128 bytes, 16-byte chunks swizzled by row.
 constexpr int OUT_REGION = 32 * 128;
 template <class S>
@@ -767,12 +767,12 @@ static void dense_tile_launch_out(const BlockArgs& a, hipStream_t st) {
     else dense_tile_launch<S, MOE_DT_BF16>(a, st);
 }
 
-// The largest tiles that still give most compute units one (us, 256 x 256 /
-// 128 x 128 / 64 x 64 tiles, bf16 results; n x k 4096 x 6144: 300 rows 93 / 41 /
-// 25, 1000 rows 94 / 44 / 50, 4096 rows 118 / 124 / 199; 4096 x 2048: 2048 rows
-// 40 / 26 / 41; 700 x 1024: 4096 rows 24 / 12.2 / 12.9).  fp32 results double
+// The largest tiles that still give most compute units one (us a call, 256 x 256
+// / 128 x 128 / 64 x 64 tiles, bf16 results; n x k 4096 x 6144: 300 rows 77 / 40 /
+// 25, 1000 rows 77 / 44 / 55, 4096 rows 95 / 124 / 192; 4096 x 2048: 2048 rows
+// 34 / 26 / 39; 700 x 1024: 4096 rows 21.5 / 12.3 / 12.2).  fp32 results double
 // the matrix work: 128 x 256 tiles pay from 256 of them (2048 rows of 4096 x
-// 2048 46 against 54 us for 128 x 128).
+// 2048 39 against 48 us for 128 x 128).
 hipError_t launch_block_matmul_tile(const BlockArgs& a, hipStream_t st) {
     auto tiles = [&](int bm, int tn) { return (long)((a.m + bm - 1) / bm) * ((a.n + tn - 1) / tn); };
     if (a.odt == MOE_DT_F32 && tiles(128, 256) >= 256) dense_tile_launch<Rows128, MOE_DT_F32>(a, st);
