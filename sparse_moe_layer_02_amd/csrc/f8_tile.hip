@@ -12,8 +12,9 @@
 // chunks swizzled by row as dma_dev.h describes), in a ring of stages behind
 // one barrier per stage.  A block's sum over the stage starts from zero on the
 // matrix cores and is added with the weight block's fp32 scale, uniform over
-// the block (one FMA per lane's result, an SGPR operand); the activation rows'
-// e8m0 scales are applied by the matrix instruction.
+// the block (one FMA per lane's result, an SGPR operand).  The activation rows'
+// e8m0 scales are applied by the 8-bit instruction itself, or (WIDE) as the rows
+// are widened or after the sum.
 //
 // WIDE: the codes are widened to bf16 and the sums are fp32 (f8_dev.h): every
 // product of the layers, and the dense one to fp32.  In 64-row tiles the weight
@@ -54,10 +55,10 @@ struct Shape {
 // stages, so that one's start and end lie under the other's loop (gate/up of
 // 512 tokens, 16 rows per expert: 1.00 ms, 6.6 TB/s of weights; one workgroup
 // with four stages took 1.35 ms when this took 1.06).  More: 128 rows, whose
-// widened operands (64 registers of weights) fit beside the accumulators; a larger
-// tile reads LDS less per product (128 rows per expert: gate/up 2.29 ms and down
-// 1.34; 256-row tiles, which widen half a stage at a time, 2.64 and 1.62; two
-// stages, or four of weights, in place of three: the same within 2%).
+// widened operands (64 registers of weights) fit beside the accumulators (128 rows
+// per expert: gate/up 2.29 ms and down 1.34; 256-row tiles, which widen half a
+// stage at a time, 2.64 and 1.62; two stages, or four of weights, in place of
+// three: within 2%).
 typedef Shape<1, 2, 2, 4, 2> Rows64;
 typedef Shape<2, 2, 2, 4, 3> Rows128;  // also of the dense product to fp32
 // Tiles of the dense product: its weights are shared by every row tile, so one
