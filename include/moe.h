@@ -45,6 +45,8 @@
  *    F8B128 = e4m3 codes (OCP, largest value 448) [n, rows, cols] plus one
  *    fp32 scale per block of 128 x 128 [n, ceil(rows/128), ceil(cols/128)];
  *    weight = scale * code.
+ *    I8CH = int8 codes [n, rows, cols] plus one fp32 scale per row (output
+ *    channel) [n, rows]; weight = scale * code.
  *  - Products with F8B128 weights are products of e4m3 operands: activations
  *    are quantised per row and 128 columns as moe_quantize_rows does (x, and
  *    the SwiGLU intermediate from its fp32 values).  Sums are fp32; only
@@ -53,6 +55,11 @@
  *    (1.5e-5 of a result on normal operands).  Layers with
  *    F8B128 weights need n_tokens * d_model < 2^32.  Softmax scores are taken
  *    over all n_expert logits of a token.
+ *  - Products with I8CH weights are products of int8 operands: activations are
+ *    quantised per row as moe_quantize_tokens does (x, and the SwiGLU
+ *    intermediate from its fp32 values, over the whole row).  Sums are exact
+ *    (int32); d_model, d_ff and d_ff_shared are at most MOE_I8_MAX_K there, and
+ *    n_tokens * d_model < 2^32.
  *  - Results: expert indices and the permutation are exact and do not depend
  *    on the path taken; logits and scores are accumulated in fp64 and rounded
  *    once to fp32; the SwiGLU intermediate is rounded to the activation format
@@ -80,7 +87,7 @@ typedef enum {
 } moe_status;
 
 typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SQRT_SOFTPLUS = 1, MOE_SCORE_SOFTMAX = 2 } moe_score;
-typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_Q8B32 = 2, MOE_DT_F8B128 = 3 } moe_dtype;
+typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_Q8B32 = 2, MOE_DT_F8B128 = 3, MOE_DT_I8CH = 4 } moe_dtype;
 typedef enum { MOE_PATH_AUTO = 0, MOE_PATH_DECODE = 1, MOE_PATH_PREFILL = 2 } moe_path;
 
 /* Largest token count the decode path accepts (MOE_PATH_AUTO takes it for
@@ -98,14 +105,15 @@ typedef struct {
     int32_t score;       /* moe_score */
     float route_scale;   /* finite, > 0: 1.5 for the sqrt(softplus) router, 1.0 for sigmoid */
     int32_t act_dtype;   /* moe_dtype of x and of the SwiGLU intermediate: F32 or BF16 */
-    int32_t w_dtype;     /* moe_dtype of the expert weights: (F32,F32) (BF16,BF16) (BF16,Q8B32) (BF16,F8B128) */
+    int32_t w_dtype;     /* moe_dtype of the expert weights: (F32,F32) (BF16,BF16) (BF16,Q8B32) (BF16,F8B128) (BF16,I8CH) */
     int32_t path;        /* moe_path, used by moe_layer_forward */
 } moe_config;
 
 typedef struct {
-    const void *q;          /* [n, rows, cols] elements of w_dtype (int8 for Q8B32, e4m3 for F8B128) */
+    const void *q;          /* [n, rows, cols] elements of w_dtype (int8 for Q8B32 and I8CH, e4m3 for F8B128) */
     const uint16_t *scale;  /* Q8B32: fp16 bits [n, rows, cols/32]; F8B128: the address of fp32 [n,
-                               ceil(rows/128), ceil(cols/128)], cast; 4-byte aligned; else ignored */
+                               ceil(rows/128), ceil(cols/128)], I8CH: of fp32 [n, rows], cast; 4-byte
+                               aligned; else ignored */
 } moe_mat;
 
 typedef struct {
@@ -125,7 +133,9 @@ typedef struct {
  * events unrecorded.  F8B128 layers have one path: stages 0 to 5 at every
  * n_tokens, but up to 16 tokens stage 1 includes the permutation (stage 2's
  * events stay unrecorded), and the quantisation of x is in stage 1 there and
- * in none beyond. */
+ * in none beyond.  I8CH layers: stages 0 to 5
+ * (the quantisation of x in none), and stage 3 ends with the quantisation of
+ * the SwiGLU intermediate. */
 #define MOE_STAGES 6
 #define MOE_STAGE_EVENTS (2 * MOE_STAGES)
 
@@ -218,7 +228,7 @@ int moe_layer_forward(const moe_config *cfg, const void *x, const moe_weights *w
 
 /* moe_layer_forward with expert groups (NULL: {1, 1, 1, 1}) and a choice of
  * y's type: y_dtype MOE_DT_F32, or MOE_DT_BF16 (the fp32 sum rounded once;
- * F8B128 weights only, else MOE_ERR_UNSUPPORTED). */
+ * F8B128 and I8CH weights only, else MOE_ERR_UNSUPPORTED). */
 int moe_layer_forward_grouped(const moe_config *cfg, const moe_groups *groups, const void *x, const moe_weights *w,
                               void *y, int32_t y_dtype, moe_debug *dbg, void *ws, size_t ws_bytes, void *stream);
 
@@ -293,6 +303,36 @@ int moe_block_matmul(const void *x, int32_t x_dtype, const uint8_t *x_scale, con
                      int32_t m, int32_t n, int32_t k, void *out, int32_t out_dtype, void *ws, size_t ws_bytes,
                      void *stream);
 
+/* Rows to int8 codes with one fp32 scale per row (token).  x [rows, cols] of
+ * x_dtype (MOE_DT_F32 or MOE_DT_BF16), rows ldx elements apart.  For each row
+ * with largest magnitude a, the scale s is the fp32 value nearest to a / 127, at
+ * least 2^-120, and 1 if a = 0; q [rows, cols] is the integer nearest to x / s,
+ * ties to even (of the exact quotient).  A row with a NaN or an infinity gets
+ * the scale NaN and codes 0.
+ * rows >= 0 (0 enqueues nothing), 16 <= cols <= 2^20 a multiple of 16 and
+ * ldx >= cols a multiple of 16 bytes, else MOE_ERR_INVALID; x and q 16-byte
+ * aligned, scale 4-byte.  q and scale must not overlap x.  No workspace. */
+int moe_quantize_tokens(const void *x, int32_t x_dtype, int32_t rows, int32_t cols, int64_t ldx, int8_t *q,
+                        float *scale, void *stream);
+
+/* out [m, n] = x [m, k] w[n, k]^T with int8 operands, a scale per token and one
+ * per output channel:
+ *   out[i, j] = x_scale[i] * w_scale[j] * sum_c x[i, c] * w[j, c]
+ * (the sum exact, then rounded to fp32 and multiplied by x_scale and by w_scale:
+ * both products must stay within fp32's range).  x is MOE_DT_I8CH codes
+ * with x_scale [m], or MOE_DT_BF16 / MOE_DT_F32 rows, which are quantised as
+ * moe_quantize_tokens does first (x_scale NULL, workspace needed).  Codes may
+ * take every int8 value.  out_dtype MOE_DT_F32, or MOE_DT_BF16 (one rounding
+ * more).  0 <= m <= 2^20 (0 enqueues nothing), 1 <= n <= 2^20, 16 <= k <=
+ * MOE_I8_MAX_K a multiple of 16, else MOE_ERR_INVALID; x, w, out and ws 16-byte
+ * aligned, the scales 4-byte.  out must not overlap an input.  The workspace
+ * size is 0 for I8CH rows and for sizes out of range. */
+#define MOE_I8_MAX_K 131056
+size_t moe_channel_matmul_workspace_bytes(int32_t x_dtype, int32_t m, int32_t k);
+int moe_channel_matmul(const void *x, int32_t x_dtype, const float *x_scale, const int8_t *w, const float *w_scale,
+                       int32_t m, int32_t n, int32_t k, void *out, int32_t out_dtype, void *ws, size_t ws_bytes,
+                       void *stream);
+
 /* Router look-ahead, its read half (NeutronStar fork page, "Cross-layer
  * expert prefetch": the next layer's router runs on this layer's hidden
  * state and the experts it predicts are read while the GPU still computes).
@@ -301,7 +341,7 @@ int moe_block_matmul(const void *x, int32_t x_dtype, const uint8_t *x_scale, con
  * experts ids [n_ids] int32 (device memory, e.g. that topk_idx; entries
  * outside [0, n_expert) are skipped on the device) of the layer w: bit 0 of
  * `which` selects gate, bit 1 up, bit 2 down (for MOE_DT_Q8B32 the codes
- * and their scales, for MOE_DT_F8B128 the codes), and `rows` > 0 limits the read to the leading rows of
+ * and their scales, for MOE_DT_F8B128 and MOE_DT_I8CH the codes), and `rows` > 0 limits the read to the leading rows of
  * each selected matrix (gate and up have d_ff rows, down d_model; 0: all).
  * It writes no memory, so no result of any call changes; the reads leave
  * those weights in the device's memory-side cache (the Infinity Cache),

@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe_mi355x.so")
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE = range(5)
 SCORE = {"sigmoid": 0, "sqrt_softplus": 1, "softmax": 2}
-DTYPE = {"f32": 0, "bf16": 1, "q8b32": 2, "f8b128": 3}
+DTYPE = {"f32": 0, "bf16": 1, "q8b32": 2, "f8b128": 3, "i8ch": 4}
 PATH = {"auto": 0, "decode": 1, "prefill": 2}
 DECODE_MAX_TOKENS = 8
 
@@ -66,7 +66,8 @@ class moe_debug(ctypes.Structure):
 EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_select", "moe_permute", "moe_expert_ffn",
            "moe_combine", "moe_layer_forward", "moe_layer_forward_noalloc", "moe_topk_rows",
            "moe_prefetch_experts", "moe_select_grouped", "moe_route_grouped", "moe_layer_forward_grouped",
-           "moe_quantize_rows", "moe_block_matmul", "moe_block_matmul_workspace_bytes", "moe_status_str")
+           "moe_quantize_rows", "moe_block_matmul", "moe_quantize_tokens", "moe_channel_matmul",
+           "moe_block_matmul_workspace_bytes", "moe_channel_matmul_workspace_bytes", "moe_status_str")
 STATIC_SCRATCH_BYTES = 64 << 20  # MOE_STATIC_SCRATCH_BYTES
 TOPK_ROWS_MAX_N = 65536  # MOE_TOPK_ROWS_MAX_N
 PREFETCH_MAX_IDS = 65536  # MOE_PREFETCH_MAX_IDS
@@ -107,11 +108,15 @@ def load(path: str = LIB_PATH):
     lib.moe_quantize_rows.argtypes = [P, I, I, I, ctypes.c_int64, P, P, P]
     lib.moe_block_matmul.argtypes = [P, I, P, P, P, I, I, I, P, I, P, S, P]
     lib.moe_block_matmul_workspace_bytes.argtypes = [I, I, I]
+    lib.moe_quantize_tokens.argtypes = [P, I, I, I, ctypes.c_int64, P, P, P]
+    lib.moe_channel_matmul.argtypes = [P, I, P, P, P, I, I, I, P, I, P, S, P]
+    lib.moe_channel_matmul_workspace_bytes.argtypes = [I, I, I]
     lib.moe_status_str.argtypes = [ctypes.c_int]
     lib.moe_status_str.restype = ctypes.c_char_p
     for name in EXPORTS[1:-1]:
         getattr(lib, name).restype = ctypes.c_int
     lib.moe_block_matmul_workspace_bytes.restype = ctypes.c_size_t
+    lib.moe_channel_matmul_workspace_bytes.restype = ctypes.c_size_t
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -382,7 +387,7 @@ def moe_route_grouped(cfg, groups, x, w_router, bias, logits, topk_idx, topk_w, 
 
 def moe_layer_forward_grouped(cfg, groups, x, weights: moe_weights, y, ws, debug: dict | None = None, stream=None,
                               stage_events=None):
-    """moe_layer_forward with expert groups; y float32, or (f8b128 weights) bfloat16."""
+    """moe_layer_forward with expert groups; y float32, or (f8b128 or i8ch weights) bfloat16."""
     _rows_match(cfg, x)
     _dense(y, (cfg.n_tokens, cfg.d_model), "y")
     _same_device(x, y, ws)
@@ -447,6 +452,60 @@ def moe_block_matmul(x, x_scale, w, w_scale, out, ws=None, stream=None):
             _invalid("x_scale goes with e4m3 rows only")
     _same_device(x, x_scale, w, w_scale, out, ws)
     return _call(load().moe_block_matmul, x.device, stream, ptr(x), xdt, ptr(x_scale), ptr(w), ptr(w_scale), m, n, k,
+                 ptr(out), _row_dtype(out), ptr(ws), _bytes(ws))
+
+
+def moe_quantize_tokens(x, q, scale, stream=None):
+    """Rows ``x`` [rows, cols] (float32 or bfloat16, unit column stride) to int8 codes ``q`` [rows, cols] and one
+    float32 ``scale`` [rows] each."""
+    import torch
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        _invalid("x must be [rows, cols] with adjacent columns")
+    rows, cols = x.shape
+    dt = _row_dtype(x)
+    _dense(q, (rows, cols), "q", torch.int8)
+    _dense(scale, (rows,), "scale", torch.float32)
+    _same_device(x, q, scale)
+    return _call(load().moe_quantize_tokens, x.device, stream, ptr(x), dt, rows, cols,
+                 x.stride(0) if rows > 1 else -(-cols // 16) * 16, ptr(q), ptr(scale))
+
+
+def moe_channel_matmul_workspace_bytes(x_dtype, m, k) -> int:
+    return load().moe_channel_matmul_workspace_bytes(DTYPE.get(x_dtype, x_dtype), m, k)
+
+
+def channel_matmul_workspace(x):
+    """A workspace tensor for moe_channel_matmul of rows ``x`` (None if none is needed)."""
+    import torch
+    if x.dtype is torch.int8:
+        return None
+    size = moe_channel_matmul_workspace_bytes(_row_dtype(x), *x.shape)
+    return torch.empty(size, dtype=torch.uint8, device=x.device)
+
+
+def moe_channel_matmul(x, x_scale, w, w_scale, out, ws=None, stream=None):
+    """out [m, n] (float32 or bfloat16) = x [m, k] w[n, k]^T with int8 operands: ``x`` int8 codes with ``x_scale`` [m]
+    float32 (moe_quantize_tokens), or float32 / bfloat16 rows (x_scale None, ``ws`` needed); ``w`` int8 codes with
+    ``w_scale`` [n] float32."""
+    import torch
+    if x.dim() != 2 or w.dim() != 2:
+        _invalid("x and w must have two dimensions")
+    (m, k), n = x.shape, w.shape[0]
+    _dense(x, (m, k), "x")
+    _dense(w, (n, k), "w", torch.int8)
+    _dense(w_scale, (n,), "w_scale", torch.float32)
+    _dense(out, (m, n), "out")
+    if x.dtype is torch.int8:
+        xdt = 4
+        if x_scale is None:
+            _invalid("int8 rows need their scales")
+        _dense(x_scale, (m,), "x_scale", torch.float32)
+    else:
+        xdt = _row_dtype(x)
+        if x_scale is not None:
+            _invalid("x_scale goes with int8 rows only")
+    _same_device(x, x_scale, w, w_scale, out, ws)
+    return _call(load().moe_channel_matmul, x.device, stream, ptr(x), xdt, ptr(x_scale), ptr(w), ptr(w_scale), m, n, k,
                  ptr(out), _row_dtype(out), ptr(ws), _bytes(ws))
 
 

@@ -33,6 +33,13 @@ bool opt_ptr_ok(const void* p) { return p == nullptr || aligned16(p); }
 bool elt_ok(const void* p) { return p != nullptr && aligned4(p); }
 bool opt_elt_ok(const void* p) { return p == nullptr || aligned4(p); }
 
+// Layers whose activations are quantised: one path for every n_tokens.
+bool is_8bit(const moe_config* c) { return c->w_dtype == MOE_DT_F8B128 || c->w_dtype == MOE_DT_I8CH; }
+
+int ldh_of(const moe_config* c) {
+    return c->n_shared ? (c->d_ff > c->d_ff_shared ? c->d_ff : c->d_ff_shared) : c->d_ff;
+}
+
 int validate_config(const moe_config* c) {
     if (!c) return MOE_ERR_INVALID;
     if (c->n_tokens < 1 || c->n_tokens > MAX_TOKENS) return MOE_ERR_INVALID;
@@ -43,24 +50,23 @@ int validate_config(const moe_config* c) {
     if (c->n_shared == 1 && c->d_ff_shared < 1) return MOE_ERR_INVALID;
     if (c->score < MOE_SCORE_SIGMOID || c->score > MOE_SCORE_SOFTMAX) return MOE_ERR_INVALID;
     if (!(c->route_scale > 0.0f) || isinf(c->route_scale)) return MOE_ERR_INVALID;
-    if (c->act_dtype < 0 || c->act_dtype > 1 || c->w_dtype < 0 || c->w_dtype > MOE_DT_F8B128) return MOE_ERR_INVALID;
+    if (c->act_dtype < 0 || c->act_dtype > 1 || c->w_dtype < 0 || c->w_dtype > MOE_DT_I8CH) return MOE_ERR_INVALID;
     if (c->path < MOE_PATH_AUTO || c->path > MOE_PATH_PREFILL) return MOE_ERR_INVALID;
     const bool pair_ok = (c->act_dtype == MOE_DT_F32 && c->w_dtype == MOE_DT_F32) ||
                          (c->act_dtype == MOE_DT_BF16 && c->w_dtype == MOE_DT_BF16) ||
                          (c->act_dtype == MOE_DT_BF16 && c->w_dtype == MOE_DT_Q8B32) ||
-                         (c->act_dtype == MOE_DT_BF16 && c->w_dtype == MOE_DT_F8B128);
+                         (c->act_dtype == MOE_DT_BF16 && c->w_dtype == MOE_DT_F8B128) ||
+                         (c->act_dtype == MOE_DT_BF16 && c->w_dtype == MOE_DT_I8CH);
     if (!pair_ok) return MOE_ERR_UNSUPPORTED;
     if (c->d_model % 64 || c->d_ff % 64 || (c->n_shared && c->d_ff_shared % 64)) return MOE_ERR_UNSUPPORTED;
     if ((size_t)c->d_model > (1u << 20) || (size_t)c->d_ff > (1u << 20) ||
         (c->n_shared && (size_t)c->d_ff_shared > (1u << 20)))
         return MOE_ERR_UNSUPPORTED;
-    // e4m3 layers address the quantised rows with 32-bit offsets (f8_tile.hip)
-    if (c->w_dtype == MOE_DT_F8B128 && (int64_t)c->n_tokens * c->d_model > 0xFFFFFFFFll) return MOE_ERR_UNSUPPORTED;
+    // these layers address the quantised rows with 32-bit offsets (f8_tile.hip, i8_tile.hip)
+    if (is_8bit(c) && (int64_t)c->n_tokens * c->d_model > 0xFFFFFFFFll) return MOE_ERR_UNSUPPORTED;
+    // int32 sums
+    if (c->w_dtype == MOE_DT_I8CH && (c->d_model > MOE_I8_MAX_K || ldh_of(c) > MOE_I8_MAX_K)) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
-}
-
-int ldh_of(const moe_config* c) {
-    return c->n_shared ? (c->d_ff > c->d_ff_shared ? c->d_ff : c->d_ff_shared) : c->d_ff;
 }
 
 // Rows per grouped-GEMM tile.  256 (the LDS-copy kernels of
@@ -77,7 +83,7 @@ int ldh_of(const moe_config* c) {
 int gemm_bm(const moe_config* c) {
     if (c->w_dtype == MOE_DT_Q8B32) return 64;
     const long n = (long)c->n_tokens * c->top_k, e = c->n_expert;
-    if (c->w_dtype == MOE_DT_F8B128) return n >= 64 * e ? 128 : 64;
+    if (is_8bit(c)) return n >= 64 * e ? 128 : 64;
     return n >= 96L * c->n_expert ? 256 : 64;
 }
 
@@ -97,7 +103,8 @@ int n_dslots_of(const moe_config* c) {
     return c->n_shared + (n < c->n_expert ? n : c->n_expert);
 }
 
-// With the rows of x and h as codes and scale bytes (e4m3 layers).
+// With the rows of x and h as codes and their scales (e4m3: bytes per 128
+// columns; int8: an fp32 value per row).
 struct LayerLayout : Layout {
     size_t xq, xe, hq, he;
 };
@@ -106,9 +113,9 @@ LayerLayout make_layout(const moe_config* c) {
     LayerLayout L;
     const size_t T = (size_t)c->n_tokens, E = (size_t)c->n_expert, k = (size_t)c->top_k;
     const size_t d = (size_t)c->d_model, n = T * k;
-    const size_t hsz = c->act_dtype == MOE_DT_BF16 ? 2 : 4;
+    const bool f8 = c->w_dtype == MOE_DT_F8B128, i8 = c->w_dtype == MOE_DT_I8CH;
+    const size_t hsz = c->act_dtype == MOE_DT_BF16 && !i8 ? 2 : 4;
     L.n_blk = (int)((n + PERM_BLOCK - 1) / PERM_BLOCK);
-    const bool f8 = c->w_dtype == MOE_DT_F8B128;
     L.max_tiles = max_tiles_of(c, GEMM_BM);  // the smallest tile: capacity for any bm
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -133,10 +140,10 @@ LayerLayout make_layout(const moe_config* c) {
     L.shared_out = take(c->n_shared ? T * d * 4 : 0);
     L.scores = take(T * E * 4);
     L.dslots = take((size_t)n_dslots_of(c) * sizeof(DecodeSlot));
-    L.xq = take(f8 ? T * d : 0);
-    L.xe = take(f8 ? T * f8_scale_ld(c->d_model) : 0);
-    L.hq = take(f8 ? hrows * (size_t)ldh_of(c) : 0);
-    L.he = take(f8 ? hrows * f8_scale_ld(ldh_of(c)) : 0);
+    L.xq = take(f8 || i8 ? T * d : 0);
+    L.xe = take(f8 ? T * f8_scale_ld(c->d_model) : i8 ? T * 4 : 0);
+    L.hq = take(f8 || i8 ? hrows * (size_t)ldh_of(c) : 0);
+    L.he = take(f8 ? hrows * f8_scale_ld(ldh_of(c)) : i8 ? hrows * 4 : 0);
     L.total = o;
     return L;
 }
@@ -154,7 +161,7 @@ int check_ws(const moe_config* c, const void* ws, size_t ws_bytes) {
 
 bool mat_ok(const moe_config* c, const moe_mat& m) {
     if (!ptr_ok(m.q)) return false;
-    if ((c->w_dtype == MOE_DT_Q8B32 || c->w_dtype == MOE_DT_F8B128) &&
+    if ((c->w_dtype == MOE_DT_Q8B32 || is_8bit(c)) &&
         (m.scale == nullptr || ((uintptr_t)m.scale & 3u)))
         return false;
     return true;
@@ -266,11 +273,37 @@ hipError_t run_f8_experts(const FfnArgs& f, const LayerLayout& L, void* ws, hipS
     return e == hipSuccess ? launch_f8_down(a, st, kd) : e;
 }
 
+// int8 experts over the quantised rows of x: gate/up to fp32, whose rows are
+// quantised as a whole behind it, down.
+TokenQuantArgs i8_quant_args(const moe_config* c, const LayerLayout& L, void* ws, const void* x) {
+    const int64_t T = c->n_tokens, d = c->d_model;
+    return TokenQuantArgs{x, MOE_DT_BF16, T, T, (int)d, (int)d, d, d, at<int8_t>(ws, L.xq), at<float>(ws, L.xe)};
+}
+
+hipError_t run_i8_experts(const FfnArgs& f, const LayerLayout& L, void* ws, hipStream_t st, const KTime& kg = KTime(),
+                          const KTime& kd = KTime()) {
+    const I8Ffn a{f, at<int8_t>(ws, L.xq), at<float>(ws, L.xe), at<float>(ws, L.h), at<int8_t>(ws, L.hq), at<float>(ws, L.he)};
+    hipError_t e = launch_i8_gateup(a, st, kg.first());
+    if (e != hipSuccess) return e;
+    const int64_t n = (int64_t)f.T * f.k;
+    const TokenQuantArgs q{a.h, MOE_DT_F32, n + (f.n_shared ? f.T : 0), n, f.F, f.Fs, f.ldh, f.ldh, a.hq, a.hs};
+    if ((e = launch_quantize_tokens(q, st, kg.last())) != hipSuccess) return e;
+    return launch_i8_down(a, st, kd);
+}
+
+// The quantisation of x for layers that need it.
+hipError_t run_quantize_x(const moe_config* c, const LayerLayout& L, void* ws, const void* x, hipStream_t st) {
+    if (c->w_dtype == MOE_DT_F8B128) return launch_quantize_rows(f8_quant_args(c, L, ws, x), st);
+    if (c->w_dtype == MOE_DT_I8CH) return launch_quantize_tokens(i8_quant_args(c, L, ws, x), st);
+    return hipSuccess;
+}
+
 hipError_t run_expert_kernels(const FfnArgs& f, const LayerLayout& L, void* ws, hipStream_t st,
                               const KTime& kg = KTime(), const KTime& kd = KTime()) {
     hipError_t e;
     if (f.wdt == MOE_DT_BF16) return run_bf16_experts(f, st, kg, kd);
     if (f.wdt == MOE_DT_F8B128) return run_f8_experts(f, L, ws, st, kg, kd);
+    if (f.wdt == MOE_DT_I8CH) return run_i8_experts(f, L, ws, st, kg, kd);
     e = q8_mfma_gateup(f) ? launch_gateup_mfma_q8(f, st, kg) : launch_gateup_gemv(f, st, kg);
     if (e != hipSuccess) return e;
     return q8_mfma_down(f) ? launch_down_mfma_q8(f, st, kd) : launch_down_slots_gemv(f, st, kd);
@@ -496,6 +529,52 @@ int moe_block_matmul(const void* x, int32_t x_dtype, const uint8_t* x_scale, con
     return device_status(launch_block_matmul(a, st));
 }
 
+namespace {
+bool i8_cols_ok(int32_t k) { return k >= 16 && k <= MOE_I8_MAX_K && k % 16 == 0; }
+}  // namespace
+
+int moe_quantize_tokens(const void* x, int32_t x_dtype, int32_t rows, int32_t cols, int64_t ldx, int8_t* q, float* scale,
+                        void* stream) {
+    if (x_dtype != MOE_DT_F32 && x_dtype != MOE_DT_BF16) return MOE_ERR_INVALID;
+    if (rows < 0 || !f8_cols_ok(cols)) return MOE_ERR_INVALID;
+    const int64_t per16 = x_dtype == MOE_DT_BF16 ? 8 : 4;  // elements in 16 bytes
+    if (ldx < cols || ldx % per16 || ldx > INT64_MAX / 4 / (rows ? rows : 1)) return MOE_ERR_INVALID;
+    if (rows == 0) return MOE_OK;
+    if (!ptr_ok(x) || !ptr_ok(q) || !elt_ok(scale)) return MOE_ERR_INVALID;
+    const TokenQuantArgs a{x, x_dtype, rows, rows, cols, cols, ldx, cols, q, scale};
+    return device_status(launch_quantize_tokens(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_channel_matmul_workspace_bytes(int32_t x_dtype, int32_t m, int32_t k) {
+    if ((x_dtype != MOE_DT_F32 && x_dtype != MOE_DT_BF16) || m < 0 || m > F8_MAX_DIM || !i8_cols_ok(k)) return 0;
+    return align256((size_t)m * k) + align256((size_t)m * 4);
+}
+
+int moe_channel_matmul(const void* x, int32_t x_dtype, const float* x_scale, const int8_t* w, const float* w_scale,
+                       int32_t m, int32_t n, int32_t k, void* out, int32_t out_dtype, void* ws, size_t ws_bytes,
+                       void* stream) {
+    if (x_dtype != MOE_DT_F32 && x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_I8CH) return MOE_ERR_INVALID;
+    if (out_dtype != MOE_DT_F32 && out_dtype != MOE_DT_BF16) return MOE_ERR_INVALID;
+    if (m < 0 || m > F8_MAX_DIM || n < 1 || n > F8_MAX_DIM || !i8_cols_ok(k)) return MOE_ERR_INVALID;
+    const bool codes = x_dtype == MOE_DT_I8CH;
+    if (codes ? (m && !elt_ok(x_scale)) : x_scale != nullptr) return MOE_ERR_INVALID;
+    if (m == 0) return MOE_OK;
+    if (!ptr_ok(x) || !ptr_ok(w) || !elt_ok(w_scale) || !ptr_ok(out)) return MOE_ERR_INVALID;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    ChannelArgs a{x, x_scale, w, w_scale, m, n, k, out, out_dtype};
+    if (!codes) {
+        if (!ptr_ok(ws)) return MOE_ERR_INVALID;
+        if (ws_bytes < moe_channel_matmul_workspace_bytes(x_dtype, m, k)) return MOE_ERR_WORKSPACE;
+        int8_t* q = static_cast<int8_t*>(ws);
+        float* s = reinterpret_cast<float*>(q + align256((size_t)m * k));
+        const TokenQuantArgs qa{x, x_dtype, m, m, k, k, k, k, q, s};
+        if (launch_quantize_tokens(qa, st) != hipSuccess) return MOE_ERR_DEVICE;
+        a.x = q;
+        a.xs = s;
+    }
+    return device_status(launch_channel_matmul(a, st));
+}
+
 int moe_topk_rows(const float* scores, int32_t rows, int32_t n, int32_t k, int32_t* idx, float* vals,
                   void** events, void* stream) {
     static_assert(MOE_TOPK_ROWS_MAX_N == TOPK_ROWS_MAX_N, "row top-k limit");
@@ -530,7 +609,7 @@ int moe_prefetch_experts(const moe_config* cfg, const moe_weights* w, const int3
     // every matrix of an expert holds F * d elements: gate and up F rows of d,
     // down d rows of F
     const int64_t elems = (int64_t)cfg->d_ff * cfg->d_model;
-    const int64_t esize = cfg->w_dtype == MOE_DT_F32 ? 4 : cfg->w_dtype == MOE_DT_BF16 ? 2 : 1;  // (F8B128: codes)
+    const int64_t esize = cfg->w_dtype == MOE_DT_F32 ? 4 : cfg->w_dtype == MOE_DT_BF16 ? 2 : 1;  // (F8B128, I8CH: codes)
     if (elems * esize > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;  // one buffer descriptor per expert matrix
     const bool q8 = cfg->w_dtype == MOE_DT_Q8B32;
     const moe_mat* mats[3] = {&w->gate, &w->up, &w->down};
@@ -587,7 +666,7 @@ int moe_expert_ffn(const moe_config* cfg, const void* x, const moe_weights* w, c
     FfnArgs f = ffn_args(cfg, L, ws, x, w, offsets, perm_rows, topk_w);
     f.slot_out = slot_out;
     f.shared_out = cfg->n_shared ? shared_out : nullptr;
-    if (f.wdt == MOE_DT_F8B128 && launch_quantize_rows(f8_quant_args(cfg, L, ws, x), st) != hipSuccess) return MOE_ERR_DEVICE;
+    if (run_quantize_x(cfg, L, ws, x, st) != hipSuccess) return MOE_ERR_DEVICE;
     return device_status(run_expert_kernels(f, L, ws, st));
 }
 
@@ -614,7 +693,7 @@ int moe_layer_forward_grouped(const moe_config* cfg, const moe_groups* groups, c
     GroupArgs g;
     if ((s = check_groups(cfg, groups, &g))) return s;
     if (y_dtype != MOE_DT_F32 && y_dtype != MOE_DT_BF16) return MOE_ERR_INVALID;
-    if (y_dtype == MOE_DT_BF16 && cfg->w_dtype != MOE_DT_F8B128) return MOE_ERR_UNSUPPORTED;
+    if (y_dtype == MOE_DT_BF16 && !is_8bit(cfg)) return MOE_ERR_UNSUPPORTED;
     if ((s = check_ws(cfg, ws, ws_bytes))) return s;
     return enqueue_layer(cfg, g, x, w, y, y_dtype, dbg, ws, stream);
 }
@@ -636,7 +715,7 @@ namespace {
 // The layer's launches over a workspace `ws` already checked to be large enough.
 int enqueue_layer(const moe_config* cfg, const GroupArgs& g, const void* x, const moe_weights* w, void* y, int ydt,
                   moe_debug* dbg, void* ws, void* stream) {
-    const bool decode = cfg->w_dtype != MOE_DT_F8B128 &&  // (e4m3 layers have one path)
+    const bool decode = !is_8bit(cfg) &&  // (those have one path)
                         (cfg->path == MOE_PATH_DECODE ||
                          (cfg->path == MOE_PATH_AUTO && cfg->n_tokens <= MOE_DECODE_MAX_TOKENS));
     const LayerLayout L = make_layout(cfg);
@@ -678,7 +757,7 @@ int enqueue_layer(const moe_config* cfg, const GroupArgs& g, const void* x, cons
         e = launch_router_logits(r, st, kt[0]);
         if (e == hipSuccess) e = run_select(cfg, g, sel, st, kt[1]);
         if (e == hipSuccess) e = launch_permute(pa, st, kt[2]);
-        if (e == hipSuccess && f8) e = launch_quantize_rows(f8_quant_args(cfg, L, ws, x), st);
+        if (e == hipSuccess) e = run_quantize_x(cfg, L, ws, x, st);
     }
     if (e != hipSuccess) return MOE_ERR_DEVICE;
     FfnArgs f = ffn_args(cfg, L, ws, x, w, off, perm, wts);

@@ -1,0 +1,424 @@
+// i8_tile.hip - int8 products for many activation rows per weight matrix.
+//
+//   gate/up:  h[r, c] = silu(x_r Wg_c) (x_r Wu_c), fp32
+//   down:     slot_out[f, :] = w_f (h_r Wd^T), h's rows quantised
+//   dense:    out[m, n] = x_m W_n
+//
+// A workgroup computes a tile of activation rows x weight rows (gate/up: 128
+// gate and the same 128 up rows), each wavefront blocks of 32 x 32 of it.  A stage
+// is 128 columns of K: 128-byte rows, copied straight from global memory into
+// LDS (eight whole cache lines per copy instruction, 16-byte chunks swizzled by
+// row as dma_dev.h describes), in a ring of stages behind one barrier per
+// stage.  The sums stay in int32 accumulators over the whole of K; the scales of
+// rows and columns are applied once, behind the loop.
+//
+// A tile computes only the 32-row blocks that hold rows: blocks are dealt to the
+// two wavefront rows in turn, and each wavefront runs the K loop built for its
+// number of live blocks.
+#include "common.h"
+#include "i8_dev.h"
+#include "tile_dev.h"
+
+namespace moe {
+namespace {
+
+constexpr int TK = F8_BLK;  // columns of a stage
+
+// Expert tiles (256 weight rows) and tiles of the dense product.
+typedef Shape<1, 2, 2, 4, 2> Rows64;
+typedef Shape<2, 2, 2, 4, 3> Rows128;
+typedef Shape<4, 2, 2, 4, 2> Square256;
+typedef Shape<2, 2, 2, 2, 2> Square128;
+typedef Shape<1, 1, 2, 2, 4> Square64;
+
+// Sources of one tile: wave-uniform buffers and 32-bit lane offsets.
+template <class S>
+struct I8Tile {
+    const uint8_t *wbase, *xbase;  // weight rows (of gate or of up), activation rows
+    uint32_t woff[S::WQ];          // the copy lane's bytes of weight copy q, at K = 0
+    uint32_t xoff[S::XQ];
+    int ch;                        // the copy lane's 16-byte chunk in a stage row, in bytes
+    int K;
+    bool once = false;             // no other tile reads these weights
+};
+
+__device__ __forceinline__ i32x4_t tile_chunk(const uint8_t* S, uint32_t at) {
+    return *reinterpret_cast<const i32x4_t*>(S + at);
+}
+
+// The K loop of one wavefront with L live blocks and XC activation copies per
+// stage; acc[i][j]: block i (activation rows) x weight row block j.
+template <class S, int L, int XC, bool EXPERT>
+__device__ __forceinline__ void tile_loop(I8Tile<S> g, uint8_t* const (&W)[S::NST], uint8_t* const (&X)[S::NST],
+                                          i32x16_t (&out)[S::NB][S::NJ]) {
+    constexpr int NST = S::NST, NB = S::NB, NJ = S::NJ, TW = S::W, TWC = S::WQ, NC = TWC + XC;
+    const int wave = wave_index(), mh = wave / S::GN, wn = wave % S::GN;
+    const F8Lane fl = tile_lane(lane_id());
+    g.wbase = uniform_ptr(g.wbase);
+    g.xbase = uniform_ptr(g.xbase);
+    const int nfull = g.K / TK, last = nfull - 1;  // whole stages
+    // (opaque: single registers, not parts of vectors or of 64-bit values)
+#pragma unroll
+    for (int q = 0; q < TWC; ++q) __asm__ volatile("" : "+v"(g.woff[q]));
+#pragma unroll
+    for (int q = 0; q < XC; ++q) __asm__ volatile("" : "+v"(g.xoff[q]));
+    const __amdgpu_buffer_rsrc_t wr = tile_buffer(g.wbase), xr = tile_buffer(g.xbase);
+    // expert weights that no other tile reads are copied non-temporal
+    const bool once = EXPERT && NB == 1 && __builtin_amdgcn_readfirstlane(g.once);
+    // (stages past the end re-read the last; not used)
+    auto issue_at = [&](auto ss, int kb) {
+        uint8_t *w = W[decltype(ss)::value % NST], *x = X[decltype(ss)::value % NST];
+        auto copies = [&](auto nt) {
+#pragma unroll
+            for (int q = 0; q < TWC; ++q)
+                buffer_copy16<decltype(nt)::value != 0>(wr, g.woff[q], min(kb, last) * TK, w + (q * TW + wave) * 1024);
+        };
+        if (once) copies(ic<1>());
+        else copies(ic<0>());
+#pragma unroll
+        for (int q = 0; q < XC; ++q) buffer_copy16(xr, g.xoff[q], min(kb, last) * TK, x + (q * TW + wave) * 1024);
+    };
+    if (nfull > 0) {
+        each<NST - 1>([&](auto ss) { issue_at(ss, decltype(ss)::value); });
+    }
+    i32x16_t acc[NB][NJ];
+    each<NB * NJ>([&](auto b) { acc[decltype(b)::value / NJ][decltype(b)::value % NJ] = i32x16_t{}; });
+    auto products = [&](auto nn) {
+        constexpr int B = decltype(nn)::value % NST;
+        // (opaque: addresses formed from them are not kept over the loop)
+        uint32_t wo = S::WR * wn * TK, xo = 32 * mh * TK;
+        __asm__ volatile("" : "+s"(wo), "+s"(xo));
+        each<4>([&](auto ss) {
+            constexpr int s = decltype(ss)::value;
+            i32x4_t w[NJ], x[NB];
+            each<NJ>([&](auto jj) { w[decltype(jj)::value] = tile_chunk(W[B] + 32 * decltype(jj)::value * TK, fl.o[s] + wo); });
+            each<L>([&](auto ii) { x[decltype(ii)::value] = tile_chunk(X[B] + 32 * S::GM * decltype(ii)::value * TK, fl.o[s] + xo); });
+            each<L * NJ>([&](auto b) {
+                constexpr int i = decltype(b)::value / NJ, j = decltype(b)::value % NJ;
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[j], x[i], acc[i][j], 0, 0, 0);
+            });
+        });
+        wait_lgkm0();  // this stage's reads are done before the next barrier releases its refill
+    };
+    auto stage = [&](auto nn, int kb) {
+        wait_vm<(NST - 2) * NC>();  // all but the copies sent after this stage's last
+        barrier_nofence();
+        issue_at(ic<decltype(nn)::value + NST - 1>(), kb + NST - 1);
+        if constexpr (L > 0) products(nn);
+    };
+    for (int kb = 0; kb < nfull; kb += NST) {
+        each<NST>([&](auto nn) {
+            if (kb + decltype(nn)::value < nfull) stage(nn, kb + decltype(nn)::value);
+        });
+    }
+    if (g.K > nfull * TK) {  // the step that K ends in: columns past K come from a row of zeros
+        wait_vm<0>();
+        barrier_nofence();  // every stage has landed and been read
+        const bool in = g.ch < g.K - nfull * TK;
+        const uint8_t* zero = reinterpret_cast<const uint8_t*>(f8_zeros);
+        // (opaque: or the 64-bit forms of the offsets would be kept over the loop)
+        auto from = [&](const uint8_t* base, uint32_t off) {
+            __asm__ volatile("" : "+v"(off));
+            return in ? base + nfull * TK + off : zero;
+        };
+#pragma unroll
+        for (int q = 0; q < TWC; ++q) copy16(from(g.wbase, g.woff[q]), W[0] + (q * TW + wave) * 1024);
+#pragma unroll
+        for (int q = 0; q < XC; ++q) copy16(from(g.xbase, g.xoff[q]), X[0] + (q * TW + wave) * 1024);
+        wait_vm<0>();
+        barrier_nofence();
+        if constexpr (L > 0) products(ic<0>());
+    }
+    wait_vm<0>();  // no copy may still be writing LDS when the workgroup ends
+    each<NB * NJ>([&](auto b) {
+        constexpr int i = decltype(b)::value / NJ, j = decltype(b)::value % NJ;
+        out[i][j] = acc[i][j];
+    });
+}
+
+// Runs the loop built for this wavefront's live blocks (rows of the tile: nrows).
+template <class S, bool EXPERT>
+__device__ __forceinline__ void tile_run(const I8Tile<S>& g, int nrows, uint8_t* const (&W)[S::NST],
+                                         uint8_t* const (&X)[S::NST], i32x16_t (&acc)[S::NB][S::NJ]) {
+    const int wave = wave_index(), nblk = (nrows + 31) / 32, live = (nblk - wave / S::GN + S::GM - 1) / S::GM;
+    auto run = [&](auto l, auto xc) { tile_loop<S, decltype(l)::value, decltype(xc)::value, EXPERT>(g, W, X, acc); };
+    static_assert(S::GM == 2, "two wavefronts along the activation rows");
+    constexpr int RB = S::W / 4;  // a round of activation copies covers W / 4 blocks
+    if constexpr (S::NB == 4) {
+        static_assert(RB == 2, "eight wavefronts");
+        if (nblk > 6) return live == 4 ? run(ic<4>(), ic<4>()) : run(ic<3>(), ic<4>());
+        if (nblk > 4) return live == 3 ? run(ic<3>(), ic<3>()) : run(ic<2>(), ic<3>());
+    }
+    if constexpr (S::NB >= 2) {
+        if (nblk > 2) return live == 2 ? run(ic<2>(), ic<4 / RB>()) : run(ic<1>(), ic<4 / RB>());
+    }
+    return live == 1 ? run(ic<1>(), ic<2 / RB>()) : run(ic<0>(), ic<2 / RB>());
+}
+
+template <class S, bool EXPERT>
+__device__ __forceinline__ void tile_go(const I8Tile<S>& g, int nrows, uint8_t* const (&WS)[4], uint8_t* const (&XS)[4],
+                                        i32x16_t (&acc)[S::NB][S::NJ]) {
+    ring<S::NST>(WS, [&](auto& W) { ring<S::NST>(XS, [&](auto& X) { tile_run<S, EXPERT>(g, nrows, W, X, acc); }); });
+}
+
+// A block's sums as fp32 with the activation row's scale sx and the lane's
+// weight rows' sw (4 in each 8: element 4 q + v is weight row 8 q + 4 (lane / 32) + v).
+__device__ __forceinline__ f8_f16 scaled(const i32x16_t& p, float sx, const f8_f4 (&sw)[4]) {
+    f8_f16 r;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) r[v] = (float)p[v] * sx * sw[v / 4][v % 4];
+    return r;
+}
+// Those weight rows' scales, from row c of n (rows past the last repeat it).
+__device__ __forceinline__ void tile_scales(const float* s, int c, int n, int lane, f8_f4 (&sw)[4]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int at = c + 8 * q + 4 * (lane >> 5);
+        if (at + 4 <= n) {
+            sw[q] = i8_scales4(s + at);
+        } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) sw[q][v] = s[min(at + v, n - 1)];
+        }
+    }
+}
+
+template <class S>
+__global__ __launch_bounds__(64 * S::W, S::WAVES) void i8_gateup_tile_kernel(I8Ffn a) {
+    constexpr int NB = S::NB, BM = S::BM, HC = S::WR / 2, TW = S::W, TWC = S::WQ;  // h columns per wavefront
+    F8_TILE_LDS(S);
+    int tile, ntile;
+    if (!work_item<4>(tile_count(a.f), tile, ntile)) return;
+    TileRows tr;
+    if (!tile_rows<BM>(a.f, tile, tr)) return;
+    const bool shared = tr.g == a.f.E;
+    const int F = shared ? a.f.Fs : a.f.F, d = a.f.d, n0 = ntile * (S::TN / 2);
+    if (n0 >= F) return;
+    const int lane = lane_id(), wave = wave_index(), mh = wave / S::GN, wn = wave % S::GN;
+    const MatRef& G = shared ? a.f.s_gate : a.f.gate;
+    const MatRef& U = shared ? a.f.s_up : a.f.up;
+    const size_t e = shared ? 0 : tr.g;
+    I8Tile<S> g;
+    g.K = d;
+    // stage rows 2 HC m .. + HC - 1: gate rows n0 + HC m .., the HC rows after
+    // them: the same up rows (a wavefront's copies are 64 rows apart: all of
+    // them gate, or all up)
+    static_assert(64 % (2 * HC) == 0 && TW == 8, "gate and up copies");
+    g.wbase = static_cast<const uint8_t*>((8 * wave & HC) ? U.q : G.q) + (e * F + n0) * d;
+#pragma unroll
+    for (int q = 0; q < TWC; ++q) {
+        const int r8 = 8 * (q * TW + wave), n = HC * (r8 / (2 * HC)) + r8 % HC + (lane >> 3);
+        g.ch = copy_chunk(r8 + (lane >> 3), lane);
+        g.woff[q] = (uint32_t)(min(n, F - 1 - n0) * d + g.ch);
+    }
+    auto token = [&](int r) {  // rows past the tile repeat its first; their results are not stored
+        r = r < tr.nrows ? r : 0;
+        if (shared) return tr.rbeg - a.f.T * a.f.k + r;
+        const int f = a.f.perm_rows[tr.rbeg + r];
+        return f >= 0 && f < a.f.T * a.f.k ? f / a.f.k : 0;
+    };
+    g.xbase = reinterpret_cast<const uint8_t*>(a.xq);  // (T * d is below 2^32)
+#pragma unroll
+    for (int q = 0; q < S::XQ; ++q) g.xoff[q] = (uint32_t)token(copy_row(q * TW + wave, lane)) * d + g.ch;
+    g.once = one_tile<BM>(a.f, tr);
+    i32x16_t acc[NB][S::NJ];
+    tile_go<S, true>(g, tr.nrows, WS, XS, acc);
+    static_assert(S::NJ == 2 && HC == 32, "a block of gate, a block of up");
+    __syncthreads();  // every wavefront has read its last stage
+    const int c0 = n0 + HC * wn;
+    if (c0 >= F) return;  // (F is a multiple of 64)
+    uint8_t* R = out_region<S>(WS, wave);
+    f8_f4 sg[4], su[4];
+    tile_scales(reinterpret_cast<const float*>(G.scale) + e * F, c0, F, lane, sg);
+    tile_scales(reinterpret_cast<const float*>(U.scale) + e * F, c0, F, lane, su);
+    each<NB>([&](auto ii) {
+        constexpr int i = decltype(ii)::value;
+        const int r0 = 32 * (mh + S::GM * i), rows = tr.nrows - r0;
+        if (rows <= 0) return;
+        const float sx = a.xs[token(r0 + (lane & 31))];
+        const f8_f16 ga = scaled(acc[i][0], sx, sg), up = scaled(acc[i][1], sx, su);
+        f8_f16 h;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) h[v] = silu_f32(ga[v]) * up[v];
+        out_put_f32(R, lane, h);
+        out_fence();
+        out_rows<float, f8_u4, 128>(R, lane, a.h + (size_t)(tr.rbeg + r0) * a.f.ldh + c0, a.f.ldh, rows, HC);
+        out_fence();
+    });
+}
+
+template <class S>
+__global__ __launch_bounds__(64 * S::W, S::WAVES) void i8_down_tile_kernel(I8Ffn a) {
+    constexpr int NB = S::NB, BM = S::BM, TN = S::TN, TW = S::W, TWC = S::WQ;
+    F8_TILE_LDS(S);
+    int tile, ntile;
+    if (!work_item<4>(tile_count(a.f), tile, ntile)) return;
+    TileRows tr;
+    if (!tile_rows<BM>(a.f, tile, tr)) return;
+    const bool shared = tr.g == a.f.E;
+    const int F = shared ? a.f.Fs : a.f.F, d = a.f.d, n0 = ntile * TN;
+    const int lane = lane_id(), wave = wave_index(), mh = wave / S::GN, wn = wave % S::GN;
+    const MatRef& D = shared ? a.f.s_down : a.f.down;
+    const size_t e = shared ? 0 : tr.g;
+    I8Tile<S> g;
+    g.K = F;
+#pragma unroll
+    for (int q = 0; q < TWC; ++q) {
+        const int sr = copy_row(q * TW + wave, lane);
+        g.ch = copy_chunk(sr, lane);
+        g.woff[q] = (uint32_t)(min(sr, d - 1 - n0) * F + g.ch);
+    }
+    g.once = one_tile<BM>(a.f, tr);
+    g.wbase = static_cast<const uint8_t*>(D.q) + (e * d + n0) * F;
+    g.xbase = reinterpret_cast<const uint8_t*>(a.hq) + (size_t)tr.rbeg * a.f.ldh;
+#pragma unroll
+    for (int q = 0; q < S::XQ; ++q) {
+        const int sr = copy_row(q * TW + wave, lane);
+        g.xoff[q] = (uint32_t)((sr < tr.nrows ? sr : 0) * a.f.ldh + g.ch);
+    }
+    i32x16_t acc[NB][S::NJ];
+    tile_go<S, true>(g, tr.nrows, WS, XS, acc);
+    float* out = shared ? a.f.shared_out : a.f.slot_out;
+    __syncthreads();  // every wavefront has read its last stage
+    uint8_t* R = out_region<S>(WS, wave);
+    int ln = lane;  // (opaque: nothing formed from it is kept over the loop)
+    __asm__ volatile("" : "+v"(ln));
+    const int c0 = n0 + S::WR * wn;
+    if (c0 >= d) return;  // (d is a multiple of 64)
+    f8_f4 sw[S::NJ][4];
+    each<S::NJ>([&](auto jj) {
+        constexpr int j = decltype(jj)::value;
+        tile_scales(reinterpret_cast<const float*>(D.scale) + e * d, c0 + 32 * j, d, ln, sw[j]);
+    });
+    auto slot = [&](int r) {  // the result row of tile row r, or -1
+        if (r >= tr.nrows) return -1;
+        if (shared) return tr.rbeg - a.f.T * a.f.k + r;
+        const int f = a.f.perm_rows[tr.rbeg + r];
+        return f >= 0 && f < a.f.T * a.f.k ? f : -1;
+    };
+    each<NB>([&](auto ii) {
+        constexpr int i = decltype(ii)::value;
+        const int r0 = 32 * (mh + S::GM * i), r = r0 + (ln & 31);
+        if (r0 >= tr.nrows) return;
+        const int f = slot(r);
+        const float w = shared ? 1.0f : f < 0 ? 0.0f : a.f.topk_w[f];
+        const float sx = a.hs[tr.rbeg + min(r, tr.nrows - 1)];
+        each<S::NJ>([&](auto jj) {
+            constexpr int j = decltype(jj)::value;
+            out_put_f32(R, ln, scaled(acc[i][j], sx, sw[j]) * w);
+            out_fence();
+            const int c = c0 + 32 * j + 4 * (ln & 7);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const f8_f4 v = *reinterpret_cast<const f8_f4*>(R + out_chunk(8 * s + (ln >> 3), ln & 7));
+                const int dst = __shfl(f, 8 * s + (ln >> 3));
+                if (dst >= 0 && c < d) *reinterpret_cast<f8_f4*>(out + (size_t)dst * d + c) = v;
+            }
+            out_fence();
+        });
+    });
+}
+
+template <class S, int OF>
+__global__ __launch_bounds__(64 * S::W) void i8_dense_tile_kernel(ChannelArgs a) {
+    constexpr int NB = S::NB, BM = S::BM, TN = S::TN, TW = S::W, TWC = S::WQ;
+    F8_TILE_LDS(S);
+    // consecutive workgroups go to the 8 XCDs in turn: give each a contiguous
+    // range of the tiles, walked in groups of 4 weight tiles (gemm_dev.h)
+    const int gx = gridDim.x, gy = gridDim.y, L = blockIdx.x + blockIdx.y * gx, N = gx * gy;
+    const int xcd = L % N_XCD, loc = L / N_XCD, qn = N / N_XCD, rn = N % N_XCD;
+    const int at = xcd < rn ? xcd * (qn + 1) + loc : rn * (qn + 1) + (xcd - rn) * qn + loc;
+    const int grp = at / (gx * 4), rem = at % (gx * 4), gs = min(4, gy - grp * 4);
+    const int m0 = rem / gs * BM, n0 = (grp * 4 + rem % gs) * TN, nrows = min(BM, a.m - m0);
+    const int lane = lane_id(), wave = wave_index(), mh = wave / S::GN, wn = wave % S::GN;
+    I8Tile<S> g;
+    g.K = a.k;
+#pragma unroll
+    for (int q = 0; q < TWC; ++q) {
+        const int sr = copy_row(q * TW + wave, lane);
+        g.ch = copy_chunk(sr, lane);
+        g.woff[q] = (uint32_t)(min(sr, a.n - 1 - n0) * a.k + g.ch);
+    }
+    g.wbase = reinterpret_cast<const uint8_t*>(a.wq) + (size_t)n0 * a.k;
+    g.xbase = static_cast<const uint8_t*>(a.x) + (size_t)m0 * a.k;
+#pragma unroll
+    for (int q = 0; q < S::XQ; ++q) g.xoff[q] = (uint32_t)(min(copy_row(q * TW + wave, lane), nrows - 1) * a.k + g.ch);
+    i32x16_t acc[NB][S::NJ];
+    tile_go<S, false>(g, nrows, WS, XS, acc);
+    __syncthreads();  // every wavefront has read its last stage
+    uint8_t* R = out_region<S>(WS, wave);
+    const int c0 = n0 + S::WR * wn;
+    if (c0 >= a.n) return;
+    f8_f4 sw[S::NJ][4];
+    each<S::NJ>([&](auto jj) {
+        constexpr int j = decltype(jj)::value;
+        tile_scales(a.ws, c0 + 32 * j, a.n, lane, sw[j]);
+    });
+    each<NB>([&](auto ii) {
+        constexpr int i = decltype(ii)::value;
+        const int r0 = 32 * (mh + S::GM * i), rows = nrows - r0;
+        if (rows <= 0) return;
+        const float sx = a.xs[m0 + r0 + min(lane & 31, rows - 1)];
+        const size_t at = (size_t)(m0 + r0) * a.n + c0;
+        if constexpr (OF == MOE_DT_BF16) {
+            each<S::NJ>([&](auto jj) {
+                constexpr int j = decltype(jj)::value;
+                out_put_bf16(R, lane, j, scaled(acc[i][j], sx, sw[j]));
+            });
+            out_fence();
+            uint16_t* out = static_cast<uint16_t*>(a.out) + at;
+            constexpr int BYTES = 64 * S::NJ;
+            if (a.n % 8 == 0) out_rows<uint16_t, f8_u4, BYTES>(R, lane, out, a.n, rows, a.n - c0);
+            else if (a.n % 4 == 0) out_rows<uint16_t, uint2, BYTES>(R, lane, out, a.n, rows, a.n - c0);
+            else if (a.n % 2 == 0) out_rows<uint16_t, uint32_t, BYTES>(R, lane, out, a.n, rows, a.n - c0);
+            else out_rows<uint16_t, uint16_t, BYTES>(R, lane, out, a.n, rows, a.n - c0);
+            out_fence();
+        } else {
+            each<S::NJ>([&](auto jj) {
+                constexpr int j = decltype(jj)::value;
+                out_put_f32(R, lane, scaled(acc[i][j], sx, sw[j]));
+                out_fence();
+                float* out = static_cast<float*>(a.out) + at + 32 * j;
+                if (a.n % 4 == 0) out_rows<float, f8_u4, 128>(R, lane, out, a.n, rows, a.n - c0 - 32 * j);
+                else out_rows<float, uint32_t, 128>(R, lane, out, a.n, rows, a.n - c0 - 32 * j);
+                out_fence();
+            });
+        }
+    });
+}
+
+template <class S>
+void dense_launch(const ChannelArgs& a, hipStream_t st) {
+    const dim3 grid((a.m + S::BM - 1) / S::BM, (a.n + S::TN - 1) / S::TN);
+    if (a.odt == MOE_DT_F32) i8_dense_tile_kernel<S, MOE_DT_F32><<<grid, 64 * S::W, 0, st>>>(a);
+    else i8_dense_tile_kernel<S, MOE_DT_BF16><<<grid, 64 * S::W, 0, st>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_i8_gateup(const I8Ffn& a, hipStream_t st, const KTime& kt) {
+    const int fmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F;
+    const dim3 grid(a.f.max_tiles, (fmax + Rows64::TN / 2 - 1) / (Rows64::TN / 2));
+    if (a.f.bm == 64) launch_kernel(i8_gateup_tile_kernel<Rows64>, grid, 64 * Rows64::W, st, kt, a);
+    else launch_kernel(i8_gateup_tile_kernel<Rows128>, grid, 64 * Rows128::W, st, kt, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_i8_down(const I8Ffn& a, hipStream_t st, const KTime& kt) {
+    static_assert(Rows64::TN == Rows128::TN, "one grid");
+    const dim3 grid(a.f.max_tiles, (a.f.d + Rows64::TN - 1) / Rows64::TN);
+    if (a.f.bm == 64) launch_kernel(i8_down_tile_kernel<Rows64>, grid, 64 * Rows64::W, st, kt, a);
+    else launch_kernel(i8_down_tile_kernel<Rows128>, grid, 64 * Rows128::W, st, kt, a);
+    return hipGetLastError();
+}
+
+// The largest tiles that still give most compute units one.
+hipError_t launch_channel_matmul(const ChannelArgs& a, hipStream_t st) {
+    auto tiles = [&](int bm, int tn) { return (long)((a.m + bm - 1) / bm) * ((a.n + tn - 1) / tn); };
+    if (tiles(256, 256) >= 192) dense_launch<Square256>(a, st);
+    else if (tiles(128, 128) >= 192) dense_launch<Square128>(a, st);
+    else dense_launch<Square64>(a, st);
+    return hipGetLastError();
+}
+
+}  // namespace moe

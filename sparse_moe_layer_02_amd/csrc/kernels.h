@@ -79,6 +79,31 @@ bool block_matmul_takes(int xdt, int m, int n);
 hipError_t launch_block_matmul(const BlockArgs& a, hipStream_t st);
 hipError_t launch_block_matmul_tile(const BlockArgs& a, hipStream_t st);  // many rows
 
+// Rows [rows, cols] (row stride ldx elements) to int8 codes (row stride ldq) and
+// one scale per row; from row rows0 on, rows have cols1 columns.
+struct TokenQuantArgs {
+    const void* x;
+    int xdt;  // MOE_DT_F32 or MOE_DT_BF16
+    int64_t rows, rows0;
+    int cols, cols1;
+    int64_t ldx, ldq;
+    int8_t* q;
+    float* s;
+};
+hipError_t launch_quantize_tokens(const TokenQuantArgs& a, hipStream_t st, const KTime& kt = KTime());
+
+// Dense product out[m, n] = x[m, k] w[n, k]^T of int8 codes.
+struct ChannelArgs {
+    const void* x;     // [m, k] codes
+    const float* xs;   // [m]
+    const int8_t* wq;  // [n, k]
+    const float* ws;   // [n]
+    int m, n, k;
+    void* out;         // [m, n]
+    int odt;           // MOE_DT_F32 or MOE_DT_BF16
+};
+hipError_t launch_channel_matmul(const ChannelArgs& a, hipStream_t st);
+
 struct PermArgs {
     const int32_t* topk_idx;
     int T, k, E;
@@ -165,6 +190,17 @@ struct F8Ffn {
     uint8_t *xq, *xe;        // [T, d], [T, f8_scale_ld(d)]
     uint8_t *hq, *he;        // [T*k + T*n_shared, ldh], [.., f8_scale_ld(ldh)]
 };
+// Experts with int8 codes and one scale per weight row.
+struct I8Ffn {
+    FfnArgs f;    // h unused; ldh is the row stride of h and hq
+    int8_t* xq;   // [T, d]
+    float* xs;    // [T]
+    float* h;     // [T*k + T*n_shared, ldh] fp32
+    int8_t* hq;   // the same as codes
+    float* hs;    // their rows' scales
+};
+hipError_t launch_i8_gateup(const I8Ffn& a, hipStream_t st, const KTime& kt = KTime());
+hipError_t launch_i8_down(const I8Ffn& a, hipStream_t st, const KTime& kt = KTime());
 // Selection, grouping and quantisation of x (bf16) in one launch, for up to
 // F8_ROUTE_MAX_T tokens.
 constexpr int F8_ROUTE_MAX_T = 16;
