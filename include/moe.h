@@ -333,6 +333,49 @@ int moe_channel_matmul(const void *x, int32_t x_dtype, const float *x_scale, con
                        int32_t m, int32_t n, int32_t k, void *out, int32_t out_dtype, void *ws, size_t ws_bytes,
                        void *stream);
 
+/* How evenly a selection loads the experts, sequence by sequence.  With s the
+ * scores of cfg->score, p[t, e] = s[t, e] / sum_e s[t, e]:
+ *   counts[q, e]  selections of expert e by the tokens of sequence q
+ *   tokens[q]     tokens of sequence q
+ *   prob[q, e]    mean of p[t, e] over them (0 if there are none)
+ *   loss[q]       sum_e f[q, e] prob[q, e],  f[q, e] = E counts[q, e] / (top_k tokens[q])
+ * so f is 1 and the loss 1 where the load is even.  A caller's balance loss is any
+ * weighted sum of loss[]; its gradient comes from moe_route_backward.
+ * logits [T, E] fp32; topk_idx [T, k] (entries outside [0, E) are not counted);
+ * mask [T] bytes or NULL: tokens whose byte is 0 (padding) belong to no
+ * sequence, and their logits have no effect; seq_offsets [n_seq + 1] int32, in
+ * device memory: sequence q has the tokens seq_offsets[q] <= t < seq_offsets[q +
+ * 1] (ascending values in [0, T], else the results are unspecified; empty
+ * sequences are allowed and tokens before the first or behind the last offset
+ * belong to none), or NULL with n_seq 1: all tokens.  A token whose scores sum
+ * to less than 2^-126 has p = 0.  counts [n_seq, E], tokens [n_seq] int32; prob
+ * [n_seq, E], loss [n_seq] fp32.  Scores are fp32, their sums over tokens fp32
+ * within a workgroup and fp64 beyond, in a fixed order.
+ * 1 <= n_seq <= 2^20, else MOE_ERR_INVALID; the workspace has at least
+ * moe_balance_workspace_bytes(cfg, n_seq) bytes (0 for invalid arguments; monotone
+ * in n_tokens, n_expert and n_seq) and is 16-byte aligned.  Outputs must not
+ * overlap inputs. */
+size_t moe_balance_workspace_bytes(const moe_config *cfg, int32_t n_seq);
+int moe_balance(const moe_config *cfg, const float *logits, const int32_t *topk_idx, const uint8_t *mask,
+                const int32_t *seq_offsets, int32_t n_seq, int32_t *counts, int32_t *tokens, float *prob, float *loss,
+                void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient of the router's logits: d_logits [T, E] fp32 of
+ *   sum_{t, j} d_topk_w[t, j] w[t, j] + sum_q d_loss[q] loss[q]
+ * where w are the selection's weights (route_scale * s, divided by the sum of the
+ * selected s if groups->normalise; groups == NULL: it is 1) and loss is
+ * moe_balance's with its counts as constants, as topk_idx and the expert groups
+ * are.  d_topk_w [T, k] and d_loss [n_seq] may be NULL (one of them at most);
+ * with d_loss, counts and tokens are moe_balance's outputs.  topk_idx entries
+ * outside [0, E) have no weight; an expert listed twice has the sum of both.
+ * Every row is written: rows of tokens that the mask or the offsets leave out are
+ * zeros, whatever their logits and d_topk_w hold.  The other arguments as for
+ * moe_balance.  No workspace; d_logits must not overlap an input. */
+int moe_route_backward(const moe_config *cfg, const moe_groups *groups, const float *logits, const int32_t *topk_idx,
+                       const float *d_topk_w, const uint8_t *mask, const int32_t *seq_offsets, int32_t n_seq,
+                       const int32_t *counts, const int32_t *tokens, const float *d_loss, float *d_logits,
+                       void *stream);
+
 /* Router look-ahead, its read half (NeutronStar fork page, "Cross-layer
  * expert prefetch": the next layer's router runs on this layer's hidden
  * state and the experts it predicts are read while the GPU still computes).

@@ -67,6 +67,7 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_select", "moe_permute", "moe
            "moe_combine", "moe_layer_forward", "moe_layer_forward_noalloc", "moe_topk_rows",
            "moe_prefetch_experts", "moe_select_grouped", "moe_route_grouped", "moe_layer_forward_grouped",
            "moe_quantize_rows", "moe_block_matmul", "moe_quantize_tokens", "moe_channel_matmul",
+           "moe_balance", "moe_route_backward", "moe_balance_workspace_bytes",
            "moe_block_matmul_workspace_bytes", "moe_channel_matmul_workspace_bytes", "moe_status_str")
 STATIC_SCRATCH_BYTES = 64 << 20  # MOE_STATIC_SCRATCH_BYTES
 TOPK_ROWS_MAX_N = 65536  # MOE_TOPK_ROWS_MAX_N
@@ -111,12 +112,16 @@ def load(path: str = LIB_PATH):
     lib.moe_quantize_tokens.argtypes = [P, I, I, I, ctypes.c_int64, P, P, P]
     lib.moe_channel_matmul.argtypes = [P, I, P, P, P, I, I, I, P, I, P, S, P]
     lib.moe_channel_matmul_workspace_bytes.argtypes = [I, I, I]
+    lib.moe_balance.argtypes = [C, P, P, P, P, I, P, P, P, P, P, S, P]
+    lib.moe_route_backward.argtypes = [C, G, P, P, P, P, P, I, P, P, P, P, P]
+    lib.moe_balance_workspace_bytes.argtypes = [C, I]
     lib.moe_status_str.argtypes = [ctypes.c_int]
     lib.moe_status_str.restype = ctypes.c_char_p
     for name in EXPORTS[1:-1]:
         getattr(lib, name).restype = ctypes.c_int
     lib.moe_block_matmul_workspace_bytes.restype = ctypes.c_size_t
     lib.moe_channel_matmul_workspace_bytes.restype = ctypes.c_size_t
+    lib.moe_balance_workspace_bytes.restype = ctypes.c_size_t
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -507,6 +512,76 @@ def moe_channel_matmul(x, x_scale, w, w_scale, out, ws=None, stream=None):
     _same_device(x, x_scale, w, w_scale, out, ws)
     return _call(load().moe_channel_matmul, x.device, stream, ptr(x), xdt, ptr(x_scale), ptr(w), ptr(w_scale), m, n, k,
                  ptr(out), _row_dtype(out), ptr(ws), _bytes(ws))
+
+
+# ---------------------------------------------------------------------------
+# the router's training side: load, balance loss, gradient of the logits
+# ---------------------------------------------------------------------------
+
+def balance_workspace(cfg: moe_config, n_seq=1, device="cuda"):
+    """A workspace tensor for moe_balance of ``n_seq`` sequences."""
+    import torch
+    n = load().moe_balance_workspace_bytes(ctypes.byref(cfg), n_seq)
+    if n == 0:
+        _invalid("config or number of sequences")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_balance_workspace_bytes(cfg: moe_config, n_seq=1) -> int:
+    return load().moe_balance_workspace_bytes(ctypes.byref(cfg), n_seq)
+
+
+def _sequences(cfg, logits, topk_idx, mask, seq_offsets):
+    """Checks of what moe_balance and moe_route_backward share; the number of sequences."""
+    import torch
+    _dense(logits, (cfg.n_tokens, cfg.n_expert), "logits", torch.float32)
+    _dense(topk_idx, (cfg.n_tokens, cfg.top_k), "topk_idx", torch.int32)
+    if mask is not None:
+        if mask.dtype is not torch.bool:
+            _dense(mask, (cfg.n_tokens,), "mask", torch.uint8)
+        _dense(mask, (cfg.n_tokens,), "mask")
+    if seq_offsets is None:
+        return 1
+    if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
+        _invalid("seq_offsets must have one dimension and two values or more")
+    _dense(seq_offsets, (seq_offsets.numel(),), "seq_offsets", torch.int32)
+    return seq_offsets.numel() - 1
+
+
+def moe_balance(cfg, logits, topk_idx, counts, tokens, prob, loss, ws, mask=None, seq_offsets=None, stream=None):
+    """Per sequence: selections of each expert into ``counts`` [n_seq, E] int32, tokens into ``tokens`` [n_seq] int32,
+    mean probabilities into ``prob`` [n_seq, E] and the balance loss into ``loss`` [n_seq] (float32).  ``mask`` [T]
+    bool or uint8 (zero: padding); ``seq_offsets`` [n_seq + 1] int32 (None: one sequence of all tokens)."""
+    import torch
+    n = _sequences(cfg, logits, topk_idx, mask, seq_offsets)
+    _dense(counts, (n, cfg.n_expert), "counts", torch.int32)
+    _dense(tokens, (n,), "tokens", torch.int32)
+    _dense(prob, (n, cfg.n_expert), "prob", torch.float32)
+    _dense(loss, (n,), "loss", torch.float32)
+    _same_device(logits, topk_idx, mask, seq_offsets, counts, tokens, prob, loss, ws)
+    return _call(load().moe_balance, logits.device, stream, ctypes.byref(cfg), ptr(logits), ptr(topk_idx), ptr(mask),
+                 ptr(seq_offsets), n, ptr(counts), ptr(tokens), ptr(prob), ptr(loss), ptr(ws), _bytes(ws))
+
+
+def moe_route_backward(cfg, groups, logits, topk_idx, d_logits, d_topk_w=None, counts=None, tokens=None, d_loss=None,
+                       mask=None, seq_offsets=None, stream=None):
+    """Gradient of the logits into ``d_logits`` [T, E] float32, from the selected weights' ``d_topk_w`` [T, k] and the
+    balance losses' ``d_loss`` [n_seq] (with moe_balance's ``counts`` and ``tokens``); either may be None."""
+    import torch
+    n = _sequences(cfg, logits, topk_idx, mask, seq_offsets)
+    _dense(d_logits, (cfg.n_tokens, cfg.n_expert), "d_logits", torch.float32)
+    if d_topk_w is not None:
+        _dense(d_topk_w, (cfg.n_tokens, cfg.top_k), "d_topk_w", torch.float32)
+    if d_loss is not None:
+        if counts is None or tokens is None:
+            _invalid("d_loss goes with counts and tokens")
+        _dense(d_loss, (n,), "d_loss", torch.float32)
+        _dense(counts, (n, cfg.n_expert), "counts", torch.int32)
+        _dense(tokens, (n,), "tokens", torch.int32)
+    _same_device(logits, topk_idx, mask, seq_offsets, d_logits, d_topk_w, d_loss, counts, tokens)
+    return _call(load().moe_route_backward, logits.device, stream, ctypes.byref(cfg), _ref(groups), ptr(logits),
+                 ptr(topk_idx), ptr(d_topk_w), ptr(mask), ptr(seq_offsets), n, ptr(counts), ptr(tokens), ptr(d_loss),
+                 ptr(d_logits))
 
 
 def workspace(cfg: moe_config, device="cuda"):

@@ -8,6 +8,7 @@
 
 #include <mutex>
 
+#include "balance.h"
 #include "common.h"
 #include "f8_dev.h"
 #include "kernels.h"
@@ -573,6 +574,58 @@ int moe_channel_matmul(const void* x, int32_t x_dtype, const float* x_scale, con
         a.xs = s;
     }
     return device_status(launch_channel_matmul(a, st));
+}
+
+namespace {
+// Partial sums of moe_balance: a slot per range of tokens and per sequence
+// (balance.hip), for the most ranges that any number of tokens up to T makes.
+size_t balance_slots(const moe_config* c, int32_t n_seq) {
+    const int ranges = (c->n_tokens + 15) / 16;
+    return (size_t)(ranges < BALANCE_MAX_RANGES ? ranges : BALANCE_MAX_RANGES) + n_seq;
+}
+bool seqs_ok(const int32_t* off, int32_t n_seq) {
+    return n_seq >= 1 && n_seq <= MAX_TOKENS && (off ? aligned4(off) : n_seq == 1);
+}
+}  // namespace
+
+size_t moe_balance_workspace_bytes(const moe_config* cfg, int32_t n_seq) {
+    if (validate_config(cfg) != MOE_OK || n_seq < 1 || n_seq > MAX_TOKENS) return 0;
+    const size_t slots = balance_slots(cfg, n_seq);
+    return 2 * align256(slots * cfg->n_expert * 4) + align256(slots * 4);
+}
+
+int moe_balance(const moe_config* cfg, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                const int32_t* seq_offsets, int32_t n_seq, int32_t* counts, int32_t* tokens, float* prob, float* loss,
+                void* ws, size_t ws_bytes, void* stream) {
+    int s = validate_config(cfg);
+    if (s) return s;
+    if (!seqs_ok(seq_offsets, n_seq)) return MOE_ERR_INVALID;
+    if (!elt_ok(logits) || !elt_ok(topk_idx) || !elt_ok(counts) || !elt_ok(tokens) || !elt_ok(prob) || !elt_ok(loss))
+        return MOE_ERR_INVALID;
+    if (!ptr_ok(ws)) return MOE_ERR_INVALID;
+    if (ws_bytes < moe_balance_workspace_bytes(cfg, n_seq)) return MOE_ERR_WORKSPACE;
+    const size_t part = align256(balance_slots(cfg, n_seq) * cfg->n_expert * 4);
+    const BalanceArgs a{logits, topk_idx, mask, seq_offsets, cfg->n_tokens, cfg->n_expert, cfg->top_k, cfg->score, n_seq,
+                        balance_chunk(cfg->n_tokens), at<float>(ws, 0), at<int32_t>(ws, part), at<int32_t>(ws, 2 * part),
+                        counts, tokens, prob, loss};
+    return device_status(launch_balance(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_route_backward(const moe_config* cfg, const moe_groups* groups, const float* logits, const int32_t* topk_idx,
+                       const float* d_topk_w, const uint8_t* mask, const int32_t* seq_offsets, int32_t n_seq,
+                       const int32_t* counts, const int32_t* tokens, const float* d_loss, float* d_logits,
+                       void* stream) {
+    int s = validate_config(cfg);
+    if (s) return s;
+    GroupArgs g;
+    if ((s = check_groups(cfg, groups, &g))) return s;
+    if (!seqs_ok(seq_offsets, n_seq) || (!d_topk_w && !d_loss)) return MOE_ERR_INVALID;
+    if (!elt_ok(logits) || !elt_ok(topk_idx) || !opt_elt_ok(d_topk_w) || !opt_elt_ok(d_loss) || !elt_ok(d_logits))
+        return MOE_ERR_INVALID;
+    if (d_loss && (!elt_ok(counts) || !elt_ok(tokens))) return MOE_ERR_INVALID;
+    const RouteGradArgs a{logits, topk_idx, d_topk_w, mask, seq_offsets, counts, tokens, d_loss, d_logits, cfg->n_tokens,
+                          cfg->n_expert, cfg->top_k, cfg->score, n_seq, g.normalise, cfg->route_scale, 0};
+    return device_status(launch_route_backward(a, static_cast<hipStream_t>(stream)));
 }
 
 int moe_topk_rows(const float* scores, int32_t rows, int32_t n, int32_t k, int32_t* idx, float* vals,

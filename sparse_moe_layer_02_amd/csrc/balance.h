@@ -1,0 +1,44 @@
+// balance.h - internal launch interface of the balance loss and the routing's
+// gradient (balance.hip).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+struct BalanceArgs {
+    const float* logits;   // [T, E]
+    const int32_t* idx;    // [T, k]
+    const uint8_t* mask;   // [T] or null
+    const int32_t* off;    // [n_seq + 1] or null: one sequence of all tokens
+    int T, E, k, score, n_seq;
+    int chunk;             // tokens per workgroup (balance_chunk)
+    float* sum;            // [slots, E] workspace; slots = ceil(T / chunk) + n_seq
+    int32_t* cnt;          // [slots, E]
+    int32_t* num;          // [slots] tokens
+    int32_t* counts;       // [n_seq, E]
+    int32_t* tokens;       // [n_seq]
+    float* prob;           // [n_seq, E]
+    float* loss;           // [n_seq]
+};
+constexpr int BALANCE_MAX_RANGES = 256;  // workgroups of the first launch, at most
+int balance_chunk(int T);
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t st);
+
+struct RouteGradArgs {
+    const float* logits;
+    const int32_t* idx;
+    const float* d_w;       // [T, k] or null
+    const uint8_t* mask;
+    const int32_t* off;
+    const int32_t* counts;  // with d_loss
+    const int32_t* tokens;
+    const float* d_loss;    // [n_seq] or null
+    float* d_logits;        // [T, E]
+    int T, E, k, score, n_seq, normalise;
+    float scale;
+    int chunk;              // tokens per wavefront, set by the launcher
+};
+hipError_t launch_route_backward(RouteGradArgs a, hipStream_t st);
+
+}  // namespace moe
