@@ -564,8 +564,12 @@ int moe_channel_matmul(const void* x, int32_t x_dtype, const float* x_scale, con
     hipStream_t st = static_cast<hipStream_t>(stream);
     ChannelArgs a{x, x_scale, w, w_scale, m, n, k, out, out_dtype};
     if (!codes) {
-        if (!ptr_ok(ws)) return MOE_ERR_INVALID;
+        if (!ptr_ok(ws)) return MOE_ERR_INVALID;  // (asked for at every m, though few rows do not use it)
         if (ws_bytes < moe_channel_matmul_workspace_bytes(x_dtype, m, k)) return MOE_ERR_WORKSPACE;
+        if (channel_matmul_takes(m, n, k)) {
+            a.xdt = x_dtype;
+            return device_status(launch_channel_matmul(a, st));
+        }
         int8_t* q = static_cast<int8_t*>(ws);
         float* s = reinterpret_cast<float*>(q + align256((size_t)m * k));
         const TokenQuantArgs qa{x, x_dtype, m, m, k, k, k, k, q, s};

@@ -58,6 +58,30 @@ __device__ __forceinline__ uint32_t i8_pack4(float a, float b, float c, float d,
     return p.none ? 0u : lo | hi;
 }
 
+// Eight columns of a row (16-byte aligned), their largest |x| bits, their codes.
+template <int XF>
+__device__ __forceinline__ void i8_load8(const void* x, size_t at, float (&v)[8]) {
+    if constexpr (XF == MOE_DT_BF16) {
+        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
+        v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
+        v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
+    } else {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+        const float4 u = p[0], w = p[1];
+        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+        v[4] = w.x; v[5] = w.y; v[6] = w.z; v[7] = w.w;
+    }
+}
+__device__ __forceinline__ uint32_t i8_max8(const float (&v)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, f8_abs_bits(v[j]));
+    return m;
+}
+__device__ __forceinline__ uint2 i8_codes8(const float (&v)[8], const I8Scale& p) {
+    return make_uint2(i8_pack4(v[0], v[1], v[2], v[3], p), i8_pack4(v[4], v[5], v[6], v[7], p));
+}
+
 // Four adjacent scales of weight rows (any 4-byte alignment).
 __device__ __forceinline__ f8_f4 i8_scales4(const float* p) {
     f8_f4 v;

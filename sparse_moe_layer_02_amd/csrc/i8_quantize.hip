@@ -15,29 +15,6 @@ constexpr int QT = 256;  // threads per row
 constexpr int QN = 4;    // groups of 8 columns a thread keeps
 
 template <int XF>
-__device__ __forceinline__ void load8(const void* x, size_t at, float (&v)[8]) {
-    if constexpr (XF == MOE_DT_BF16) {
-        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
-        v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
-        v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
-    } else {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-        const float4 u = p[0], w = p[1];
-        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-        v[4] = w.x; v[5] = w.y; v[6] = w.z; v[7] = w.w;
-    }
-}
-__device__ __forceinline__ uint32_t max8(const float (&v)[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, f8_abs_bits(v[j]));
-    return m;
-}
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], const I8Scale& p) {
-    return make_uint2(i8_pack4(v[0], v[1], v[2], v[3], p), i8_pack4(v[4], v[5], v[6], v[7], p));
-}
-
-template <int XF>
 __global__ __launch_bounds__(QT) void quantize_tokens_kernel(TokenQuantArgs a) {
     __shared__ uint32_t part[2][QT / WAVE];
     int at = 0;
@@ -51,18 +28,18 @@ __global__ __launch_bounds__(QT) void quantize_tokens_kernel(TokenQuantArgs a) {
         for (int j = 0; j < QN; ++j) {
             const int c = 8 * (QT * j + threadIdx.x);
             if (c < cols) {
-                load8<XF>(a.x, in + c, v[j]);
+                i8_load8<XF>(a.x, in + c, v[j]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
             }
         }
 #pragma unroll
-        for (int j = 0; j < QN; ++j) m = max(m, max8(v[j]));
+        for (int j = 0; j < QN; ++j) m = max(m, i8_max8(v[j]));
         for (int c = 8 * (QT * QN + threadIdx.x); c < cols; c += 8 * QT) {
             float u[8];
-            load8<XF>(a.x, in + c, u);
-            m = max(m, max8(u));
+            i8_load8<XF>(a.x, in + c, u);
+            m = max(m, i8_max8(u));
         }
         m = wave_max_u32(m);
         // (two sets in turn: a row's maxima are read while the next row's are written)
@@ -77,12 +54,12 @@ __global__ __launch_bounds__(QT) void quantize_tokens_kernel(TokenQuantArgs a) {
 #pragma unroll
         for (int j = 0; j < QN; ++j) {
             const int c = 8 * (QT * j + threadIdx.x);
-            if (c < cols) *reinterpret_cast<uint2*>(out + c) = codes8(v[j], p);
+            if (c < cols) *reinterpret_cast<uint2*>(out + c) = i8_codes8(v[j], p);
         }
         for (int c = 8 * (QT * QN + threadIdx.x); c < cols; c += 8 * QT) {
             float u[8];
-            load8<XF>(a.x, in + c, u);
-            *reinterpret_cast<uint2*>(out + c) = codes8(u, p);
+            i8_load8<XF>(a.x, in + c, u);
+            *reinterpret_cast<uint2*>(out + c) = i8_codes8(u, p);
         }
     }
 }

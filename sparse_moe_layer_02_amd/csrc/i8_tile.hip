@@ -413,7 +413,7 @@ hipError_t launch_i8_down(const I8Ffn& a, hipStream_t st, const KTime& kt) {
 }
 
 // The largest tiles that still give most compute units one.
-hipError_t launch_channel_matmul(const ChannelArgs& a, hipStream_t st) {
+hipError_t launch_channel_matmul_tile(const ChannelArgs& a, hipStream_t st) {
     auto tiles = [&](int bm, int tn) { return (long)((a.m + bm - 1) / bm) * ((a.n + tn - 1) / tn); };
     if (tiles(256, 256) >= 192) dense_launch<Square256>(a, st);
     else if (tiles(128, 128) >= 192) dense_launch<Square128>(a, st);

@@ -94,15 +94,18 @@ hipError_t launch_quantize_tokens(const TokenQuantArgs& a, hipStream_t st, const
 
 // Dense product out[m, n] = x[m, k] w[n, k]^T of int8 codes.
 struct ChannelArgs {
-    const void* x;     // [m, k] codes
+    const void* x;     // [m, k] codes (or rows of xdt)
     const float* xs;   // [m]
     const int8_t* wq;  // [n, k]
     const float* ws;   // [n]
     int m, n, k;
     void* out;         // [m, n]
     int odt;           // MOE_DT_F32 or MOE_DT_BF16
+    int xdt = MOE_DT_I8CH;  // where channel_matmul_takes says so, MOE_DT_F32 or MOE_DT_BF16 rows (xs unused)
 };
+bool channel_matmul_takes(int m, int n, int k);
 hipError_t launch_channel_matmul(const ChannelArgs& a, hipStream_t st);
+hipError_t launch_channel_matmul_tile(const ChannelArgs& a, hipStream_t st);  // many rows
 
 struct PermArgs {
     const int32_t* topk_idx;
