@@ -26,11 +26,13 @@ namespace {
 
 constexpr int SW = 8;  // wavefronts per workgroup
 constexpr int SK = 64; // columns of a step
+// Steps loaded at once.  A wavefront's share of K is a multiple of them: with 8 at
+// once and 12 for a wavefront the loads past its end, repeats of its last step,
+// cost more than they hid (1 x 4096 x 6144: 9.7 us, 7.3 so; non-temporal loads 7.9;
+// two groups ahead in place of one 8.1; 24576 x 6144: 30 us, 5.0 TB/s).
+constexpr int UU = 4;
 constexpr int I8_FUSE_VALUES = 24 * 1024;  // values a workgroup quantises itself, at most (their codes lie in LDS)
 
-__device__ __forceinline__ i32x4_t ld_weights(const int8_t* p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const i32x4_t*>(p));
-}
 __device__ __forceinline__ i32x4_t ld_codes(const int8_t* p) { return *reinterpret_cast<const i32x4_t*>(p); }
 __device__ __forceinline__ i32x4_t dot16(i32x4_t w, i32x4_t x, i32x4_t c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, c, 0, 0, 0);
@@ -55,7 +57,7 @@ __device__ __forceinline__ void stream(const int8_t* const (&wp)[NR], X x, int s
         for (int u = 0; u < U; ++u) {
             const int c = min(SK * min(s + u, s1 - 1) + lo, K - 16);
 #pragma unroll
-            for (int r = 0; r < NR; ++r) f.w[u][r] = ld_weights(wp[r] + c);
+            for (int r = 0; r < NR; ++r) f.w[u][r] = ld_codes(wp[r] + c);
             if constexpr (!LX) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) f.x[u][t] = x(t, c);
@@ -82,7 +84,6 @@ __device__ __forceinline__ void stream(const int8_t* const (&wp)[NR], X x, int s
     F a, b;
     if (s0 < s1) load(a, s0);
     between();
-    if (s0 >= s1) return;
     for (int s = s0; s < s1; s += 2 * U) {
         if (s + U < s1) load(b, s + U);
         compute(a, s);
@@ -170,16 +171,16 @@ __global__ __launch_bounds__(WAVE * SW) void i8_dense_stream_kernel(ChannelArgs 
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) xr[t] = min(m0 + 16 * t + lane % 16, a.m - 1);
-    const int per = (steps + SW - 1) / SW, s0 = wave * per, s1 = min(steps, s0 + per);
+    const int per = (steps + SW * UU - 1) / (SW * UU) * UU, s0 = wave * per, s1 = min(steps, s0 + per);
     if constexpr (LX) {
-        stream<NR, NT, 8 / NR, true>(
+        stream<NR, NT, UU, true>(
             wp, [&](int t, int c) { return *reinterpret_cast<const i32x4_t*>(codes + xr[t] * a.k + c); }, s0, s1, a.k, acc,
             [&] { rows_to_lds<XF>(a.x, a.m, a.k, a.k, codes, a.k, top, scales); });
     } else {
         const int8_t* xp[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) xp[t] = static_cast<const int8_t*>(a.x) + (size_t)xr[t] * a.k;
-        stream<NR, NT, 8 / NR, false>(wp, [&](int t, int c) { return ld_codes(xp[t] + c); }, s0, s1, a.k, acc, [] {});
+        stream<NR, NT, UU, false>(wp, [&](int t, int c) { return ld_codes(xp[t] + c); }, s0, s1, a.k, acc, [] {});
     }
 #pragma unroll
     for (int r = 0; r < NR; ++r)
