@@ -42,18 +42,24 @@ struct I8Tile {
     bool once = false;             // no other tile reads these weights
 };
 
-__device__ __forceinline__ i32x4_t tile_chunk(const uint8_t* S, uint32_t at) {
-    return *reinterpret_cast<const i32x4_t*>(S + at);
-}
+// A wavefront's sums: rows of 16 activation rows (two in a block), 16 weight
+// rows.  Lane l holds weight rows 4 (l / 16) + v of activation row l % 16.
+template <class S>
+struct I8Sums {
+    i32x4_t v[2 * S::NB][2 * S::NJ];
+};
 
 // The K loop of one wavefront with L live blocks and XC activation copies per
-// stage; acc[i][j]: block i (activation rows) x weight row block j.
+// stage.
 template <class S, int L, int XC, bool EXPERT>
 __device__ __forceinline__ void tile_loop(I8Tile<S> g, uint8_t* const (&W)[S::NST], uint8_t* const (&X)[S::NST],
-                                          i32x16_t (&out)[S::NB][S::NJ]) {
+                                          I8Sums<S>& out) {
     constexpr int NST = S::NST, NB = S::NB, NJ = S::NJ, TW = S::W, TWC = S::WQ, NC = TWC + XC;
     const int wave = wave_index(), mh = wave / S::GN, wn = wave % S::GN;
-    const F8Lane fl = tile_lane(lane_id());
+    const int lane = lane_id();
+    uint32_t ro[2];  // this lane's 16 bytes of 16 rows of a stage, of its first and second 64 columns
+#pragma unroll
+    for (int h = 0; h < 2; ++h) ro[h] = (lane & 15) * TK + (((4 * h + (lane >> 4)) ^ pair_swz(lane & 15)) << 4);
     g.wbase = uniform_ptr(g.wbase);
     g.xbase = uniform_ptr(g.xbase);
     const int nfull = g.K / TK, last = nfull - 1;  // whole stages
@@ -65,7 +71,7 @@ __device__ __forceinline__ void tile_loop(I8Tile<S> g, uint8_t* const (&W)[S::NS
     const __amdgpu_buffer_rsrc_t wr = tile_buffer(g.wbase), xr = tile_buffer(g.xbase);
     // expert weights that no other tile reads are copied non-temporal
     const bool once = EXPERT && NB == 1 && __builtin_amdgcn_readfirstlane(g.once);
-    // (stages past the end re-read the last; not used)
+    // (stages past the end re-read the last; not multiplied)
     auto issue_at = [&](auto ss, int kb) {
         uint8_t *w = W[decltype(ss)::value % NST], *x = X[decltype(ss)::value % NST];
         auto copies = [&](auto nt) {
@@ -78,41 +84,79 @@ __device__ __forceinline__ void tile_loop(I8Tile<S> g, uint8_t* const (&W)[S::NS
 #pragma unroll
         for (int q = 0; q < XC; ++q) buffer_copy16(xr, g.xoff[q], min(kb, last) * TK, x + (q * TW + wave) * 1024);
     };
-    if (nfull > 0) {
-        each<NST - 1>([&](auto ss) { issue_at(ss, decltype(ss)::value); });
-    }
-    i32x16_t acc[NB][NJ];
-    each<NB * NJ>([&](auto b) { acc[decltype(b)::value / NJ][decltype(b)::value % NJ] = i32x16_t{}; });
-    auto products = [&](auto nn) {
-        constexpr int B = decltype(nn)::value % NST;
-        // (opaque: addresses formed from them are not kept over the loop)
-        uint32_t wo = S::WR * wn * TK, xo = 32 * mh * TK;
-        __asm__ volatile("" : "+s"(wo), "+s"(xo));
-        each<4>([&](auto ss) {
-            constexpr int s = decltype(ss)::value;
-            i32x4_t w[NJ], x[NB];
-            each<NJ>([&](auto jj) { w[decltype(jj)::value] = tile_chunk(W[B] + 32 * decltype(jj)::value * TK, fl.o[s] + wo); });
-            each<L>([&](auto ii) { x[decltype(ii)::value] = tile_chunk(X[B] + 32 * S::GM * decltype(ii)::value * TK, fl.o[s] + xo); });
-            each<L * NJ>([&](auto b) {
-                constexpr int i = decltype(b)::value / NJ, j = decltype(b)::value % NJ;
-                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[j], x[i], acc[i][j], 0, 0, 0);
-            });
-        });
-        wait_lgkm0();  // this stage's reads are done before the next barrier releases its refill
+    I8Sums<S> acc;
+    each<4 * NB * NJ>([&](auto b) { acc.v[decltype(b)::value / (2 * NJ)][decltype(b)::value % (2 * NJ)] = i32x4_t{0, 0, 0, 0}; });
+    // A stage is NR reads of 16 activation rows, those of its first 64 columns
+    // and those of its second; each is multiplied with the wavefront's weight
+    // rows while the XR reads behind it are on their way, across the stages' ends.
+    constexpr int NR = 4 * L, XR = L > 1 ? 4 : 2;
+    i32x4_t w[2][2 * NJ], x[XR];
+    // (opaque: addresses formed from them are not kept over the loop)
+    auto at = [&](auto hh, int rows) {
+        uint32_t o = rows * TK;
+        __asm__ volatile("" : "+s"(o));
+        return ro[decltype(hh)::value] + o;
     };
+    auto read_w = [&](auto nn, auto hh) {
+        constexpr int B = decltype(nn)::value % NST, h = decltype(hh)::value;
+        const uint32_t o = at(hh, S::WR * wn);
+        each<2 * NJ>([&](auto jj) {
+            w[h][decltype(jj)::value] = *reinterpret_cast<const i32x4_t*>(W[B] + 16 * decltype(jj)::value * TK + o);
+        });
+    };
+    auto read_x = [&](auto nn, auto rr) {  // (r >= NR: of the next stage)
+        constexpr int r = decltype(rr)::value, B = (decltype(nn)::value + r / NR) % NST, h = r % NR / (2 * L), b = r % (2 * L);
+        x[r % XR] = *reinterpret_cast<const i32x4_t*>(X[B] + (32 * S::GM * (b / 2) + 16 * (b % 2)) * TK + at(ic<h>(), 32 * mh));
+    };
+    auto multiply = [&](auto rr) {
+        constexpr int r = decltype(rr)::value, h = r / (2 * L), b = r % (2 * L);
+        each<2 * NJ>([&](auto jj) {
+            constexpr int j = decltype(jj)::value;
+            acc.v[b][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h][j], x[r % XR], acc.v[b][j], 0, 0, 0);
+        });
+    };
+    // Stage kb; the first weights and the first XR reads of it are on their way.
     auto stage = [&](auto nn, int kb) {
-        wait_vm<(NST - 2) * NC>();  // all but the copies sent after this stage's last
-        barrier_nofence();
-        issue_at(ic<decltype(nn)::value + NST - 1>(), kb + NST - 1);
-        if constexpr (L > 0) products(nn);
+        constexpr int n = decltype(nn)::value;
+        if constexpr (L == 0) {
+            wait_vm<(NST - 2) * NC>();
+            barrier_nofence();
+            issue_at(nn, kb + NST);
+        } else {
+            each<NR>([&](auto rr) {
+                constexpr int r = decltype(rr)::value;
+                if constexpr (r == 0) read_w(nn, ic<1>());
+                if constexpr (r + XR == NR) {
+                    // everything this wavefront reads of the stage is in registers: handed over
+                    wait_lgkm0();
+                    wait_vm<(NST - 2) * NC>();  // stage kb + 1 has landed
+                    barrier_nofence();
+                    issue_at(nn, kb + NST);
+                    if constexpr (NR / 2 + XR <= NR) read_w(ic<n + 1>(), ic<0>());
+                }
+                multiply(rr);
+                read_x(nn, ic<r + XR>());
+                pin();
+            });
+        }
     };
-    for (int kb = 0; kb < nfull; kb += NST) {
-        each<NST>([&](auto nn) {
-            if (kb + decltype(nn)::value < nfull) stage(nn, kb + decltype(nn)::value);
-        });
+    if (nfull > 0) {
+        each<NST>([&](auto ss) { issue_at(ss, decltype(ss)::value); });
+        wait_vm<(NST - 1) * NC>();
+        barrier_nofence();
+        if constexpr (L > 0) {
+            read_w(ic<0>(), ic<0>());
+            each<XR>([&](auto rr) { read_x(ic<0>(), rr); });
+        }
+        for (int kb = 0; kb < nfull; kb += NST) {
+            each<NST>([&](auto nn) {
+                if (kb + decltype(nn)::value < nfull) stage(nn, kb + decltype(nn)::value);
+            });
+        }
     }
     if (g.K > nfull * TK) {  // the step that K ends in: columns past K come from a row of zeros
         wait_vm<0>();
+        wait_lgkm0();
         barrier_nofence();  // every stage has landed and been read
         const bool in = g.ch < g.K - nfull * TK;
         const uint8_t* zero = reinterpret_cast<const uint8_t*>(f8_zeros);
@@ -127,19 +171,23 @@ __device__ __forceinline__ void tile_loop(I8Tile<S> g, uint8_t* const (&W)[S::NS
         for (int q = 0; q < XC; ++q) copy16(from(g.xbase, g.xoff[q]), X[0] + (q * TW + wave) * 1024);
         wait_vm<0>();
         barrier_nofence();
-        if constexpr (L > 0) products(ic<0>());
+        if constexpr (L > 0) {
+            read_w(ic<0>(), ic<0>());
+            read_w(ic<0>(), ic<1>());
+            each<NR>([&](auto rr) {
+                read_x(ic<0>(), rr);
+                multiply(rr);
+            });
+        }
     }
     wait_vm<0>();  // no copy may still be writing LDS when the workgroup ends
-    each<NB * NJ>([&](auto b) {
-        constexpr int i = decltype(b)::value / NJ, j = decltype(b)::value % NJ;
-        out[i][j] = acc[i][j];
-    });
+    out = acc;
 }
 
 // Runs the loop built for this wavefront's live blocks (rows of the tile: nrows).
 template <class S, bool EXPERT>
 __device__ __forceinline__ void tile_run(const I8Tile<S>& g, int nrows, uint8_t* const (&W)[S::NST],
-                                         uint8_t* const (&X)[S::NST], i32x16_t (&acc)[S::NB][S::NJ]) {
+                                         uint8_t* const (&X)[S::NST], I8Sums<S>& acc) {
     const int wave = wave_index(), nblk = (nrows + 31) / 32, live = (nblk - wave / S::GN + S::GM - 1) / S::GM;
     auto run = [&](auto l, auto xc) { tile_loop<S, decltype(l)::value, decltype(xc)::value, EXPERT>(g, W, X, acc); };
     static_assert(S::GM == 2, "two wavefronts along the activation rows");
@@ -157,30 +205,33 @@ __device__ __forceinline__ void tile_run(const I8Tile<S>& g, int nrows, uint8_t*
 
 template <class S, bool EXPERT>
 __device__ __forceinline__ void tile_go(const I8Tile<S>& g, int nrows, uint8_t* const (&WS)[4], uint8_t* const (&XS)[4],
-                                        i32x16_t (&acc)[S::NB][S::NJ]) {
+                                        I8Sums<S>& acc) {
     ring<S::NST>(WS, [&](auto& W) { ring<S::NST>(XS, [&](auto& X) { tile_run<S, EXPERT>(g, nrows, W, X, acc); }); });
 }
 
-// A block's sums as fp32 with the activation row's scale sx and the lane's
-// weight rows' sw (4 in each 8: element 4 q + v is weight row 8 q + 4 (lane / 32) + v).
-__device__ __forceinline__ f8_f16 scaled(const i32x16_t& p, float sx, const f8_f4 (&sw)[4]) {
-    f8_f16 r;
+// Sums as fp32 with the activation row's scale sx and the lane's weight rows' sw.
+__device__ __forceinline__ f8_f4 scaled(const i32x4_t& p, float sx, const f8_f4& sw) {
+    f8_f4 r;
 #pragma unroll
-    for (int v = 0; v < 16; ++v) r[v] = (float)p[v] * sx * sw[v / 4][v % 4];
+    for (int v = 0; v < 4; ++v) r[v] = (float)p[v] * sx * sw[v];
     return r;
 }
-// Those weight rows' scales, from row c of n (rows past the last repeat it).
-__device__ __forceinline__ void tile_scales(const float* s, int c, int n, int lane, f8_f4 (&sw)[4]) {
+// Scales of weight rows c .. c + 3 of n (rows past the last repeat it).
+__device__ __forceinline__ f8_f4 tile_scales(const float* s, int c, int n) {
+    if (c + 4 <= n) return i8_scales4(s + c);
+    f8_f4 r;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int at = c + 8 * q + 4 * (lane >> 5);
-        if (at + 4 <= n) {
-            sw[q] = i8_scales4(s + at);
-        } else {
-#pragma unroll
-            for (int v = 0; v < 4; ++v) sw[q][v] = s[min(at + v, n - 1)];
-        }
-    }
+    for (int v = 0; v < 4; ++v) r[v] = s[min(c + v, n - 1)];
+    return r;
+}
+// Results of 16 x 16 to the wavefront's region (tile_dev.h), rows 16 i .. of its
+// 32, columns 16 j .. of its 32 fp32 or 64 bf16.
+__device__ __forceinline__ void put_f32(uint8_t* R, int lane, int i, int j, const f8_f4& p) {
+    *reinterpret_cast<f8_f4*>(R + out_chunk(16 * i + (lane & 15), 4 * j + (lane >> 4))) = p;
+}
+__device__ __forceinline__ void put_bf16(uint8_t* R, int lane, int i, int j, const f8_f4& p) {
+    *reinterpret_cast<uint2*>(R + out_chunk(16 * i + (lane & 15), 2 * j + (lane >> 5)) + 8 * ((lane >> 4) & 1)) =
+        make_uint2(f32_to_bf16(p[0]) | (uint32_t)f32_to_bf16(p[1]) << 16, f32_to_bf16(p[2]) | (uint32_t)f32_to_bf16(p[3]) << 16);
 }
 
 template <class S>
@@ -221,26 +272,35 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void i8_gateup_tile_kernel(I8F
 #pragma unroll
     for (int q = 0; q < S::XQ; ++q) g.xoff[q] = (uint32_t)token(copy_row(q * TW + wave, lane)) * d + g.ch;
     g.once = one_tile<BM>(a.f, tr);
-    i32x16_t acc[NB][S::NJ];
+    I8Sums<S> acc;
     tile_go<S, true>(g, tr.nrows, WS, XS, acc);
     static_assert(S::NJ == 2 && HC == 32, "a block of gate, a block of up");
     __syncthreads();  // every wavefront has read its last stage
     const int c0 = n0 + HC * wn;
     if (c0 >= F) return;  // (F is a multiple of 64)
     uint8_t* R = out_region<S>(WS, wave);
-    f8_f4 sg[4], su[4];
-    tile_scales(reinterpret_cast<const float*>(G.scale) + e * F, c0, F, lane, sg);
-    tile_scales(reinterpret_cast<const float*>(U.scale) + e * F, c0, F, lane, su);
+    f8_f4 sg[2], su[2];  // (the wavefront's first two rows of 16 are gate, the others the same rows of up)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        sg[j] = tile_scales(reinterpret_cast<const float*>(G.scale) + e * F, c0 + 16 * j + 4 * (lane >> 4), F);
+        su[j] = tile_scales(reinterpret_cast<const float*>(U.scale) + e * F, c0 + 16 * j + 4 * (lane >> 4), F);
+    }
     each<NB>([&](auto ii) {
         constexpr int i = decltype(ii)::value;
         const int r0 = 32 * (mh + S::GM * i), rows = tr.nrows - r0;
         if (rows <= 0) return;
-        const float sx = a.xs[token(r0 + (lane & 31))];
-        const f8_f16 ga = scaled(acc[i][0], sx, sg), up = scaled(acc[i][1], sx, su);
-        f8_f16 h;
+        each<2>([&](auto bb) {
+            constexpr int b = decltype(bb)::value;
+            const float sx = a.xs[token(r0 + 16 * b + (lane & 15))];
+            each<2>([&](auto jj) {
+                constexpr int j = decltype(jj)::value;
+                const f8_f4 ga = scaled(acc.v[2 * i + b][j], sx, sg[j]), up = scaled(acc.v[2 * i + b][2 + j], sx, su[j]);
+                f8_f4 h;
 #pragma unroll
-        for (int v = 0; v < 16; ++v) h[v] = silu_f32(ga[v]) * up[v];
-        out_put_f32(R, lane, h);
+                for (int v = 0; v < 4; ++v) h[v] = silu_f32(ga[v]) * up[v];
+                put_f32(R, lane, b, j, h);
+            });
+        });
         out_fence();
         out_rows<float, f8_u4, 128>(R, lane, a.h + (size_t)(tr.rbeg + r0) * a.f.ldh + c0, a.f.ldh, rows, HC);
         out_fence();
@@ -276,7 +336,7 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void i8_down_tile_kernel(I8Ffn
         const int sr = copy_row(q * TW + wave, lane);
         g.xoff[q] = (uint32_t)((sr < tr.nrows ? sr : 0) * a.f.ldh + g.ch);
     }
-    i32x16_t acc[NB][S::NJ];
+    I8Sums<S> acc;
     tile_go<S, true>(g, tr.nrows, WS, XS, acc);
     float* out = shared ? a.f.shared_out : a.f.slot_out;
     __syncthreads();  // every wavefront has read its last stage
@@ -285,11 +345,10 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void i8_down_tile_kernel(I8Ffn
     __asm__ volatile("" : "+v"(ln));
     const int c0 = n0 + S::WR * wn;
     if (c0 >= d) return;  // (d is a multiple of 64)
-    f8_f4 sw[S::NJ][4];
-    each<S::NJ>([&](auto jj) {
-        constexpr int j = decltype(jj)::value;
-        tile_scales(reinterpret_cast<const float*>(D.scale) + e * d, c0 + 32 * j, d, ln, sw[j]);
-    });
+    f8_f4 sw[2 * S::NJ];
+#pragma unroll
+    for (int j = 0; j < 2 * S::NJ; ++j)
+        sw[j] = tile_scales(reinterpret_cast<const float*>(D.scale) + e * d, c0 + 16 * j + 4 * (ln >> 4), d);
     auto slot = [&](int r) {  // the result row of tile row r, or -1
         if (r >= tr.nrows) return -1;
         if (shared) return tr.rbeg - a.f.T * a.f.k + r;
@@ -298,14 +357,22 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void i8_down_tile_kernel(I8Ffn
     };
     each<NB>([&](auto ii) {
         constexpr int i = decltype(ii)::value;
-        const int r0 = 32 * (mh + S::GM * i), r = r0 + (ln & 31);
+        const int r0 = 32 * (mh + S::GM * i);
         if (r0 >= tr.nrows) return;
-        const int f = slot(r);
-        const float w = shared ? 1.0f : f < 0 ? 0.0f : a.f.topk_w[f];
-        const float sx = a.hs[tr.rbeg + min(r, tr.nrows - 1)];
+        const int f = slot(r0 + (ln & 31));
+        float w[2], sx[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int fb = __shfl(f, 16 * b + (ln & 15));
+            w[b] = shared ? 1.0f : fb < 0 ? 0.0f : a.f.topk_w[fb];
+            sx[b] = a.hs[tr.rbeg + min(r0 + 16 * b + (ln & 15), tr.nrows - 1)];
+        }
         each<S::NJ>([&](auto jj) {
             constexpr int j = decltype(jj)::value;
-            out_put_f32(R, ln, scaled(acc[i][j], sx, sw[j]) * w);
+            each<4>([&](auto qq) {
+                constexpr int b = decltype(qq)::value / 2, q = decltype(qq)::value % 2;
+                put_f32(R, ln, b, q, scaled(acc.v[2 * i + b][2 * j + q], sx[b], sw[2 * j + q]) * w[b]);
+            });
             out_fence();
             const int c = c0 + 32 * j + 4 * (ln & 7);
 #pragma unroll
@@ -343,27 +410,27 @@ __global__ __launch_bounds__(64 * S::W) void i8_dense_tile_kernel(ChannelArgs a)
     g.xbase = static_cast<const uint8_t*>(a.x) + (size_t)m0 * a.k;
 #pragma unroll
     for (int q = 0; q < S::XQ; ++q) g.xoff[q] = (uint32_t)(min(copy_row(q * TW + wave, lane), nrows - 1) * a.k + g.ch);
-    i32x16_t acc[NB][S::NJ];
+    I8Sums<S> acc;
     tile_go<S, false>(g, nrows, WS, XS, acc);
     __syncthreads();  // every wavefront has read its last stage
     uint8_t* R = out_region<S>(WS, wave);
     const int c0 = n0 + S::WR * wn;
     if (c0 >= a.n) return;
-    f8_f4 sw[S::NJ][4];
-    each<S::NJ>([&](auto jj) {
-        constexpr int j = decltype(jj)::value;
-        tile_scales(a.ws, c0 + 32 * j, a.n, lane, sw[j]);
-    });
+    f8_f4 sw[2 * S::NJ];
+#pragma unroll
+    for (int j = 0; j < 2 * S::NJ; ++j) sw[j] = tile_scales(a.ws, c0 + 16 * j + 4 * (lane >> 4), a.n);
     each<NB>([&](auto ii) {
         constexpr int i = decltype(ii)::value;
         const int r0 = 32 * (mh + S::GM * i), rows = nrows - r0;
         if (rows <= 0) return;
-        const float sx = a.xs[m0 + r0 + min(lane & 31, rows - 1)];
+        float sx[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) sx[b] = a.xs[m0 + r0 + min(16 * b + (lane & 15), rows - 1)];
         const size_t at = (size_t)(m0 + r0) * a.n + c0;
         if constexpr (OF == MOE_DT_BF16) {
-            each<S::NJ>([&](auto jj) {
-                constexpr int j = decltype(jj)::value;
-                out_put_bf16(R, lane, j, scaled(acc[i][j], sx, sw[j]));
+            each<4 * S::NJ>([&](auto qq) {
+                constexpr int b = decltype(qq)::value / (2 * S::NJ), j = decltype(qq)::value % (2 * S::NJ);
+                put_bf16(R, lane, b, j, scaled(acc.v[2 * i + b][j], sx[b], sw[j]));
             });
             out_fence();
             uint16_t* out = static_cast<uint16_t*>(a.out) + at;
@@ -376,7 +443,10 @@ __global__ __launch_bounds__(64 * S::W) void i8_dense_tile_kernel(ChannelArgs a)
         } else {
             each<S::NJ>([&](auto jj) {
                 constexpr int j = decltype(jj)::value;
-                out_put_f32(R, lane, scaled(acc[i][j], sx, sw[j]));
+                each<4>([&](auto qq) {
+                    constexpr int b = decltype(qq)::value / 2, q = decltype(qq)::value % 2;
+                    put_f32(R, lane, b, q, scaled(acc.v[2 * i + b][2 * j + q], sx[b], sw[2 * j + q]));
+                });
                 out_fence();
                 float* out = static_cast<float*>(a.out) + at + 32 * j;
                 if (a.n % 4 == 0) out_rows<float, f8_u4, 128>(R, lane, out, a.n, rows, a.n - c0 - 32 * j);
