@@ -80,11 +80,16 @@ int validate_config(const moe_config* c) {
 // CU).  int8 weights always take 64-row tiles (grouped_gemm_q8.hip).  e4m3
 // weights: 64 rows, or 128 where experts average 64 or more (f8_tile.hip; whole
 // layers at d 6144, F 2048, 64- / 128-row tiles: 32 rows per expert 1.97 / 2.06 ms,
-// 47 rows 2.25 / 2.37, 64 rows 2.78 / 2.66, 256 rows 8.2 / 7.1).
+// 47 rows 2.25 / 2.37, 64 rows 2.78 / 2.66, 256 rows 8.2 / 7.1).  int8 codes
+// (i8_tile.hip): 64, 128 or 256 rows (the same layers, 64- / 128- / 256-row tiles: 32
+// rows per expert 2.09 / 2.15 / 2.29 ms, 48 rows 2.29 / 2.27 / 2.40, 64 rows 2.62 /
+// 2.42 / 2.55, 94 rows 3.06 / 2.66 / 2.79, 128 rows 3.01 with 128 and 2.95 with 256,
+// 256 rows 4.97 / 4.50).
 int gemm_bm(const moe_config* c) {
     if (c->w_dtype == MOE_DT_Q8B32) return 64;
     const long n = (long)c->n_tokens * c->top_k, e = c->n_expert;
-    if (is_8bit(c)) return n >= 64 * e ? 128 : 64;
+    if (c->w_dtype == MOE_DT_I8CH) return n >= 112 * e ? 256 : n >= 48 * e ? 128 : 64;
+    if (c->w_dtype == MOE_DT_F8B128) return n >= 64 * e ? 128 : 64;
     return n >= 96L * c->n_expert ? 256 : 64;
 }
 

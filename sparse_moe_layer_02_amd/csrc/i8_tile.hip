@@ -24,23 +24,64 @@ namespace {
 
 constexpr int TK = F8_BLK;  // columns of a stage
 
-// Expert tiles (256 weight rows) and tiles of the dense product.
-typedef Shape<1, 2, 2, 4, 2> Rows64;
-typedef Shape<2, 2, 2, 4, 3> Rows128;
-typedef Shape<4, 2, 2, 4, 2> Square256;
-typedef Shape<2, 2, 2, 2, 2> Square128;
-typedef Shape<1, 1, 2, 2, 4> Square64;
+// A tile's shape (tile_dev.h) with rings of NW stages of weights and NX of
+// activation rows.
+template <int NB_, int NJ_, int GM_, int GN_, int NW_, int NX_>
+struct Rings : Shape<NB_, NJ_, GM_, GN_, 2> {
+    typedef Shape<NB_, NJ_, GM_, GN_, 2> Base;
+    static constexpr int NW = NW_, NX = NX_;
+    static constexpr int LDS = NW * Base::WB + NX * Base::XB;
+    static constexpr int WAVES = LDS <= 80 * 1024 && Base::W == 8 ? 4 : 2;  // per SIMD: two workgroups where LDS has room
+    // Half of the wavefronts copy weights, half activation rows: a wavefront waits
+    // for copies in the order it sent them, and the rings are of different lengths.
+    static constexpr int CW = Base::W / 2;                       // copying wavefronts of a kind
+    static constexpr int WQ = Base::WB / 1024 / CW, XQ = Base::XB / 1024 / CW;  // 1 KB copies of each, stage by stage
+    static constexpr int Q = WQ > XQ ? WQ : XQ;
+    static_assert(WQ * CW * 1024 == Base::WB && XQ * CW * 1024 == Base::XB, "whole copies");
+};
+// Expert tiles (256 weight rows): up to 64 rows, two workgroups per compute unit
+// (16 rows per expert: gate/up 1.05 ms, 6.1 TB/s of weights); beyond, all of LDS in
+// one.  The rows come through the L2 as slowly as the weights do (a tile's 786 KB of
+// a 6144-column x beside 31 others' in 4 MB): gate/up of 4096 tokens, 128 rows per
+// expert, stages of weights + of rows: 128-row tiles 4 + 2 2.03 ms, 3 + 3 1.70, 3 + 4
+// 1.69; 256-row tiles 2 + 2 1.72, 3 + 2 1.71, 2 + 3 1.63.  (Weights straight from
+// memory into registers, in the instruction's order, with rows alone in LDS: 1.65
+// to 2.0 ms.  A load of 16 rows x 64 bytes moves 18 bytes a clock and compute unit
+// from the L2, one of 8 rows x 128 bytes 60.)
+typedef Rings<1, 2, 2, 4, 2, 2> Rows64;
+typedef Rings<2, 2, 2, 4, 3, 4> Rows128;
+typedef Rings<4, 2, 2, 4, 2, 3> Rows256;
+// Tiles of the dense product.
+typedef Rings<4, 2, 2, 4, 2, 2> Square256;
+typedef Rings<2, 2, 2, 2, 2, 2> Square128;
+typedef Rings<1, 1, 2, 2, 4, 4> Square64;
 
 // Sources of one tile: wave-uniform buffers and 32-bit lane offsets.
 template <class S>
 struct I8Tile {
-    const uint8_t *wbase, *xbase;  // weight rows (of gate or of up), activation rows
-    uint32_t woff[S::WQ];          // the copy lane's bytes of weight copy q, at K = 0
-    uint32_t xoff[S::XQ];
-    int ch;                        // the copy lane's 16-byte chunk in a stage row, in bytes
+    const uint8_t* base;     // rows of this wavefront's copies: weights (of gate or of up), or activations
+    uint32_t off[S::Q];      // the copy lane's bytes of copy q, at K = 0
+    int ch;                  // the copy lane's 16-byte chunk in a stage row, in bytes
     int K;
-    bool once = false;             // no other tile reads these weights
+    bool once = false;       // no other tile reads these weights
 };
+// Whether this wavefront copies weights, and which row of a stage copy q's lane fills.
+template <class S>
+__device__ __forceinline__ bool copies_weights() { return wave_index() < S::CW; }
+template <class S>
+__device__ __forceinline__ int x_copy(int q) { return q * S::CW + wave_index() % S::CW; }
+// Weights: copies c and c ^ 4 (32 rows apart: gate and up) are different wavefronts'.
+template <class S>
+__device__ __forceinline__ int w_copy(int q) {
+    const int me = wave_index() % S::CW;
+    if constexpr (S::CW != 4) return q * S::CW + me;
+    const int g = 2 * q + (me & 1);
+    return 8 * (g >> 2) + (g & 3) + 4 * (me >> 1);
+}
+template <class S>
+__device__ __forceinline__ int stage_row(int q, int lane) {
+    return copy_row(copies_weights<S>() ? w_copy<S>(q) : x_copy<S>(q), lane);
+}
 
 // A wavefront's sums: rows of 16 activation rows (two in a block), 16 weight
 // rows.  Lane l holds weight rows 4 (l / 16) + v of activation row l % 16.
@@ -49,64 +90,80 @@ struct I8Sums {
     i32x4_t v[2 * S::NB][2 * S::NJ];
 };
 
+// The copies of the loop are written out: the compiler puts waits for copies it
+// knows of before reads of LDS, and where paths or rounds of a ring meet it takes
+// copies just sent for ones the read needs.  Here it sees none, every wait is the
+// loop's own, and the rings need no names of their own for their stages.  (M0,
+// where a copy finds its LDS address, is set with each; nothing the compiler
+// makes of these kernels uses it.)
+// 16 bytes per lane from src + off + k0 to LDS at dst (wave-uniform) + 16 lane.
+template <bool NT>
+__device__ __forceinline__ void send16(i32x4_t src, uint32_t off, int k0, uint32_t dst) {
+    if constexpr (NT)
+        __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+                         :
+                         : "s"(dst), "v"(off), "s"(src), "s"(k0)
+                         : "memory");
+    else
+        __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                         :
+                         : "s"(dst), "v"(off), "s"(src), "s"(k0)
+                         : "memory");
+}
+// The same from an address of the lane's own.
+__device__ __forceinline__ void send16_from(const uint8_t* src, uint32_t dst) {
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(dst), "v"(src) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(uint8_t* p) { return (uint32_t)reinterpret_cast<uintptr_t>((lds_void*)p); }
+
 // The K loop of one wavefront with L live blocks and XC activation copies per
-// stage.
+// stage; lds: the ring of weights, then the ring of activation rows.
 template <class S, int L, int XC, bool EXPERT>
-__device__ __forceinline__ void tile_loop(I8Tile<S> g, uint8_t* const (&W)[S::NST], uint8_t* const (&X)[S::NST],
-                                          I8Sums<S>& out) {
-    constexpr int NST = S::NST, NB = S::NB, NJ = S::NJ, TW = S::W, TWC = S::WQ, NC = TWC + XC;
-    const int wave = wave_index(), mh = wave / S::GN, wn = wave % S::GN;
-    const int lane = lane_id();
+__device__ __forceinline__ void tile_loop(I8Tile<S> g, uint8_t* lds, I8Sums<S>& acc) {
+    constexpr int NW = S::NW, NX = S::NX, NB = S::NB, NJ = S::NJ, WC = S::WQ, WB = S::WB, XB = S::XB;
+    uint8_t *const W = lds, *const X = lds + NW * WB;
+    const int wave = wave_index(), mh = wave / S::GN, wn = wave % S::GN, lane = lane_id();
     uint32_t ro[2];  // this lane's 16 bytes of 16 rows of a stage, of its first and second 64 columns
 #pragma unroll
     for (int h = 0; h < 2; ++h) ro[h] = (lane & 15) * TK + (((4 * h + (lane >> 4)) ^ pair_swz(lane & 15)) << 4);
-    g.wbase = uniform_ptr(g.wbase);
-    g.xbase = uniform_ptr(g.xbase);
+    const bool cw = copies_weights<S>();
     const int nfull = g.K / TK, last = nfull - 1;  // whole stages
-    // (opaque: single registers, not parts of vectors or of 64-bit values)
-#pragma unroll
-    for (int q = 0; q < TWC; ++q) __asm__ volatile("" : "+v"(g.woff[q]));
-#pragma unroll
-    for (int q = 0; q < XC; ++q) __asm__ volatile("" : "+v"(g.xoff[q]));
-    const __amdgpu_buffer_rsrc_t wr = tile_buffer(g.wbase), xr = tile_buffer(g.xbase);
+    const uint64_t base = reinterpret_cast<uint64_t>(uniform_ptr(g.base));
+    const i32x4_t src = {(int)(uint32_t)base, (int)(uint32_t)(base >> 32) & 0xFFFF, -1, 0x00020000};
+    const uint32_t w0 = lds_address(W), x0 = lds_address(X);
     // expert weights that no other tile reads are copied non-temporal
     const bool once = EXPERT && NB == 1 && __builtin_amdgcn_readfirstlane(g.once);
     // (stages past the end re-read the last; not multiplied)
-    auto issue_at = [&](auto ss, int kb) {
-        uint8_t *w = W[decltype(ss)::value % NST], *x = X[decltype(ss)::value % NST];
-        auto copies = [&](auto nt) {
+    auto send = [&](int kb, uint32_t ws, uint32_t xs) {  // stage kb's weights to W + ws, or its rows to X + xs
+        const int k0 = min(kb, last) * TK;
+        auto weights = [&](auto nt) {
 #pragma unroll
-            for (int q = 0; q < TWC; ++q)
-                buffer_copy16<decltype(nt)::value != 0>(wr, g.woff[q], min(kb, last) * TK, w + (q * TW + wave) * 1024);
+            for (int q = 0; q < WC; ++q) send16<decltype(nt)::value != 0>(src, g.off[q], k0, w0 + ws + w_copy<S>(q) * 1024);
         };
-        if (once) copies(ic<1>());
-        else copies(ic<0>());
+        if (!cw) {
 #pragma unroll
-        for (int q = 0; q < XC; ++q) buffer_copy16(xr, g.xoff[q], min(kb, last) * TK, x + (q * TW + wave) * 1024);
+            for (int q = 0; q < XC; ++q) send16<false>(src, g.off[q], k0, x0 + xs + x_copy<S>(q) * 1024);
+        } else if (once) {
+            weights(ic<1>());
+        } else {
+            weights(ic<0>());
+        }
     };
-    I8Sums<S> acc;
     each<4 * NB * NJ>([&](auto b) { acc.v[decltype(b)::value / (2 * NJ)][decltype(b)::value % (2 * NJ)] = i32x4_t{0, 0, 0, 0}; });
     // A stage is NR reads of 16 activation rows, those of its first 64 columns
     // and those of its second; each is multiplied with the wavefront's weight
     // rows while the XR reads behind it are on their way, across the stages' ends.
-    constexpr int NR = 4 * L, XR = L > 1 ? 4 : 2;
+    constexpr int NR = 4 * L, XR = L > 1 ? 4 : 2;  // (L == 0: none)
     i32x4_t w[2][2 * NJ], x[XR];
-    // (opaque: addresses formed from them are not kept over the loop)
-    auto at = [&](auto hh, int rows) {
-        uint32_t o = rows * TK;
-        __asm__ volatile("" : "+s"(o));
-        return ro[decltype(hh)::value] + o;
+    uint32_t ws = 0, xs = 0;  // the stage's places in the rings
+    auto read_w = [&](auto hh) {
+        constexpr int h = decltype(hh)::value;
+        const uint8_t* p = W + (ro[h] + (ws + S::WR * wn * TK));
+        each<2 * NJ>([&](auto jj) { w[h][decltype(jj)::value] = *reinterpret_cast<const i32x4_t*>(p + 16 * decltype(jj)::value * TK); });
     };
-    auto read_w = [&](auto nn, auto hh) {
-        constexpr int B = decltype(nn)::value % NST, h = decltype(hh)::value;
-        const uint32_t o = at(hh, S::WR * wn);
-        each<2 * NJ>([&](auto jj) {
-            w[h][decltype(jj)::value] = *reinterpret_cast<const i32x4_t*>(W[B] + 16 * decltype(jj)::value * TK + o);
-        });
-    };
-    auto read_x = [&](auto nn, auto rr) {  // (r >= NR: of the next stage)
-        constexpr int r = decltype(rr)::value, B = (decltype(nn)::value + r / NR) % NST, h = r % NR / (2 * L), b = r % (2 * L);
-        x[r % XR] = *reinterpret_cast<const i32x4_t*>(X[B] + (32 * S::GM * (b / 2) + 16 * (b % 2)) * TK + at(ic<h>(), 32 * mh));
+    auto read_x = [&](auto rr) {
+        constexpr int r = decltype(rr)::value, h = r / (2 * L), b = r % (2 * L);
+        x[r % XR] = *reinterpret_cast<const i32x4_t*>(X + (ro[h] + (xs + 32 * mh * TK)) + (32 * S::GM * (b / 2) + 16 * (b % 2)) * TK);
     };
     auto multiply = [&](auto rr) {
         constexpr int r = decltype(rr)::value, h = r / (2 * L), b = r % (2 * L);
@@ -115,98 +172,114 @@ __device__ __forceinline__ void tile_loop(I8Tile<S> g, uint8_t* const (&W)[S::NS
             acc.v[b][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h][j], x[r % XR], acc.v[b][j], 0, 0, 0);
         });
     };
-    // Stage kb; the first weights and the first XR reads of it are on their way.
-    auto stage = [&](auto nn, int kb) {
-        constexpr int n = decltype(nn)::value;
-        if constexpr (L == 0) {
-            wait_vm<(NST - 2) * NC>();
-            barrier_nofence();
-            issue_at(nn, kb + NST);
-        } else {
-            each<NR>([&](auto rr) {
-                constexpr int r = decltype(rr)::value;
-                if constexpr (r == 0) read_w(nn, ic<1>());
-                if constexpr (r + XR == NR) {
-                    // everything this wavefront reads of the stage is in registers: handed over
-                    wait_lgkm0();
-                    wait_vm<(NST - 2) * NC>();  // stage kb + 1 has landed
-                    barrier_nofence();
-                    issue_at(nn, kb + NST);
-                    if constexpr (NR / 2 + XR <= NR) read_w(ic<n + 1>(), ic<0>());
-                }
-                multiply(rr);
-                read_x(nn, ic<r + XR>());
+    // The products of a stage but the last XR, whose operands are on their way then.
+    auto begin = [&] {
+        each<(L > 0 ? NR - XR : 0)>([&](auto rr) {
+            constexpr int r = decltype(rr)::value;
+            if constexpr (r == 0) read_w(ic<1>());
+            multiply(rr);
+            read_x(ic<r + XR>());
+            pin();
+        });
+    };
+    auto end = [&](auto more) {
+        if constexpr (L > 0) {
+            if constexpr (decltype(more)::value != 0) read_w(ic<0>());
+            each<XR>([&](auto rr) {
+                multiply(ic<NR - XR + decltype(rr)::value>());
+                if constexpr (decltype(more)::value != 0) read_x(rr);
                 pin();
             });
         }
     };
     if (nfull > 0) {
-        each<NST>([&](auto ss) { issue_at(ss, decltype(ss)::value); });
-        wait_vm<(NST - 1) * NC>();
+        if (cw) {
+#pragma unroll
+            for (int s = 0; s < NW; ++s) send(s, s * WB, 0);
+            wait_vm<(NW - 1) * WC>();
+        } else {
+#pragma unroll
+            for (int s = 0; s < NX; ++s) send(s, 0, s * XB);
+            wait_vm<(NX - 1) * XC>();
+        }
         barrier_nofence();
         if constexpr (L > 0) {
-            read_w(ic<0>(), ic<0>());
-            each<XR>([&](auto rr) { read_x(ic<0>(), rr); });
+            read_w(ic<0>());
+            each<XR>([&](auto rr) { read_x(rr); });
         }
-        for (int kb = 0; kb < nfull; kb += NST) {
-            each<NST>([&](auto nn) {
-                if (kb + decltype(nn)::value < nfull) stage(nn, kb + decltype(nn)::value);
-            });
+        begin();
+        for (int kb = 1; kb < nfull; ++kb) {
+            // From stage kb - 1 to stage kb: everything this wavefront reads of the first
+            // is in registers, so its place is free; the last products of the one are
+            // made while the first operands of the other are read.
+            wait_lgkm0();
+            if (cw) wait_vm<(NW - 2) * WC>();
+            else wait_vm<(NX - 2) * XC>();
+            barrier_nofence();
+            send(kb - 1 + (cw ? NW : NX), ws, xs);
+            ws = ws == (NW - 1) * WB ? 0 : ws + WB;
+            xs = xs == (NX - 1) * XB ? 0 : xs + XB;
+            end(ic<1>());
+            begin();
         }
-    }
-    if (g.K > nfull * TK) {  // the step that K ends in: columns past K come from a row of zeros
+        end(ic<0>());
         wait_vm<0>();
         wait_lgkm0();
         barrier_nofence();  // every stage has landed and been read
+    }
+    if (g.K > nfull * TK) {  // the step that K ends in: columns past K come from a row of zeros
+        ws = xs = 0;
         const bool in = g.ch < g.K - nfull * TK;
         const uint8_t* zero = reinterpret_cast<const uint8_t*>(f8_zeros);
-        // (opaque: or the 64-bit forms of the offsets would be kept over the loop)
-        auto from = [&](const uint8_t* base, uint32_t off) {
-            __asm__ volatile("" : "+v"(off));
-            return in ? base + nfull * TK + off : zero;
+        auto tail = [&](uint32_t to, auto count, auto copy) {
+#pragma unroll
+            for (int q = 0; q < decltype(count)::value; ++q) {
+                uint32_t off = g.off[q];  // (opaque: or its 64-bit form would be kept over the loop)
+                __asm__ volatile("" : "+v"(off));
+                send16_from(in ? g.base + nfull * TK + off : zero, to + copy(q) * 1024);
+            }
         };
-#pragma unroll
-        for (int q = 0; q < TWC; ++q) copy16(from(g.wbase, g.woff[q]), W[0] + (q * TW + wave) * 1024);
-#pragma unroll
-        for (int q = 0; q < XC; ++q) copy16(from(g.xbase, g.xoff[q]), X[0] + (q * TW + wave) * 1024);
+        if (cw) tail(w0, ic<WC>(), [](int q) { return w_copy<S>(q); });
+        else tail(x0, ic<XC>(), [](int q) { return x_copy<S>(q); });
         wait_vm<0>();
         barrier_nofence();
         if constexpr (L > 0) {
-            read_w(ic<0>(), ic<0>());
-            read_w(ic<0>(), ic<1>());
+            read_w(ic<0>());
+            read_w(ic<1>());
             each<NR>([&](auto rr) {
-                read_x(ic<0>(), rr);
+                read_x(rr);
                 multiply(rr);
             });
         }
+        wait_lgkm0();
+        barrier_nofence();  // every wavefront has read its last stage: LDS is the results' now
     }
-    wait_vm<0>();  // no copy may still be writing LDS when the workgroup ends
-    out = acc;
 }
 
 // Runs the loop built for this wavefront's live blocks (rows of the tile: nrows).
+// No copy is on its way and no stage is read when it returns.
 template <class S, bool EXPERT>
-__device__ __forceinline__ void tile_run(const I8Tile<S>& g, int nrows, uint8_t* const (&W)[S::NST],
-                                         uint8_t* const (&X)[S::NST], I8Sums<S>& acc) {
+__device__ __forceinline__ void tile_go(const I8Tile<S>& g, int nrows, uint8_t* lds, I8Sums<S>& acc) {
     const int wave = wave_index(), nblk = (nrows + 31) / 32, live = (nblk - wave / S::GN + S::GM - 1) / S::GM;
-    auto run = [&](auto l, auto xc) { tile_loop<S, decltype(l)::value, decltype(xc)::value, EXPERT>(g, W, X, acc); };
+    auto run = [&](auto l, auto xc) { tile_loop<S, decltype(l)::value, decltype(xc)::value, EXPERT>(g, lds, acc); };
     static_assert(S::GM == 2, "two wavefronts along the activation rows");
-    constexpr int RB = S::W / 4;  // a round of activation copies covers W / 4 blocks
+    constexpr int PB = 4 / S::CW;  // copies per wavefront and block of 32 rows
+    static_assert(PB * S::CW == 4, "whole copies");
     if constexpr (S::NB == 4) {
-        static_assert(RB == 2, "eight wavefronts");
-        if (nblk > 6) return live == 4 ? run(ic<4>(), ic<4>()) : run(ic<3>(), ic<4>());
-        if (nblk > 4) return live == 3 ? run(ic<3>(), ic<3>()) : run(ic<2>(), ic<3>());
+        if (nblk > 6) return live == 4 ? run(ic<4>(), ic<8 * PB>()) : run(ic<3>(), ic<8 * PB>());
+        if (nblk > 4) return live == 3 ? run(ic<3>(), ic<6 * PB>()) : run(ic<2>(), ic<6 * PB>());
     }
     if constexpr (S::NB >= 2) {
-        if (nblk > 2) return live == 2 ? run(ic<2>(), ic<4 / RB>()) : run(ic<1>(), ic<4 / RB>());
+        if (nblk > 2) return live == 2 ? run(ic<2>(), ic<4 * PB>()) : run(ic<1>(), ic<4 * PB>());
     }
-    return live == 1 ? run(ic<1>(), ic<2 / RB>()) : run(ic<0>(), ic<2 / RB>());
+    return live == 1 ? run(ic<1>(), ic<2 * PB>()) : run(ic<0>(), ic<2 * PB>());
 }
 
-template <class S, bool EXPERT>
-__device__ __forceinline__ void tile_go(const I8Tile<S>& g, int nrows, uint8_t* const (&WS)[4], uint8_t* const (&XS)[4],
-                                        I8Sums<S>& acc) {
-    ring<S::NST>(WS, [&](auto& W) { ring<S::NST>(XS, [&](auto& X) { tile_run<S, EXPERT>(g, nrows, W, X, acc); }); });
+// A wavefront's region of LDS for its results (tile_dev.h).
+template <class S>
+__device__ __forceinline__ uint8_t* result_region(uint8_t* lds, int wave) {
+    static_assert(S::W * OUT_REGION <= S::LDS, "room for every wavefront");
+    return lds + wave * OUT_REGION;
 }
 
 // Sums as fp32 with the activation row's scale sx and the lane's weight rows' sw.
@@ -236,8 +309,8 @@ __device__ __forceinline__ void put_bf16(uint8_t* R, int lane, int i, int j, con
 
 template <class S>
 __global__ __launch_bounds__(64 * S::W, S::WAVES) void i8_gateup_tile_kernel(I8Ffn a) {
-    constexpr int NB = S::NB, BM = S::BM, HC = S::WR / 2, TW = S::W, TWC = S::WQ;  // h columns per wavefront
-    F8_TILE_LDS(S);
+    constexpr int NB = S::NB, BM = S::BM, HC = S::WR / 2;  // h columns per wavefront
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
     int tile, ntile;
     if (!work_item<4>(tile_count(a.f), tile, ntile)) return;
     TileRows tr;
@@ -251,34 +324,31 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void i8_gateup_tile_kernel(I8F
     const size_t e = shared ? 0 : tr.g;
     I8Tile<S> g;
     g.K = d;
-    // stage rows 2 HC m .. + HC - 1: gate rows n0 + HC m .., the HC rows after
-    // them: the same up rows (a wavefront's copies are 64 rows apart: all of
-    // them gate, or all up)
-    static_assert(64 % (2 * HC) == 0 && TW == 8, "gate and up copies");
-    g.wbase = static_cast<const uint8_t*>((8 * wave & HC) ? U.q : G.q) + (e * F + n0) * d;
-#pragma unroll
-    for (int q = 0; q < TWC; ++q) {
-        const int r8 = 8 * (q * TW + wave), n = HC * (r8 / (2 * HC)) + r8 % HC + (lane >> 3);
-        g.ch = copy_chunk(r8 + (lane >> 3), lane);
-        g.woff[q] = (uint32_t)(min(n, F - 1 - n0) * d + g.ch);
-    }
+    static_assert(64 % (2 * HC) == 0 && HC == 32 && S::CW == 4, "gate and up copies");
     auto token = [&](int r) {  // rows past the tile repeat its first; their results are not stored
         r = r < tr.nrows ? r : 0;
         if (shared) return tr.rbeg - a.f.T * a.f.k + r;
         const int f = a.f.perm_rows[tr.rbeg + r];
         return f >= 0 && f < a.f.T * a.f.k ? f / a.f.k : 0;
     };
-    g.xbase = reinterpret_cast<const uint8_t*>(a.xq);  // (T * d is below 2^32)
+    // stage rows 2 HC m .. + HC - 1: gate rows n0 + HC m .., the HC rows after
+    // them: the same up rows (a wavefront copies gate, or up)
+    const bool cw = copies_weights<S>();
+    g.base = !cw ? reinterpret_cast<const uint8_t*>(a.xq)  // (T * d is below 2^32)
+                 : static_cast<const uint8_t*>(wave & 2 ? U.q : G.q) + (e * F + n0) * d;
 #pragma unroll
-    for (int q = 0; q < S::XQ; ++q) g.xoff[q] = (uint32_t)token(copy_row(q * TW + wave, lane)) * d + g.ch;
+    for (int q = 0; q < S::Q; ++q) {
+        const int r = stage_row<S>(q, lane), n = HC * (r / (2 * HC)) + r % HC;
+        g.ch = copy_chunk(r, lane);
+        g.off[q] = (cw ? (uint32_t)(min(n, F - 1 - n0) * d) : (uint32_t)token(r) * d) + g.ch;
+    }
     g.once = one_tile<BM>(a.f, tr);
     I8Sums<S> acc;
-    tile_go<S, true>(g, tr.nrows, WS, XS, acc);
+    tile_go<S, true>(g, tr.nrows, lds, acc);
     static_assert(S::NJ == 2 && HC == 32, "a block of gate, a block of up");
-    __syncthreads();  // every wavefront has read its last stage
     const int c0 = n0 + HC * wn;
     if (c0 >= F) return;  // (F is a multiple of 64)
-    uint8_t* R = out_region<S>(WS, wave);
+    uint8_t* R = result_region<S>(lds, wave);
     f8_f4 sg[2], su[2];  // (the wavefront's first two rows of 16 are gate, the others the same rows of up)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -309,8 +379,8 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void i8_gateup_tile_kernel(I8F
 
 template <class S>
 __global__ __launch_bounds__(64 * S::W, S::WAVES) void i8_down_tile_kernel(I8Ffn a) {
-    constexpr int NB = S::NB, BM = S::BM, TN = S::TN, TW = S::W, TWC = S::WQ;
-    F8_TILE_LDS(S);
+    constexpr int NB = S::NB, BM = S::BM, TN = S::TN;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
     int tile, ntile;
     if (!work_item<4>(tile_count(a.f), tile, ntile)) return;
     TileRows tr;
@@ -322,25 +392,20 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void i8_down_tile_kernel(I8Ffn
     const size_t e = shared ? 0 : tr.g;
     I8Tile<S> g;
     g.K = F;
-#pragma unroll
-    for (int q = 0; q < TWC; ++q) {
-        const int sr = copy_row(q * TW + wave, lane);
-        g.ch = copy_chunk(sr, lane);
-        g.woff[q] = (uint32_t)(min(sr, d - 1 - n0) * F + g.ch);
-    }
     g.once = one_tile<BM>(a.f, tr);
-    g.wbase = static_cast<const uint8_t*>(D.q) + (e * d + n0) * F;
-    g.xbase = reinterpret_cast<const uint8_t*>(a.hq) + (size_t)tr.rbeg * a.f.ldh;
+    const bool cw = copies_weights<S>();
+    g.base = cw ? static_cast<const uint8_t*>(D.q) + (e * d + n0) * F
+                : reinterpret_cast<const uint8_t*>(a.hq) + (size_t)tr.rbeg * a.f.ldh;
 #pragma unroll
-    for (int q = 0; q < S::XQ; ++q) {
-        const int sr = copy_row(q * TW + wave, lane);
-        g.xoff[q] = (uint32_t)((sr < tr.nrows ? sr : 0) * a.f.ldh + g.ch);
+    for (int q = 0; q < S::Q; ++q) {
+        const int r = stage_row<S>(q, lane);
+        g.ch = copy_chunk(r, lane);
+        g.off[q] = (uint32_t)((cw ? min(r, d - 1 - n0) * F : (r < tr.nrows ? r : 0) * a.f.ldh) + g.ch);
     }
     I8Sums<S> acc;
-    tile_go<S, true>(g, tr.nrows, WS, XS, acc);
+    tile_go<S, true>(g, tr.nrows, lds, acc);
     float* out = shared ? a.f.shared_out : a.f.slot_out;
-    __syncthreads();  // every wavefront has read its last stage
-    uint8_t* R = out_region<S>(WS, wave);
+    uint8_t* R = result_region<S>(lds, wave);
     int ln = lane;  // (opaque: nothing formed from it is kept over the loop)
     __asm__ volatile("" : "+v"(ln));
     const int c0 = n0 + S::WR * wn;
@@ -388,8 +453,8 @@ __global__ __launch_bounds__(64 * S::W, S::WAVES) void i8_down_tile_kernel(I8Ffn
 
 template <class S, int OF>
 __global__ __launch_bounds__(64 * S::W) void i8_dense_tile_kernel(ChannelArgs a) {
-    constexpr int NB = S::NB, BM = S::BM, TN = S::TN, TW = S::W, TWC = S::WQ;
-    F8_TILE_LDS(S);
+    constexpr int NB = S::NB, BM = S::BM, TN = S::TN;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
     // consecutive workgroups go to the 8 XCDs in turn: give each a contiguous
     // range of the tiles, walked in groups of 4 weight tiles (gemm_dev.h)
     const int gx = gridDim.x, gy = gridDim.y, L = blockIdx.x + blockIdx.y * gx, N = gx * gy;
@@ -400,20 +465,17 @@ __global__ __launch_bounds__(64 * S::W) void i8_dense_tile_kernel(ChannelArgs a)
     const int lane = lane_id(), wave = wave_index(), mh = wave / S::GN, wn = wave % S::GN;
     I8Tile<S> g;
     g.K = a.k;
+    const bool cw = copies_weights<S>();
+    g.base = cw ? reinterpret_cast<const uint8_t*>(a.wq) + (size_t)n0 * a.k : static_cast<const uint8_t*>(a.x) + (size_t)m0 * a.k;
 #pragma unroll
-    for (int q = 0; q < TWC; ++q) {
-        const int sr = copy_row(q * TW + wave, lane);
-        g.ch = copy_chunk(sr, lane);
-        g.woff[q] = (uint32_t)(min(sr, a.n - 1 - n0) * a.k + g.ch);
+    for (int q = 0; q < S::Q; ++q) {
+        const int r = stage_row<S>(q, lane);
+        g.ch = copy_chunk(r, lane);
+        g.off[q] = (uint32_t)(min(r, cw ? a.n - 1 - n0 : nrows - 1) * a.k + g.ch);
     }
-    g.wbase = reinterpret_cast<const uint8_t*>(a.wq) + (size_t)n0 * a.k;
-    g.xbase = static_cast<const uint8_t*>(a.x) + (size_t)m0 * a.k;
-#pragma unroll
-    for (int q = 0; q < S::XQ; ++q) g.xoff[q] = (uint32_t)(min(copy_row(q * TW + wave, lane), nrows - 1) * a.k + g.ch);
     I8Sums<S> acc;
-    tile_go<S, false>(g, nrows, WS, XS, acc);
-    __syncthreads();  // every wavefront has read its last stage
-    uint8_t* R = out_region<S>(WS, wave);
+    tile_go<S, false>(g, nrows, lds, acc);
+    uint8_t* R = result_region<S>(lds, wave);
     const int c0 = n0 + S::WR * wn;
     if (c0 >= a.n) return;
     f8_f4 sw[2 * S::NJ];
@@ -470,15 +532,17 @@ hipError_t launch_i8_gateup(const I8Ffn& a, hipStream_t st, const KTime& kt) {
     const int fmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F;
     const dim3 grid(a.f.max_tiles, (fmax + Rows64::TN / 2 - 1) / (Rows64::TN / 2));
     if (a.f.bm == 64) launch_kernel(i8_gateup_tile_kernel<Rows64>, grid, 64 * Rows64::W, st, kt, a);
-    else launch_kernel(i8_gateup_tile_kernel<Rows128>, grid, 64 * Rows128::W, st, kt, a);
+    else if (a.f.bm == 128) launch_kernel(i8_gateup_tile_kernel<Rows128>, grid, 64 * Rows128::W, st, kt, a);
+    else launch_kernel(i8_gateup_tile_kernel<Rows256>, grid, 64 * Rows256::W, st, kt, a);
     return hipGetLastError();
 }
 
 hipError_t launch_i8_down(const I8Ffn& a, hipStream_t st, const KTime& kt) {
-    static_assert(Rows64::TN == Rows128::TN, "one grid");
+    static_assert(Rows64::TN == Rows128::TN && Rows64::TN == Rows256::TN, "one grid");
     const dim3 grid(a.f.max_tiles, (a.f.d + Rows64::TN - 1) / Rows64::TN);
     if (a.f.bm == 64) launch_kernel(i8_down_tile_kernel<Rows64>, grid, 64 * Rows64::W, st, kt, a);
-    else launch_kernel(i8_down_tile_kernel<Rows128>, grid, 64 * Rows128::W, st, kt, a);
+    else if (a.f.bm == 128) launch_kernel(i8_down_tile_kernel<Rows128>, grid, 64 * Rows128::W, st, kt, a);
+    else launch_kernel(i8_down_tile_kernel<Rows256>, grid, 64 * Rows256::W, st, kt, a);
     return hipGetLastError();
 }
 
