@@ -286,15 +286,29 @@ TokenQuantArgs i8_quant_args(const moe_config* c, const LayerLayout& L, void* ws
     return TokenQuantArgs{x, MOE_DT_BF16, T, T, (int)d, (int)d, d, d, at<int8_t>(ws, L.xq), at<float>(ws, L.xe)};
 }
 
+I8Ffn i8_ffn(const FfnArgs& f, const LayerLayout& L, void* ws) {
+    return I8Ffn{f, at<int8_t>(ws, L.xq), at<float>(ws, L.xe), at<float>(ws, L.h), at<int8_t>(ws, L.hq), at<float>(ws, L.he)};
+}
+hipError_t quantize_h(const I8Ffn& a, hipStream_t st, const KTime& kt) {
+    const int64_t n = (int64_t)a.f.T * a.f.k;
+    const TokenQuantArgs q{a.h, MOE_DT_F32, n + (a.f.n_shared ? a.f.T : 0), n, a.f.F, a.f.Fs, a.f.ldh, a.f.ldh, a.hq, a.hs};
+    return launch_quantize_tokens(q, st, kt);
+}
 hipError_t run_i8_experts(const FfnArgs& f, const LayerLayout& L, void* ws, hipStream_t st, const KTime& kg = KTime(),
                           const KTime& kd = KTime()) {
-    const I8Ffn a{f, at<int8_t>(ws, L.xq), at<float>(ws, L.xe), at<float>(ws, L.h), at<int8_t>(ws, L.hq), at<float>(ws, L.he)};
+    const I8Ffn a = i8_ffn(f, L, ws);
     hipError_t e = launch_i8_gateup(a, st, kg.first());
-    if (e != hipSuccess) return e;
-    const int64_t n = (int64_t)f.T * f.k;
-    const TokenQuantArgs q{a.h, MOE_DT_F32, n + (f.n_shared ? f.T : 0), n, f.F, f.Fs, f.ldh, f.ldh, a.hq, a.hs};
-    if ((e = launch_quantize_tokens(q, st, kg.last())) != hipSuccess) return e;
-    return launch_i8_down(a, st, kd);
+    if (e == hipSuccess) e = quantize_h(a, st, kg.last());
+    return e == hipSuccess ? launch_i8_down(a, st, kd) : e;
+}
+// The experts of few tokens and their combine.
+hipError_t run_i8_few(const FfnArgs& f, const LayerLayout& L, void* ws, void* y, int ydt, hipStream_t st, const KTime& kg,
+                      const KTime& kd) {
+    const I8Ffn a = i8_ffn(f, L, ws);
+    const bool in_down = i8_stream_quantises_h(a);
+    hipError_t e = launch_i8_gateup_stream(a, st, in_down ? kg : kg.first());
+    if (e == hipSuccess && !in_down) e = quantize_h(a, st, kg.last());
+    return e == hipSuccess ? launch_i8_down_stream(a, y, ydt, st, kd) : e;
 }
 
 // The quantisation of x for layers that need it.
@@ -809,12 +823,13 @@ int enqueue_layer(const moe_config* cfg, const GroupArgs& g, const void* x, cons
     }
     const SelectArgs sel = select_args(cfg, logits, w->bias, idx, wts);
     const PermArgs pa = perm_args(cfg, L, ws, idx, off, perm, inv);
-    const bool f8 = cfg->w_dtype == MOE_DT_F8B128;
+    const bool i8 = cfg->w_dtype == MOE_DT_I8CH;
     hipError_t e;
-    if (f8 && cfg->n_tokens <= F8_ROUTE_MAX_T) {
+    if (is_8bit(cfg) && cfg->n_tokens <= F8_ROUTE_MAX_T) {
         e = launch_f8_router(r, st, kt[0]);
         if (e == hipSuccess)
-            e = launch_f8_route(sel, g, is_grouped(cfg, g), pa, f8_quant_args(cfg, L, ws, x), st, kt[1]);
+            e = i8 ? launch_i8_route(sel, g, is_grouped(cfg, g), pa, i8_quant_args(cfg, L, ws, x), st, kt[1])
+                   : launch_f8_route(sel, g, is_grouped(cfg, g), pa, f8_quant_args(cfg, L, ws, x), st, kt[1]);
     } else {
         e = launch_router_logits(r, st, kt[0]);
         if (e == hipSuccess) e = run_select(cfg, g, sel, st, kt[1]);
@@ -823,6 +838,7 @@ int enqueue_layer(const moe_config* cfg, const GroupArgs& g, const void* x, cons
     }
     if (e != hipSuccess) return MOE_ERR_DEVICE;
     FfnArgs f = ffn_args(cfg, L, ws, x, w, off, perm, wts);
+    if (i8 && i8_stream_takes(f.T, f.F, f.Fs)) return device_status(run_i8_few(f, L, ws, y, ydt, st, kt[3], kt[4]));
     e = run_expert_kernels(f, L, ws, st, kt[3], kt[4]);
     if (e == hipSuccess) {
         CombineArgs c{f.slot_out, f.shared_out, y, cfg->n_tokens, cfg->top_k, cfg->d_model, ydt};

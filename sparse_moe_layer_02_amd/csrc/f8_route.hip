@@ -1,4 +1,4 @@
-// f8_route.hip - the routing of few tokens through an e4m3 layer, in two
+// f8_route.hip - the routing of few tokens through an e4m3 or int8 layer, in two
 // launches.
 //
 // 1. Router logits, a workgroup per expert: 1024 threads of four columns each,
@@ -17,6 +17,7 @@
 #include "group_dev.h"
 #include "kernels.h"
 #include "permute_dev.h"
+#include "i8_quantize_dev.h"
 #include "quantize_dev.h"
 #include "route_dev.h"
 
@@ -68,12 +69,24 @@ __global__ __launch_bounds__(FR_WAVES * WAVE) void f8_router_kernel(const uint16
 
 static_assert(FR_WAVES * WAVE == 1024 && F8_ROUTE_MAX_T * 32 < 1024, "emit_lists_few: threads, assignments");
 
-template <int KPL>
-__global__ __launch_bounds__(FR_WAVES * WAVE) void f8_route_kernel(SelectArgs s, GroupArgs g, bool grouped, PermArgs p,
-                                                                   QuantArgs q) {
+// The rows of x in the workgroups behind the first: e4m3 codes by blocks of 128
+// columns, int8 codes by rows; how many workgroups.
+__device__ __forceinline__ void quantize_rest(const QuantArgs& q) {
+    quantize_blocks<MOE_DT_BF16>(q, (int64_t)(blockIdx.x - 1) * (FR_WAVES * 4) + threadIdx.x / 16,
+                                 (int64_t)(gridDim.x - 1) * (FR_WAVES * 4));
+}
+__device__ __forceinline__ void quantize_rest(const TokenQuantArgs& q) {
+    quantize_token_rows<MOE_DT_BF16, FR_WAVES * WAVE>(q, blockIdx.x - 1, gridDim.x - 1);
+}
+static int64_t rest_blocks(const QuantArgs& q) {
+    return ((int64_t)q.rows * f8_scale_ld(q.cols) + FR_WAVES * 4 - 1) / (FR_WAVES * 4);
+}
+static int64_t rest_blocks(const TokenQuantArgs& q) { return q.rows; }
+
+template <int KPL, class Q>
+__global__ __launch_bounds__(FR_WAVES * WAVE) void f8_route_kernel(SelectArgs s, GroupArgs g, bool grouped, PermArgs p, Q q) {
     if (blockIdx.x > 0) {
-        quantize_blocks<MOE_DT_BF16>(q, (int64_t)(blockIdx.x - 1) * (FR_WAVES * 4) + threadIdx.x / 16,
-                                     (int64_t)(gridDim.x - 1) * (FR_WAVES * 4));
+        quantize_rest(q);
         return;
     }
     __shared__ uint32_t s_key[FR_WAVES][KPL * WAVE];
@@ -109,13 +122,22 @@ hipError_t launch_f8_router(const RouteArgs& a, hipStream_t st, const KTime& kt)
     return hipGetLastError();
 }
 
+template <class Q>
+static hipError_t route_launch(const SelectArgs& s, const GroupArgs& g, bool grouped, const PermArgs& p, const Q& q,
+                               hipStream_t st, const KTime& kt) {
+    const dim3 grid(1 + (unsigned)rest_blocks(q));
+    if (s.E <= 256) launch_kernel(f8_route_kernel<4, Q>, grid, FR_WAVES * WAVE, st, kt, s, g, grouped, p, q);
+    else launch_kernel(f8_route_kernel<16, Q>, grid, FR_WAVES * WAVE, st, kt, s, g, grouped, p, q);
+    return hipGetLastError();
+}
+
 hipError_t launch_f8_route(const SelectArgs& s, const GroupArgs& g, bool grouped, const PermArgs& p, const QuantArgs& q,
                            hipStream_t st, const KTime& kt) {
-    const int64_t blocks = ((int64_t)q.rows * f8_scale_ld(q.cols) + FR_WAVES * 4 - 1) / (FR_WAVES * 4);
-    const dim3 grid(1 + (unsigned)blocks);
-    if (s.E <= 256) launch_kernel(f8_route_kernel<4>, grid, FR_WAVES * WAVE, st, kt, s, g, grouped, p, q);
-    else launch_kernel(f8_route_kernel<16>, grid, FR_WAVES * WAVE, st, kt, s, g, grouped, p, q);
-    return hipGetLastError();
+    return route_launch(s, g, grouped, p, q, st, kt);
+}
+hipError_t launch_i8_route(const SelectArgs& s, const GroupArgs& g, bool grouped, const PermArgs& p, const TokenQuantArgs& q,
+                           hipStream_t st, const KTime& kt) {
+    return route_launch(s, g, grouped, p, q, st, kt);
 }
 
 }  // namespace moe

@@ -40,9 +40,9 @@ __device__ __forceinline__ i32x4_t dot16(i32x4_t w, i32x4_t x, i32x4_t c) {
 
 // The products of steps [s0, s1) of NR blocks of 16 weight rows and NT of 16
 // activation rows.  wp: this lane's weight rows; x(t, c): columns c .. c + 15 of its
-// activation row, from memory, or from LDS (LX) once between() has put them
-// there.  U steps are in flight while the U before them are multiplied, the first
-// before between().
+// activation row, from memory, or (LX) from LDS.  The first weights are sent for
+// before between(), behind which x may be called.  U steps are in flight while the
+// U before them are multiplied.
 template <int NR, int NT, int U, bool LX>
 struct Frag {
     i32x4_t w[U][NR], x[LX ? 1 : U][NT];
@@ -52,18 +52,25 @@ __device__ __forceinline__ void stream(const int8_t* const (&wp)[NR], X x, int s
                                        i32x4_t (&acc)[NR][NT], Between between) {
     typedef Frag<NR, NT, U, LX> F;
     const int lo = 16 * (lane_id() / 16);
-    auto load = [&](F& f, int s) {
+    auto column = [&](int s) { return min(SK * min(s, s1 - 1) + lo, K - 16); };
+    auto load_w = [&](F& f, int s) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = min(SK * min(s + u, s1 - 1) + lo, K - 16);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int r = 0; r < NR; ++r) f.w[u][r] = ld_codes(wp[r] + c);
-            if constexpr (!LX) {
+            for (int r = 0; r < NR; ++r) f.w[u][r] = ld_codes(wp[r] + column(s + u));
+    };
+    auto load_x = [&](F& f, int s) {
+        if constexpr (!LX) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) f.x[u][t] = x(t, c);
-            }
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) f.x[u][t] = x(t, column(s + u));
         }
         pin();
+    };
+    auto load = [&](F& f, int s) {
+        load_w(f, s);
+        load_x(f, s);
     };
     auto compute = [&](const F& f, int s) {
 #pragma unroll
@@ -82,8 +89,10 @@ __device__ __forceinline__ void stream(const int8_t* const (&wp)[NR], X x, int s
         }
     };
     F a, b;
-    if (s0 < s1) load(a, s0);
+    if (s0 < s1) load_w(a, s0);
+    pin();
     between();
+    if (s0 < s1) load_x(a, s0);
     for (int s = s0; s < s1; s += 2 * U) {
         if (s + U < s1) load(b, s + U);
         compute(a, s);
@@ -212,18 +221,224 @@ hipError_t dense_launch(const ChannelArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Experts of few tokens.  A slot is an expert with its rows, or the shared expert
+// with the tokens: a tile of the list, of which each holds up to 16 rows.
+// ---------------------------------------------------------------------------
+
+// Gate/up: 16 columns of h of one slot per workgroup, K split over its wavefronts.
+__global__ __launch_bounds__(WAVE * SW) void i8_gateup_stream_kernel(I8Ffn a) {
+    __shared__ i32x4_t part[SW][2][WAVE];
+    const int slot = blockIdx.y, lane = lane_id(), wave = wave_index(), tid = threadIdx.x;
+    const int2 tile = a.f.tiles[slot];  // (the list has room for every slot of the grid)
+    if (slot >= tile_count(a.f)) return;
+    const bool shared = tile.x == a.f.E;
+    const int F = shared ? a.f.Fs : a.f.F, d = a.f.d, c0 = blockIdx.x * 16;
+    if (c0 >= F) return;
+    const MatRef& G = shared ? a.f.s_gate : a.f.gate;
+    const MatRef& U = shared ? a.f.s_up : a.f.up;
+    const size_t row0 = (size_t)(shared ? 0 : tile.x) * F + c0;
+    const int8_t* wp[2] = {static_cast<const int8_t*>(G.q) + (row0 + lane % 16) * d,
+                           static_cast<const int8_t*>(U.q) + (row0 + lane % 16) * d};
+    i32x4_t acc[2][1] = {{i32x4_t{0, 0, 0, 0}}, {i32x4_t{0, 0, 0, 0}}};
+    const int steps = (d + SK - 1) / SK, per = (steps + SW * UU - 1) / (SW * UU) * UU, s0 = wave * per;
+    TileRows tr;
+    int token = 0;
+    const int8_t* xp = a.xq;
+    stream<2, 1, UU, false>(
+        wp, [&](int, int c) { return ld_codes(xp + c); }, s0, min(steps, s0 + per), d, acc,
+        [&] {
+            tile_rows<16>(a.f, slot, tr);
+            const int r = min(lane % 16, tr.nrows - 1);
+            token = shared ? tr.rbeg - a.f.T * a.f.k + r : a.f.perm_rows[tr.rbeg + r] / a.f.k;
+            xp = a.xq + (size_t)token * d;
+        });
+    part[wave][0][lane] = acc[0][0];
+    part[wave][1][lane] = acc[1][0];
+    __syncthreads();
+    if (tid >= 256) return;
+    // value tid % 4 of lane tid / 4 of the sums
+    const int* p = reinterpret_cast<const int*>(&part[0][0][0]) + tid;
+    int g = 0, u = 0;
+#pragma unroll
+    for (int w = 0; w < SW; ++w) {
+        g += p[w * 512];
+        u += p[w * 512 + 256];
+    }
+    const int r = tid / 4 % 16, c = 4 * (tid / 64) + tid % 4, t = __shfl(token, r);
+    if (r >= tr.nrows) return;
+    const float sx = a.xs[t];
+    const float ga = (float)g * sx * reinterpret_cast<const float*>(G.scale)[row0 + c];
+    const float up = (float)u * sx * reinterpret_cast<const float*>(U.scale)[row0 + c];
+    a.h[(size_t)(tr.rbeg + r) * a.f.ldh + c0 + c] = silu_f32(ga) * up;
+}
+
+// Down and combine: 16 columns of y per workgroup, of all tokens.  Its items are
+// a slot and 512 columns of K each, dealt to the wavefronts in turn; an item's
+// weights are sent for while the one before it is multiplied.  The int32 sums of a
+// batch of slots meet in LDS, become rows there (with the routing weights), and at
+// the end the rows of a token are added in the order the combine has.  LX: the rows
+// of h are quantised here first, under the first weights.
+constexpr int DI = 8;  // steps of an item
+struct DownLds {
+    int cap, rows, slots, codes;  // items of a batch; rows of h; slots; bytes of codes (0: they are in memory)
+    __host__ __device__ size_t parts() const { return (size_t)cap * 1024; }
+    __host__ __device__ size_t bytes() const { return parts() + (size_t)rows * 64 + (size_t)slots * 16 + (codes ? codes + rows * 8 : 0); }
+};
+template <int OF, bool LX>
+__global__ __launch_bounds__(WAVE * SW) void i8_down_stream_kernel(I8Ffn a, void* y, DownLds m) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t down_lds[];
+    i32x4_t* part = reinterpret_cast<i32x4_t*>(down_lds);
+    float* rows = reinterpret_cast<float*>(down_lds + m.parts());
+    int4* slots = reinterpret_cast<int4*>(rows + m.rows * 16);
+    int8_t* codes = reinterpret_cast<int8_t*>(slots + m.slots);
+    uint32_t* top = reinterpret_cast<uint32_t*>(codes + m.codes);
+    float* scales = reinterpret_cast<float*>(top + m.rows);
+    const int lane = lane_id(), wave = wave_index(), tid = threadIdx.x, lo = 16 * (lane / 16);
+    const int c0 = blockIdx.x * 16, d = a.f.d, Tk = a.f.T * a.f.k;
+    const int n = min(tile_count(a.f), m.slots);
+    for (int i = tid; i < m.slots; i += WAVE * SW) {
+        const int2 t = a.f.tiles[i];
+        TileRows tr = {0, 0, 0};
+        if (i < n) tile_rows<16>(a.f, i, tr);
+        slots[i] = make_int4(t.x, tr.rbeg, tr.nrows, 0);
+    }
+    __syncthreads();
+    const int kmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F;
+    const int kx = (kmax + SK * DI - 1) / (SK * DI), batch = m.cap / kx;  // items of a slot, slots of a batch
+    struct Item {
+        i32x4_t w[DI], x[LX ? 1 : DI];
+        const int8_t* xp;
+        int K, s0;
+    };
+    auto load = [&](Item& f, int item) {
+        const int4 s = slots[item / kx];
+        const bool shared = s.x == a.f.E;
+        const MatRef& D = shared ? a.f.s_down : a.f.down;
+        f.K = shared ? a.f.Fs : a.f.F;
+        f.s0 = item % kx * DI;
+        const int8_t* wp = static_cast<const int8_t*>(D.q) + ((size_t)(shared ? 0 : s.x) * d + c0 + lane % 16) * f.K;
+        const int row = s.y + min(lane % 16, s.z - 1);
+        f.xp = LX ? codes + row * a.f.ldh : a.hq + (size_t)row * a.f.ldh;
+#pragma unroll
+        for (int u = 0; u < DI; ++u) {
+            const int c = min(SK * (f.s0 + u) + lo, f.K - 16);  // (columns past the end: re-read, not used)
+            f.w[u] = ld_codes(wp + c);
+            if constexpr (!LX) f.x[u] = ld_codes(f.xp + c);
+        }
+        pin();
+    };
+    Item cur, next;
+    const int items = n * kx;
+    if (wave < items) load(cur, wave);
+    if constexpr (LX) {
+        // rows 0 .. T k - 1 have F columns, the shared expert's behind them Fs
+        rows_to_lds<MOE_DT_F32>(a.h, Tk, a.f.F, a.f.ldh, codes, a.f.ldh, top, scales);
+        if (a.f.n_shared)
+            rows_to_lds<MOE_DT_F32>(a.h + (size_t)Tk * a.f.ldh, a.f.T, a.f.Fs, a.f.ldh, codes + Tk * a.f.ldh, a.f.ldh, top + Tk,
+                                    scales + Tk);
+    }
+    int item = wave;
+    for (int b0 = 0; b0 < n; b0 += batch) {
+        const int end = min(n, b0 + batch) * kx;
+        for (; item < end; item += SW) {
+            if (item + SW < items) load(next, item + SW);
+            i32x4_t acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int u = 0; u < DI; ++u) {
+                const int c = SK * (cur.s0 + u) + lo;
+                i32x4_t x;
+                if constexpr (LX) x = *reinterpret_cast<const i32x4_t*>(cur.xp + min(c, cur.K - 16));
+                else x = cur.x[u];
+                if (c >= cur.K) x = i32x4_t{0, 0, 0, 0};
+                acc = dot16(cur.w[u], x, acc);
+            }
+            part[(item - b0 * kx) * WAVE + lane] = acc;
+            cur = next;
+        }
+        __syncthreads();
+        for (int o = tid; o < (end - b0 * kx) / kx * 256; o += WAVE * SW) {
+            const int4 s = slots[b0 + o / 256];
+            const int r = o / 4 % 16, c = 4 * (o / 64 % 4) + o % 4;
+            if (r >= s.z) continue;
+            const int* p = reinterpret_cast<const int*>(part) + o / 256 * kx * 256 + o % 256;
+            int sum = 0;
+            for (int q = 0; q < kx; ++q) sum += p[q * 256];
+            const bool shared = s.x == a.f.E;
+            const MatRef& D = shared ? a.f.s_down : a.f.down;
+            const int row = s.y + r, f = shared ? row : a.f.perm_rows[row];
+            const float sw = reinterpret_cast<const float*>(D.scale)[(size_t)(shared ? 0 : s.x) * d + c0 + c];
+            const float v = (float)sum * (LX ? scales[row] : a.hs[row]) * sw;
+            rows[f * 16 + c] = v * (shared ? 1.0f : a.f.topk_w[f]);
+        }
+        __syncthreads();
+    }
+    if (tid < a.f.T * 16) {
+        const int t = tid / 16, c = tid % 16;
+        float v = a.f.n_shared ? rows[(Tk + t) * 16 + c] : 0.0f;
+        for (int j = 0; j < a.f.k; ++j) v += rows[(t * a.f.k + j) * 16 + c];
+        const size_t at = (size_t)t * d + c0 + c;
+        if constexpr (OF == MOE_DT_BF16) static_cast<uint16_t*>(y)[at] = f32_to_bf16(v);
+        else static_cast<float*>(y)[at] = v;
+    }
+}
+
 }  // namespace
 
-// Rows that are quantised by the product itself.
+// Rows that are quantised by the product itself: every workgroup of 16 output
+// columns does it again, so few values and few workgroups (us against a launch of its
+// own first, bf16 rows, cold weights: 4096 x 6144, 1 row 10.3 / 12.8, 4 rows 12.9 / 13.7;
+// 6144 x 2048, 8 rows 11.5 / 12, 12 rows 13.9 / 13.9; 24576 x 6144, 1 row 50 / 48).
 bool channel_matmul_takes(int m, int n, int k) { return m <= 16 && (int64_t)m * k <= I8_FUSE_VALUES && n <= 8192; }
 
+// The smallest tiles that leave no more than one workgroup to a compute unit, whose
+// eight wavefronts share the sum (us, 16 x 16 / 32 x 16 / 32 x 32 / LDS tiles of 64 x
+// 64, n x k: 64 rows of 1024 x 6144, 256 workgroups of the smallest, 8.4 / 11.6 / 13.3 /
+// 16.6; 32 rows of 4096 x 6144 15.5 / 13.7 / 16.8 / 16.7; 64 rows of it 26 / 22 / 16.4 /
+// 18.7; 96 rows 36 / 29 / 27 / 16.9; 512 rows of 512 x 2048 9.9 / 8.0 / 6.0 / 7.3; 48 of 6144 x
+// 2048 14.2 / 12.3 / 10.3 / 8.9).
 hipError_t launch_channel_matmul(const ChannelArgs& a, hipStream_t st) {
     if (a.xdt == MOE_DT_BF16) return dense_launch<1, 1, MOE_DT_BF16>(a, st);
     if (a.xdt == MOE_DT_F32) return dense_launch<1, 1, MOE_DT_F32>(a, st);
-    if (a.m <= 16) return dense_launch<1, 1, MOE_DT_I8CH>(a, st);
-    const bool few = (long)((a.m + 31) / 32) * ((a.n + 31) / 32) <= 256 && a.k >= 1024;
-    if (a.m <= 48 || few) return dense_launch<2, 2, MOE_DT_I8CH>(a, st);
+    auto groups = [&](int nt, int nr) { return (long)((a.m + 16 * nt - 1) / (16 * nt)) * ((a.n + 16 * nr - 1) / (16 * nr)); };
+    if (a.m <= 16 || groups(1, 1) <= 256) return dense_launch<1, 1, MOE_DT_I8CH>(a, st);
+    if (groups(2, 1) <= 256) return dense_launch<2, 1, MOE_DT_I8CH>(a, st);
+    if (groups(2, 2) <= 256) return dense_launch<2, 2, MOE_DT_I8CH>(a, st);
     return launch_channel_matmul_tile(a, st);
+}
+
+// Layers of few tokens whose slots fit the down kernel's batches.
+bool i8_stream_takes(int T, int F, int Fs) { return T <= F8_ROUTE_MAX_T && F <= 8192 && Fs <= 8192; }
+
+hipError_t launch_i8_gateup_stream(const I8Ffn& a, hipStream_t st, const KTime& kt) {
+    const int fmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F;
+    launch_kernel(i8_gateup_stream_kernel, dim3((fmax + 15) / 16, a.f.max_tiles), WAVE * SW, st, kt, a);
+    return hipGetLastError();
+}
+
+// Items of a slot; LDS of a workgroup: up to 64 KB, 32 items of a batch, and the
+// rows of h as codes if they are few (every workgroup makes them all).
+static int down_items(const I8Ffn& a) { return ((a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F) + SK * DI - 1) / (SK * DI); }
+static DownLds down_lds(const I8Ffn& a) {
+    const int kx = down_items(a), rows = a.f.T * a.f.k + (a.f.n_shared ? a.f.T : 0);
+    DownLds m = {kx, rows, a.f.max_tiles, rows * a.f.ldh};  // (up to 16 * 33 rows of 8192 columns)
+    if (m.codes > I8_FUSE_VALUES || rows > WAVE * SW || m.bytes() > 65536) m.codes = 0;
+    while (m.cap + kx <= 32 && m.cap / kx < a.f.max_tiles && m.bytes() + kx * 1024 <= 65536) m.cap += kx;
+    return m;
+}
+bool i8_stream_quantises_h(const I8Ffn& a) { return down_lds(a).codes != 0; }
+
+hipError_t launch_i8_down_stream(const I8Ffn& a, void* y, int ydt, hipStream_t st, const KTime& kt) {
+    const DownLds m = down_lds(a);
+    const bool lx = m.codes != 0;
+    const dim3 grid(a.f.d / 16);
+    auto go = [&](auto kernel) {
+        if (kt.start || kt.stop) hipExtLaunchKernelGGL(kernel, grid, WAVE * SW, m.bytes(), st, kt.start, kt.stop, 0, a, y, m);
+        else kernel<<<grid, WAVE * SW, m.bytes(), st>>>(a, y, m);
+    };
+    if (ydt == MOE_DT_BF16) lx ? go(i8_down_stream_kernel<MOE_DT_BF16, true>) : go(i8_down_stream_kernel<MOE_DT_BF16, false>);
+    else lx ? go(i8_down_stream_kernel<MOE_DT_F32, true>) : go(i8_down_stream_kernel<MOE_DT_F32, false>);
+    return hipGetLastError();
 }
 
 }  // namespace moe

@@ -51,8 +51,10 @@ struct Rings : Shape<NB_, NJ_, GM_, GN_, 2> {
 typedef Rings<1, 2, 2, 4, 2, 2> Rows64;
 typedef Rings<2, 2, 2, 4, 3, 4> Rows128;
 typedef Rings<4, 2, 2, 4, 2, 3> Rows256;
-// Tiles of the dense product.
+// Tiles of the dense product: the largest; 128 x 128 with eight wavefronts and four
+// stages, for a compute unit of its own, and with four and two, two to a unit; 64 x 64.
 typedef Rings<4, 2, 2, 4, 2, 2> Square256;
+typedef Rings<2, 1, 2, 4, 4, 4> Alone128;
 typedef Rings<2, 2, 2, 2, 2, 2> Square128;
 typedef Rings<1, 1, 2, 2, 4, 4> Square64;
 
@@ -546,11 +548,22 @@ hipError_t launch_i8_down(const I8Ffn& a, hipStream_t st, const KTime& kt) {
     return hipGetLastError();
 }
 
-// The largest tiles that still give most compute units one.
+// By how the tiles fill 256 compute units (us a call with cold weights, bf16
+// results, n x k; tiles of 256 x 256 / 128 x 256 / 128 x 128 alone / two to a unit / 64
+// x 64): from 192 of the largest those (2048 rows of 6144 x 2048: 36 / 43 / 43 / 42 /
+// 56; 128 of them, 2048 of 4096 x 6144: 76 / 59 / 68 / 64 / 95); from 192 of 128 x 256 and
+// not over one for each unit those (the same; 1024 of 6144 x 2048: 34 / 23.5 / 27 / 24 /
+// 33); 160 to 256 of 128 x 128 one to a unit (1024 of 4096 x 6144: 76 / 50 / 36 / 55 / 56;
+// 512 of 6144 x 2048: 33 / 22 / 16 / 22 / 20), more of them two to a unit (2048 of 4096 x
+// 512: 19 / 14 / 15 / 13.6 / 19), fewer as 64 x 64 (256 of 4096 x 6144: 79 / 50 / 35 / 55 /
+// 19; 77 of 6144 x 2048: 21 / 20 / 13 / 20 / 8.5).
 hipError_t launch_channel_matmul_tile(const ChannelArgs& a, hipStream_t st) {
     auto tiles = [&](int bm, int tn) { return (long)((a.m + bm - 1) / bm) * ((a.n + tn - 1) / tn); };
+    const long wide = tiles(128, 256), square = tiles(128, 128);
     if (tiles(256, 256) >= 192) dense_launch<Square256>(a, st);
-    else if (tiles(128, 128) >= 192) dense_launch<Square128>(a, st);
+    else if (wide >= 192 && wide <= 256) dense_launch<Rows128>(a, st);
+    else if (square > 256) dense_launch<Square128>(a, st);
+    else if (square >= 160) dense_launch<Alone128>(a, st);
     else dense_launch<Square64>(a, st);
     return hipGetLastError();
 }

@@ -177,7 +177,8 @@ def test_matmul(dev, m, n, k, xdt):
 # sizes of every larger tile, with ends in rows, columns and K; K below one step; long K
 LARGE = [(1600, 2000, 272), (3500, 3600, 400), (70, 200, 16), (300, 70, 112), (1600, 2000, 48), (3500, 3600, 80),
          (90, 150, 8464), (600, 1000, 8464), (1600, 2000, 8320), (250, 1000, 2064), (8000, 20, 1040), (70, 132, 144),
-         (70, 133, 144), (70, 134, 144), (70, 136, 144), (3500, 3601, 144), (3500, 3602, 144), (1700, 2001, 144)]
+         (70, 133, 144), (70, 134, 144), (70, 136, 144), (3500, 3601, 144), (3500, 3602, 144), (1700, 2001, 144),
+         (2000, 3899, 272), (2000, 3900, 48), (2200, 4100, 400), (2200, 4099, 144), (40, 24000, 400)]
 
 
 @pytest.mark.parametrize("odt", ["bf16", "f32"])
@@ -198,6 +199,23 @@ def test_matmul_large(dev, m, n, k, odt):
     rows = np.unique(np.concatenate([np.arange(0, m, 29), np.arange(max(0, m - 40), m)]))
     cols = np.unique(np.concatenate([np.arange(0, n, 13), np.arange(max(0, n - 40), n)]))
     check_product(torch, out[:m].cpu()[np.ix_(rows, cols)], q[rows], s[rows], wq[cols], wsc[cols])
+
+
+# one size for each kernel of the dense product; every number of whole steps of K from none on, with and without an end
+@pytest.mark.parametrize("m,n", [(3, 40), (20, 2100), (70, 2100), (300, 2100), (1500, 1700), (2000, 3900), (2200, 4100), (3500, 3600)])
+def test_matmul_every_k(dev, m, n):
+    torch, moe = dev
+    rng = np.random.default_rng(m + n)
+    for k in [16, 112, 128, 144, 256, 272, 384, 400, 512, 528, 640, 656, 768, 784, 896, 1024, 1152, 1168]:
+        wq, wsc = weights_of(rng, n, k, full=True)
+        q = rng.integers(-128, 128, (m, k)).astype(np.int8)
+        s = np.exp(rng.standard_normal(m)).astype(np.float32)
+        say("channel matmul", m, n, k)
+        out = torch.full((m, n), 123.0, device="cuda")
+        moe.moe_channel_matmul(*(torch.from_numpy(a).cuda() for a in (q, s, wq, wsc)), out)
+        torch.cuda.synchronize()
+        rows, cols = (np.unique(np.concatenate([np.arange(0, e, 37), np.arange(max(0, e - 5), e)])) for e in (m, n))
+        check_product(torch, out.cpu()[np.ix_(rows, cols)], q[rows], s[rows], wq[cols], wsc[cols])
 
 
 def test_matmul_largest_sums(dev):
@@ -376,10 +394,14 @@ def layer_ref(L, idx, w, n_shared):
 LAYERS = [dict(T=1, d=128, E=4, k=1, F=128), dict(T=1, d=192, E=16, k=8, F=64, Fs=320),
           dict(T=1, d=4160, E=6, k=2, F=2112, Fs=64), dict(T=2, d=64, E=300, k=32, F=64),
           dict(T=3, d=320, E=12, k=3, F=192, n_shared=0), dict(T=8, d=256, E=8, k=2, F=128),
+          dict(T=1, d=192, E=8, k=4, F=576, n_shared=0), dict(T=2, d=320, E=16, k=8, F=1088, Fs=2112),
+          dict(T=4, d=128, E=6, k=3, F=8192, Fs=64), dict(T=5, d=64, E=4, k=2, F=8256, Fs=128),
+          dict(T=9, d=1088, E=20, k=6, F=576, Fs=1600), dict(T=16, d=128, E=600, k=32, F=320),
+          dict(T=16, d=192, E=3, k=3, F=64, Fs=640), dict(T=12, d=64, E=40, k=32, F=64, n_shared=0),
           dict(T=16, d=320, E=40, k=5, F=192), dict(T=17, d=320, E=40, k=5, F=192, n_shared=0),
           dict(T=20, d=128, E=4, k=4, F=192), dict(T=33, d=192, E=64, k=6, F=128, Fs=64),
           dict(T=70, d=448, E=6, k=2, F=256), dict(T=150, d=256, E=3, k=1, F=320), dict(T=300, d=192, E=5, k=3, F=128),
-          dict(T=700, d=128, E=2, k=2, F=256, Fs=128), dict(T=900, d=320, E=2, k=1, F=8256, Fs=64)]
+          dict(T=700, d=128, E=2, k=2, F=256, Fs=128), dict(T=170, d=640, E=4, k=2, F=384), dict(T=500, d=768, E=4, k=3, F=192), dict(T=900, d=320, E=2, k=1, F=8256, Fs=64)]
 
 
 @pytest.mark.parametrize("spec", LAYERS, ids=lambda s: "T%d_d%d_E%d_k%d_F%d" % (s["T"], s["d"], s["E"], s["k"], s["F"]))
@@ -481,7 +503,7 @@ def test_expert_ffn_partial_routing(dev):
     assert (slot == 5.0).all()
 
 
-@pytest.mark.parametrize("T", [1, 5, 64, 300])
+@pytest.mark.parametrize("T", [1, 5, 16, 17, 64, 300])
 def test_layer_graph(dev, T):
     """Routing, quantisation, experts and sum captured together; two graphs with
     workspaces of their own, replayed in turn on new inputs."""
