@@ -273,30 +273,42 @@ __global__ __launch_bounds__(WAVE * SW) void i8_gateup_stream_kernel(I8Ffn a) {
     a.h[(size_t)(tr.rbeg + r) * a.f.ldh + c0 + c] = silu_f32(ga) * up;
 }
 
-// Down and combine: 16 columns of y per workgroup, of all tokens.  Its items are
-// a slot and 512 columns of K each, dealt to the wavefronts in turn; an item's
-// weights are sent for while the one before it is multiplied.  The int32 sums of a
-// batch of slots meet in LDS, become rows there (with the routing weights), and at
-// the end the rows of a token are added in the order the combine has.  LX: the rows
-// of h are quantised here first, under the first weights.
-constexpr int DI = 8;  // steps of an item
+// Down and combine: 16 columns of y per workgroup, of all tokens.  K goes in
+// chunks of 512 columns, the next one's weights on their way while one is
+// multiplied.  Many slots: each wavefront takes whole slots in turn, and nothing
+// stands between them.  SPLIT (few slots): the chunks are dealt to the wavefronts, a
+// batch of slots at a time, whose int32 sums meet in LDS.  A slot's sums become rows
+// in LDS (with the routing weights), and at the end the rows of a token are added
+// in the order the combine has.  LX: the rows of h are quantised here first, under
+// the first weights.
+constexpr int DI = 8;  // steps of a chunk
 struct DownLds {
-    int cap, rows, slots, codes;  // items of a batch; rows of h; slots; bytes of codes (0: they are in memory)
+    int cap, rows, slots, codes;  // chunks of a batch (0: not SPLIT); rows of h; slots; bytes of codes (0: they are in memory)
     __host__ __device__ size_t parts() const { return (size_t)cap * 1024; }
-    __host__ __device__ size_t bytes() const { return parts() + (size_t)rows * 64 + (size_t)slots * 16 + (codes ? codes + rows * 8 : 0); }
+    __host__ __device__ size_t bytes() const { return parts() + (size_t)rows * 80 + (size_t)slots * 16 + (codes ? codes + rows * 8 : 0); }
 };
-template <int OF, bool LX>
+struct DownRow {  // of h
+    int f;        // its result row
+    float w, sx;  // routing weight; scale (LX: in scales)
+    int pad;
+};
+template <int OF, bool LX, bool SPLIT>
 __global__ __launch_bounds__(WAVE * SW) void i8_down_stream_kernel(I8Ffn a, void* y, DownLds m) {
     extern __shared__ __attribute__((aligned(16))) uint8_t down_lds[];
     i32x4_t* part = reinterpret_cast<i32x4_t*>(down_lds);
     float* rows = reinterpret_cast<float*>(down_lds + m.parts());
-    int4* slots = reinterpret_cast<int4*>(rows + m.rows * 16);
+    DownRow* info = reinterpret_cast<DownRow*>(rows + m.rows * 16);
+    int4* slots = reinterpret_cast<int4*>(info + m.rows);
     int8_t* codes = reinterpret_cast<int8_t*>(slots + m.slots);
     uint32_t* top = reinterpret_cast<uint32_t*>(codes + m.codes);
     float* scales = reinterpret_cast<float*>(top + m.rows);
     const int lane = lane_id(), wave = wave_index(), tid = threadIdx.x, lo = 16 * (lane / 16);
     const int c0 = blockIdx.x * 16, d = a.f.d, Tk = a.f.T * a.f.k;
     const int n = min(tile_count(a.f), m.slots);
+    for (int i = tid; i < m.rows; i += WAVE * SW) {
+        const int f = i < Tk ? a.f.perm_rows[i] : i;  // (every assignment of a selection is listed)
+        info[i] = DownRow{f, i < Tk ? a.f.topk_w[f] : 1.0f, LX ? 0.0f : a.hs[i], 0};
+    }
     for (int i = tid; i < m.slots; i += WAVE * SW) {
         const int2 t = a.f.tiles[i];
         TileRows tr = {0, 0, 0};
@@ -305,19 +317,18 @@ __global__ __launch_bounds__(WAVE * SW) void i8_down_stream_kernel(I8Ffn a, void
     }
     __syncthreads();
     const int kmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F;
-    const int kx = (kmax + SK * DI - 1) / (SK * DI), batch = m.cap / kx;  // items of a slot, slots of a batch
-    struct Item {
+    const int kx = (kmax + SK * DI - 1) / (SK * DI);  // chunks of a slot
+    struct Chunk {
         i32x4_t w[DI], x[LX ? 1 : DI];
         const int8_t* xp;
         int K, s0;
     };
-    auto load = [&](Item& f, int item) {
-        const int4 s = slots[item / kx];
-        const bool shared = s.x == a.f.E;
-        const MatRef& D = shared ? a.f.s_down : a.f.down;
-        f.K = shared ? a.f.Fs : a.f.F;
-        f.s0 = item % kx * DI;
-        const int8_t* wp = static_cast<const int8_t*>(D.q) + ((size_t)(shared ? 0 : s.x) * d + c0 + lane % 16) * f.K;
+    auto weights_of = [&](const int4& s) -> const MatRef& { return s.x == a.f.E ? a.f.s_down : a.f.down; };
+    auto row_of = [&](const int4& s) { return (size_t)(s.x == a.f.E ? 0 : s.x) * d + c0; };  // first of the 16 weight rows
+    auto load = [&](Chunk& f, const int4& s, int chunk) {
+        f.K = s.x == a.f.E ? a.f.Fs : a.f.F;
+        f.s0 = chunk * DI;
+        const int8_t* wp = static_cast<const int8_t*>(weights_of(s).q) + (row_of(s) + lane % 16) * f.K;
         const int row = s.y + min(lane % 16, s.z - 1);
         f.xp = LX ? codes + row * a.f.ldh : a.hq + (size_t)row * a.f.ldh;
 #pragma unroll
@@ -328,48 +339,79 @@ __global__ __launch_bounds__(WAVE * SW) void i8_down_stream_kernel(I8Ffn a, void
         }
         pin();
     };
-    Item cur, next;
-    const int items = n * kx;
-    if (wave < items) load(cur, wave);
-    if constexpr (LX) {
-        // rows 0 .. T k - 1 have F columns, the shared expert's behind them Fs
-        rows_to_lds<MOE_DT_F32>(a.h, Tk, a.f.F, a.f.ldh, codes, a.f.ldh, top, scales);
-        if (a.f.n_shared)
-            rows_to_lds<MOE_DT_F32>(a.h + (size_t)Tk * a.f.ldh, a.f.T, a.f.Fs, a.f.ldh, codes + Tk * a.f.ldh, a.f.ldh, top + Tk,
-                                    scales + Tk);
-    }
-    int item = wave;
-    for (int b0 = 0; b0 < n; b0 += batch) {
-        const int end = min(n, b0 + batch) * kx;
-        for (; item < end; item += SW) {
-            if (item + SW < items) load(next, item + SW);
-            i32x4_t acc = {0, 0, 0, 0};
+    auto multiply = [&](const Chunk& f, i32x4_t acc) {
 #pragma unroll
-            for (int u = 0; u < DI; ++u) {
-                const int c = SK * (cur.s0 + u) + lo;
-                i32x4_t x;
-                if constexpr (LX) x = *reinterpret_cast<const i32x4_t*>(cur.xp + min(c, cur.K - 16));
-                else x = cur.x[u];
-                if (c >= cur.K) x = i32x4_t{0, 0, 0, 0};
-                acc = dot16(cur.w[u], x, acc);
-            }
-            part[(item - b0 * kx) * WAVE + lane] = acc;
-            cur = next;
+        for (int u = 0; u < DI; ++u) {
+            const int c = SK * (f.s0 + u) + lo;
+            i32x4_t x;
+            if constexpr (LX) x = *reinterpret_cast<const i32x4_t*>(f.xp + min(c, f.K - 16));
+            else x = f.x[u];
+            if (c >= f.K) x = i32x4_t{0, 0, 0, 0};
+            acc = dot16(f.w[u], x, acc);
         }
-        __syncthreads();
-        for (int o = tid; o < (end - b0 * kx) / kx * 256; o += WAVE * SW) {
-            const int4 s = slots[b0 + o / 256];
-            const int r = o / 4 % 16, c = 4 * (o / 64 % 4) + o % 4;
-            if (r >= s.z) continue;
-            const int* p = reinterpret_cast<const int*>(part) + o / 256 * kx * 256 + o % 256;
-            int sum = 0;
-            for (int q = 0; q < kx; ++q) sum += p[q * 256];
-            const bool shared = s.x == a.f.E;
-            const MatRef& D = shared ? a.f.s_down : a.f.down;
-            const int row = s.y + r, f = shared ? row : a.f.perm_rows[row];
-            const float sw = reinterpret_cast<const float*>(D.scale)[(size_t)(shared ? 0 : s.x) * d + c0 + c];
-            const float v = (float)sum * (LX ? scales[row] : a.hs[row]) * sw;
-            rows[f * 16 + c] = v * (shared ? 1.0f : a.f.topk_w[f]);
+        return acc;
+    };
+    auto result = [&](int sum, const int4& s, int r, int c, float sw) {  // row r of the slot, column c of the 16
+        const DownRow q = info[s.y + r];
+        const float v = (float)sum * (LX ? scales[s.y + r] : q.sx) * sw;
+        rows[q.f * 16 + c] = v * q.w;
+    };
+    Chunk cur, next;
+    if constexpr (SPLIT) {
+        const int items = n * kx, batch = m.cap / kx;  // chunks of all slots; slots of a batch
+        auto load_item = [&](Chunk& f, int item) { load(f, slots[item / kx], item % kx); };
+        if (wave < items) load_item(cur, wave);
+        if constexpr (LX) {
+            // rows 0 .. T k - 1 have F columns, the shared expert's behind them Fs
+            rows_to_lds<MOE_DT_F32>(a.h, Tk, a.f.F, a.f.ldh, codes, a.f.ldh, top, scales);
+            if (a.f.n_shared)
+                rows_to_lds<MOE_DT_F32>(a.h + (size_t)Tk * a.f.ldh, a.f.T, a.f.Fs, a.f.ldh, codes + Tk * a.f.ldh, a.f.ldh,
+                                        top + Tk, scales + Tk);
+        }
+        int item = wave;
+        for (int b0 = 0; b0 < n; b0 += batch) {
+            const int end = min(n, b0 + batch) * kx;
+            for (; item < end; item += SW) {
+                if (item + SW < items) load_item(next, item + SW);
+                part[(item - b0 * kx) * WAVE + lane] = multiply(cur, i32x4_t{0, 0, 0, 0});
+                cur = next;
+            }
+            __syncthreads();
+            for (int o = tid; o < (end - b0 * kx) / kx * 256; o += WAVE * SW) {
+                const int4 s = slots[b0 + o / 256];
+                const int r = o / 4 % 16, c = 4 * (o / 64 % 4) + o % 4;
+                if (r >= s.z) continue;
+                const int* p = reinterpret_cast<const int*>(part) + o / 256 * kx * 256 + o % 256;
+                int sum = 0;
+                for (int q = 0; q < kx; ++q) sum += p[q * 256];
+                result(sum, s, r, c, reinterpret_cast<const float*>(weights_of(s).scale)[row_of(s) + c]);
+            }
+            __syncthreads();
+        }
+    } else {
+        int slot = wave, chunk = 0;
+        int4 s = slots[min(slot, n - 1)];
+        if (slot < n) load(cur, s, 0);
+        i32x4_t acc = {0, 0, 0, 0};
+        while (slot < n) {
+            const bool done = SK * DI * (chunk + 1) >= cur.K;  // the slot's last chunk
+            const bool more = !done || slot + SW < n;
+            const int4 after = done && more ? slots[slot + SW] : s;
+            if (more) load(next, after, done ? 0 : chunk + 1);
+            acc = multiply(cur, acc);
+            ++chunk;
+            if (done) {
+                const f8_f4 sw = i8_scales4(reinterpret_cast<const float*>(weights_of(s).scale) + row_of(s) + 4 * (lane / 16));
+                if (lane % 16 < s.z) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) result(acc[v], s, lane % 16, 4 * (lane / 16) + v, sw[v]);
+                }
+                acc = i32x4_t{0, 0, 0, 0};
+                slot += SW;
+                chunk = 0;
+                s = after;
+            }
+            cur = next;
         }
         __syncthreads();
     }
@@ -416,13 +458,16 @@ hipError_t launch_i8_gateup_stream(const I8Ffn& a, hipStream_t st, const KTime& 
     return hipGetLastError();
 }
 
-// Items of a slot; LDS of a workgroup: up to 64 KB, 32 items of a batch, and the
-// rows of h as codes if they are few (every workgroup makes them all).
-static int down_items(const I8Ffn& a) { return ((a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F) + SK * DI - 1) / (SK * DI); }
+// Up to this many routed rows the chunks of K are split over the wavefronts.
+constexpr int DOWN_SPLIT_ROWS = 16;
+// LDS of a workgroup: up to 64 KB, 32 chunks of a batch, and the rows of h as codes
+// if they are few (every workgroup makes them all).
 static DownLds down_lds(const I8Ffn& a) {
-    const int kx = down_items(a), rows = a.f.T * a.f.k + (a.f.n_shared ? a.f.T : 0);
-    DownLds m = {kx, rows, a.f.max_tiles, rows * a.f.ldh};  // (up to 16 * 33 rows of 8192 columns)
-    if (m.codes > I8_FUSE_VALUES || rows > WAVE * SW || m.bytes() > 65536) m.codes = 0;
+    const int kmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F, kx = (kmax + SK * DI - 1) / (SK * DI);
+    const int rows = a.f.T * a.f.k + (a.f.n_shared ? a.f.T : 0);
+    if (a.f.T * a.f.k > DOWN_SPLIT_ROWS) return DownLds{0, rows, a.f.max_tiles, 0};  // (up to 528 rows, 522 slots)
+    DownLds m = {kx, rows, a.f.max_tiles, rows * a.f.ldh};                            // (up to 32 rows)
+    if (m.codes > I8_FUSE_VALUES) m.codes = 0;
     while (m.cap + kx <= 32 && m.cap / kx < a.f.max_tiles && m.bytes() + kx * 1024 <= 65536) m.cap += kx;
     return m;
 }
@@ -436,8 +481,14 @@ hipError_t launch_i8_down_stream(const I8Ffn& a, void* y, int ydt, hipStream_t s
         if (kt.start || kt.stop) hipExtLaunchKernelGGL(kernel, grid, WAVE * SW, m.bytes(), st, kt.start, kt.stop, 0, a, y, m);
         else kernel<<<grid, WAVE * SW, m.bytes(), st>>>(a, y, m);
     };
-    if (ydt == MOE_DT_BF16) lx ? go(i8_down_stream_kernel<MOE_DT_BF16, true>) : go(i8_down_stream_kernel<MOE_DT_BF16, false>);
-    else lx ? go(i8_down_stream_kernel<MOE_DT_F32, true>) : go(i8_down_stream_kernel<MOE_DT_F32, false>);
+    auto pick = [&](auto of) {
+        constexpr int OF = decltype(of)::value;
+        if (lx) go(i8_down_stream_kernel<OF, true, true>);
+        else if (m.cap) go(i8_down_stream_kernel<OF, false, true>);
+        else go(i8_down_stream_kernel<OF, false, false>);
+    };
+    if (ydt == MOE_DT_BF16) pick(ic<MOE_DT_BF16>());
+    else pick(ic<MOE_DT_F32>());
     return hipGetLastError();
 }
 
