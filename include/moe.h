@@ -134,9 +134,8 @@ typedef struct {
  * n_tokens, but up to 16 tokens stage 1 includes the permutation (stage 2's
  * events stay unrecorded), and the quantisation of x is in stage 1 there and
  * in none beyond.  I8CH layers: the same, stage 3
- * or 4 includes the quantisation of the SwiGLU intermediate, and up to 16 tokens
- * (d_ff and d_ff_shared up to 8192) stage 4 includes the combine (stage 5's
- * events stay unrecorded). */
+ * ends with the quantisation of the SwiGLU intermediate, and up to 16 tokens
+ * stage 4 includes the combine (stage 5's events stay unrecorded). */
 #define MOE_STAGES 6
 #define MOE_STAGE_EVENTS (2 * MOE_STAGES)
 

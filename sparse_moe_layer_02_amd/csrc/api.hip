@@ -305,9 +305,8 @@ hipError_t run_i8_experts(const FfnArgs& f, const LayerLayout& L, void* ws, hipS
 hipError_t run_i8_few(const FfnArgs& f, const LayerLayout& L, void* ws, void* y, int ydt, hipStream_t st, const KTime& kg,
                       const KTime& kd) {
     const I8Ffn a = i8_ffn(f, L, ws);
-    const bool in_down = i8_stream_quantises_h(a);
-    hipError_t e = launch_i8_gateup_stream(a, st, in_down ? kg : kg.first());
-    if (e == hipSuccess && !in_down) e = quantize_h(a, st, kg.last());
+    hipError_t e = launch_i8_gateup_stream(a, st, kg.first());
+    if (e == hipSuccess) e = quantize_h(a, st, kg.last());
     return e == hipSuccess ? launch_i8_down_stream(a, y, ydt, st, kd) : e;
 }
 
@@ -838,7 +837,7 @@ int enqueue_layer(const moe_config* cfg, const GroupArgs& g, const void* x, cons
     }
     if (e != hipSuccess) return MOE_ERR_DEVICE;
     FfnArgs f = ffn_args(cfg, L, ws, x, w, off, perm, wts);
-    if (i8 && i8_stream_takes(f.T, f.F, f.Fs)) return device_status(run_i8_few(f, L, ws, y, ydt, st, kt[3], kt[4]));
+    if (i8 && i8_stream_takes(f.T)) return device_status(run_i8_few(f, L, ws, y, ydt, st, kt[3], kt[4]));
     e = run_expert_kernels(f, L, ws, st, kt[3], kt[4]);
     if (e == hipSuccess) {
         CombineArgs c{f.slot_out, f.shared_out, y, cfg->n_tokens, cfg->top_k, cfg->d_model, ydt};

@@ -276,38 +276,35 @@ __global__ __launch_bounds__(WAVE * SW) void i8_gateup_stream_kernel(I8Ffn a) {
 // Down and combine: 16 columns of y per workgroup, of all tokens.  K goes in
 // chunks of 512 columns, the next one's weights on their way while one is
 // multiplied.  Many slots: each wavefront takes whole slots in turn, and nothing
-// stands between them.  SPLIT (few slots): the chunks are dealt to the wavefronts, a
-// batch of slots at a time, whose int32 sums meet in LDS.  A slot's sums become rows
-// in LDS (with the routing weights), and at the end the rows of a token are added
-// in the order the combine has.  LX: the rows of h are quantised here first, under
-// the first weights.
+// stands between them.  SPLIT (few slots): the chunks are dealt to the wavefronts,
+// whose int32 sums are added in LDS.  A slot's sums become rows in LDS (with the
+// routing weights), and at the end the rows of a token are added in the order the
+// combine has.  (Quantising the rows of h here too, in every workgroup under its
+// first weights, took as long as the launch that does it: one token 51.5 / 50.2 us.)
 constexpr int DI = 8;  // steps of a chunk
-struct DownLds {
-    int cap, rows, slots, codes;  // chunks of a batch (0: not SPLIT); rows of h; slots; bytes of codes (0: they are in memory)
-    __host__ __device__ size_t parts() const { return (size_t)cap * 1024; }
-    __host__ __device__ size_t bytes() const { return parts() + (size_t)rows * 80 + (size_t)slots * 16 + (codes ? codes + rows * 8 : 0); }
-};
 struct DownRow {  // of h
     int f;        // its result row
-    float w, sx;  // routing weight; scale (LX: in scales)
+    float w, sx;  // routing weight, scale
     int pad;
 };
-template <int OF, bool LX, bool SPLIT>
+struct DownLds {
+    int rows, slots;  // of h; of the list
+    bool split;
+    __host__ __device__ size_t bytes() const { return (size_t)rows * (64 + sizeof(DownRow)) + (size_t)slots * (split ? 16 + 1024 : 16); }
+};
+template <int OF, bool SPLIT>
 __global__ __launch_bounds__(WAVE * SW) void i8_down_stream_kernel(I8Ffn a, void* y, DownLds m) {
     extern __shared__ __attribute__((aligned(16))) uint8_t down_lds[];
-    i32x4_t* part = reinterpret_cast<i32x4_t*>(down_lds);
-    float* rows = reinterpret_cast<float*>(down_lds + m.parts());
+    float* rows = reinterpret_cast<float*>(down_lds);
     DownRow* info = reinterpret_cast<DownRow*>(rows + m.rows * 16);
     int4* slots = reinterpret_cast<int4*>(info + m.rows);
-    int8_t* codes = reinterpret_cast<int8_t*>(slots + m.slots);
-    uint32_t* top = reinterpret_cast<uint32_t*>(codes + m.codes);
-    float* scales = reinterpret_cast<float*>(top + m.rows);
+    int* sums = reinterpret_cast<int*>(slots + m.slots);  // [slots][4 lane + v], SPLIT
     const int lane = lane_id(), wave = wave_index(), tid = threadIdx.x, lo = 16 * (lane / 16);
     const int c0 = blockIdx.x * 16, d = a.f.d, Tk = a.f.T * a.f.k;
     const int n = min(tile_count(a.f), m.slots);
     for (int i = tid; i < m.rows; i += WAVE * SW) {
         const int f = i < Tk ? a.f.perm_rows[i] : i;  // (every assignment of a selection is listed)
-        info[i] = DownRow{f, i < Tk ? a.f.topk_w[f] : 1.0f, LX ? 0.0f : a.hs[i], 0};
+        info[i] = DownRow{f, i < Tk ? a.f.topk_w[f] : 1.0f, a.hs[i], 0};
     }
     for (int i = tid; i < m.slots; i += WAVE * SW) {
         const int2 t = a.f.tiles[i];
@@ -315,12 +312,14 @@ __global__ __launch_bounds__(WAVE * SW) void i8_down_stream_kernel(I8Ffn a, void
         if (i < n) tile_rows<16>(a.f, i, tr);
         slots[i] = make_int4(t.x, tr.rbeg, tr.nrows, 0);
     }
+    if constexpr (SPLIT) {
+        for (int i = tid; i < n * 256; i += WAVE * SW) sums[i] = 0;
+    }
     __syncthreads();
     const int kmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F;
     const int kx = (kmax + SK * DI - 1) / (SK * DI);  // chunks of a slot
     struct Chunk {
-        i32x4_t w[DI], x[LX ? 1 : DI];
-        const int8_t* xp;
+        i32x4_t w[DI], x[DI];
         int K, s0;
     };
     auto weights_of = [&](const int4& s) -> const MatRef& { return s.x == a.f.E ? a.f.s_down : a.f.down; };
@@ -330,63 +329,44 @@ __global__ __launch_bounds__(WAVE * SW) void i8_down_stream_kernel(I8Ffn a, void
         f.s0 = chunk * DI;
         const int8_t* wp = static_cast<const int8_t*>(weights_of(s).q) + (row_of(s) + lane % 16) * f.K;
         const int row = s.y + min(lane % 16, s.z - 1);
-        f.xp = LX ? codes + row * a.f.ldh : a.hq + (size_t)row * a.f.ldh;
+        const int8_t* xp = a.hq + (size_t)row * a.f.ldh;
 #pragma unroll
         for (int u = 0; u < DI; ++u) {
             const int c = min(SK * (f.s0 + u) + lo, f.K - 16);  // (columns past the end: re-read, not used)
             f.w[u] = ld_codes(wp + c);
-            if constexpr (!LX) f.x[u] = ld_codes(f.xp + c);
+            f.x[u] = ld_codes(xp + c);
         }
         pin();
     };
     auto multiply = [&](const Chunk& f, i32x4_t acc) {
 #pragma unroll
         for (int u = 0; u < DI; ++u) {
-            const int c = SK * (f.s0 + u) + lo;
-            i32x4_t x;
-            if constexpr (LX) x = *reinterpret_cast<const i32x4_t*>(f.xp + min(c, f.K - 16));
-            else x = f.x[u];
-            if (c >= f.K) x = i32x4_t{0, 0, 0, 0};
-            acc = dot16(f.w[u], x, acc);
+            const bool in = SK * (f.s0 + u) + lo < f.K;
+            acc = dot16(f.w[u], in ? f.x[u] : i32x4_t{0, 0, 0, 0}, acc);
         }
         return acc;
     };
     auto result = [&](int sum, const int4& s, int r, int c, float sw) {  // row r of the slot, column c of the 16
         const DownRow q = info[s.y + r];
-        const float v = (float)sum * (LX ? scales[s.y + r] : q.sx) * sw;
+        const float v = (float)sum * q.sx * sw;
         rows[q.f * 16 + c] = v * q.w;
     };
     Chunk cur, next;
     if constexpr (SPLIT) {
-        const int items = n * kx, batch = m.cap / kx;  // chunks of all slots; slots of a batch
-        auto load_item = [&](Chunk& f, int item) { load(f, slots[item / kx], item % kx); };
-        if (wave < items) load_item(cur, wave);
-        if constexpr (LX) {
-            // rows 0 .. T k - 1 have F columns, the shared expert's behind them Fs
-            rows_to_lds<MOE_DT_F32>(a.h, Tk, a.f.F, a.f.ldh, codes, a.f.ldh, top, scales);
-            if (a.f.n_shared)
-                rows_to_lds<MOE_DT_F32>(a.h + (size_t)Tk * a.f.ldh, a.f.T, a.f.Fs, a.f.ldh, codes + Tk * a.f.ldh, a.f.ldh,
-                                        top + Tk, scales + Tk);
+        const int items = n * kx;  // chunks of all slots
+        if (wave < items) load(cur, slots[wave / kx], wave % kx);
+        for (int item = wave; item < items; item += SW) {
+            if (item + SW < items) load(next, slots[(item + SW) / kx], (item + SW) % kx);
+            const i32x4_t acc = multiply(cur, i32x4_t{0, 0, 0, 0});
+#pragma unroll
+            for (int v = 0; v < 4; ++v) atomicAdd(&sums[item / kx * 256 + 4 * lane + v], acc[v]);
+            cur = next;
         }
-        int item = wave;
-        for (int b0 = 0; b0 < n; b0 += batch) {
-            const int end = min(n, b0 + batch) * kx;
-            for (; item < end; item += SW) {
-                if (item + SW < items) load_item(next, item + SW);
-                part[(item - b0 * kx) * WAVE + lane] = multiply(cur, i32x4_t{0, 0, 0, 0});
-                cur = next;
-            }
-            __syncthreads();
-            for (int o = tid; o < (end - b0 * kx) / kx * 256; o += WAVE * SW) {
-                const int4 s = slots[b0 + o / 256];
-                const int r = o / 4 % 16, c = 4 * (o / 64 % 4) + o % 4;
-                if (r >= s.z) continue;
-                const int* p = reinterpret_cast<const int*>(part) + o / 256 * kx * 256 + o % 256;
-                int sum = 0;
-                for (int q = 0; q < kx; ++q) sum += p[q * 256];
-                result(sum, s, r, c, reinterpret_cast<const float*>(weights_of(s).scale)[row_of(s) + c]);
-            }
-            __syncthreads();
+        __syncthreads();
+        for (int o = tid; o < n * 256; o += WAVE * SW) {
+            const int4 s = slots[o / 256];
+            const int r = o / 4 % 16, c = 4 * (o / 64 % 4) + o % 4;
+            if (r < s.z) result(sums[o], s, r, c, reinterpret_cast<const float*>(weights_of(s).scale)[row_of(s) + c]);
         }
     } else {
         int slot = wave, chunk = 0;
@@ -413,8 +393,8 @@ __global__ __launch_bounds__(WAVE * SW) void i8_down_stream_kernel(I8Ffn a, void
             }
             cur = next;
         }
-        __syncthreads();
     }
+    __syncthreads();
     if (tid < a.f.T * 16) {
         const int t = tid / 16, c = tid % 16;
         float v = a.f.n_shared ? rows[(Tk + t) * 16 + c] : 0.0f;
@@ -449,8 +429,8 @@ hipError_t launch_channel_matmul(const ChannelArgs& a, hipStream_t st) {
     return launch_channel_matmul_tile(a, st);
 }
 
-// Layers of few tokens whose slots fit the down kernel's batches.
-bool i8_stream_takes(int T, int F, int Fs) { return T <= F8_ROUTE_MAX_T && F <= 8192 && Fs <= 8192; }
+// Layers of few tokens, 16 being the rows of an instruction.
+bool i8_stream_takes(int T) { return T <= F8_ROUTE_MAX_T; }
 
 hipError_t launch_i8_gateup_stream(const I8Ffn& a, hipStream_t st, const KTime& kt) {
     const int fmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F;
@@ -460,22 +440,10 @@ hipError_t launch_i8_gateup_stream(const I8Ffn& a, hipStream_t st, const KTime& 
 
 // Up to this many routed rows the chunks of K are split over the wavefronts.
 constexpr int DOWN_SPLIT_ROWS = 16;
-// LDS of a workgroup: up to 64 KB, 32 chunks of a batch, and the rows of h as codes
-// if they are few (every workgroup makes them all).
-static DownLds down_lds(const I8Ffn& a) {
-    const int kmax = a.f.n_shared && a.f.Fs > a.f.F ? a.f.Fs : a.f.F, kx = (kmax + SK * DI - 1) / (SK * DI);
-    const int rows = a.f.T * a.f.k + (a.f.n_shared ? a.f.T : 0);
-    if (a.f.T * a.f.k > DOWN_SPLIT_ROWS) return DownLds{0, rows, a.f.max_tiles, 0};  // (up to 528 rows, 522 slots)
-    DownLds m = {kx, rows, a.f.max_tiles, rows * a.f.ldh};                            // (up to 32 rows)
-    if (m.codes > I8_FUSE_VALUES) m.codes = 0;
-    while (m.cap + kx <= 32 && m.cap / kx < a.f.max_tiles && m.bytes() + kx * 1024 <= 65536) m.cap += kx;
-    return m;
-}
-bool i8_stream_quantises_h(const I8Ffn& a) { return down_lds(a).codes != 0; }
 
 hipError_t launch_i8_down_stream(const I8Ffn& a, void* y, int ydt, hipStream_t st, const KTime& kt) {
-    const DownLds m = down_lds(a);
-    const bool lx = m.codes != 0;
+    // (up to 16 * 33 rows and 522 slots: 51 KB; split, 32 and 18: 22 KB)
+    const DownLds m = {a.f.T * a.f.k + (a.f.n_shared ? a.f.T : 0), a.f.max_tiles, a.f.T * a.f.k <= DOWN_SPLIT_ROWS};
     const dim3 grid(a.f.d / 16);
     auto go = [&](auto kernel) {
         if (kt.start || kt.stop) hipExtLaunchKernelGGL(kernel, grid, WAVE * SW, m.bytes(), st, kt.start, kt.stop, 0, a, y, m);
@@ -483,9 +451,8 @@ hipError_t launch_i8_down_stream(const I8Ffn& a, void* y, int ydt, hipStream_t s
     };
     auto pick = [&](auto of) {
         constexpr int OF = decltype(of)::value;
-        if (lx) go(i8_down_stream_kernel<OF, true, true>);
-        else if (m.cap) go(i8_down_stream_kernel<OF, false, true>);
-        else go(i8_down_stream_kernel<OF, false, false>);
+        if (m.split) go(i8_down_stream_kernel<OF, true>);
+        else go(i8_down_stream_kernel<OF, false>);
     };
     if (ydt == MOE_DT_BF16) pick(ic<MOE_DT_BF16>());
     else pick(ic<MOE_DT_F32>());

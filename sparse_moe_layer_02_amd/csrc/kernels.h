@@ -205,9 +205,8 @@ struct I8Ffn {
 hipError_t launch_i8_gateup(const I8Ffn& a, hipStream_t st, const KTime& kt = KTime());
 hipError_t launch_i8_down(const I8Ffn& a, hipStream_t st, const KTime& kt = KTime());
 // The same for few tokens, each at most once with an expert (a selection's): h, and
-// y from h with the combine; h's rows are quantised in between unless the latter does.
-bool i8_stream_takes(int T, int F, int Fs);
-bool i8_stream_quantises_h(const I8Ffn& a);
+// y from h's quantised rows with the combine.
+bool i8_stream_takes(int T);
 hipError_t launch_i8_gateup_stream(const I8Ffn& a, hipStream_t st, const KTime& kt = KTime());
 hipError_t launch_i8_down_stream(const I8Ffn& a, void* y, int ydt, hipStream_t st, const KTime& kt = KTime());
 // Selection, grouping and quantisation of x (bf16) in one launch, for up to
