@@ -602,8 +602,11 @@ namespace {
 // Partial sums of moe_balance: a slot per range of tokens and per sequence
 // (balance.hip), for the most ranges that any number of tokens up to T makes.
 size_t balance_slots(const moe_config* c, int32_t n_seq) {
-    const int ranges = (c->n_tokens + 15) / 16;
+    const int ranges = (c->n_tokens + 7) / 8;
     return (size_t)(ranges < BALANCE_MAX_RANGES ? ranges : BALANCE_MAX_RANGES) + n_seq;
+}
+size_t balance_part(const moe_config* c, int32_t n_seq) {
+    return align256(balance_slots(c, n_seq) * ((c->n_expert + 3) / 4 * 16));
 }
 bool seqs_ok(const int32_t* off, int32_t n_seq) {
     return n_seq >= 1 && n_seq <= MAX_TOKENS && (off ? aligned4(off) : n_seq == 1);
@@ -612,8 +615,8 @@ bool seqs_ok(const int32_t* off, int32_t n_seq) {
 
 size_t moe_balance_workspace_bytes(const moe_config* cfg, int32_t n_seq) {
     if (validate_config(cfg) != MOE_OK || n_seq < 1 || n_seq > MAX_TOKENS) return 0;
-    const size_t slots = balance_slots(cfg, n_seq);
-    return 2 * align256(slots * cfg->n_expert * 4) + align256(slots * 4);
+    return 2 * balance_part(cfg, n_seq) + align256(balance_slots(cfg, n_seq) * 4) +
+           align256((size_t)n_seq * ((cfg->n_expert + 63) / 64) * 8) + align256((size_t)n_seq * 4);
 }
 
 int moe_balance(const moe_config* cfg, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
@@ -626,10 +629,12 @@ int moe_balance(const moe_config* cfg, const float* logits, const int32_t* topk_
         return MOE_ERR_INVALID;
     if (!ptr_ok(ws)) return MOE_ERR_INVALID;
     if (ws_bytes < moe_balance_workspace_bytes(cfg, n_seq)) return MOE_ERR_WORKSPACE;
-    const size_t part = align256(balance_slots(cfg, n_seq) * cfg->n_expert * 4);
+    const size_t cnt = balance_part(cfg, n_seq), num = 2 * cnt, loss_part = num + align256(balance_slots(cfg, n_seq) * 4),
+                 done = loss_part + align256((size_t)n_seq * ((cfg->n_expert + 63) / 64) * 8);
     const BalanceArgs a{logits, topk_idx, mask, seq_offsets, cfg->n_tokens, cfg->n_expert, cfg->top_k, cfg->score, n_seq,
-                        balance_chunk(cfg->n_tokens), at<float>(ws, 0), at<int32_t>(ws, part), at<int32_t>(ws, 2 * part),
-                        counts, tokens, prob, loss};
+                        balance_chunk(cfg->n_tokens, cfg->n_expert, n_seq), at<float>(ws, 0), at<int32_t>(ws, cnt),
+                        at<int32_t>(ws, num), at<double>(ws, loss_part), at<int32_t>(ws, done), counts, tokens, prob, loss,
+                        0, false};
     return device_status(launch_balance(a, static_cast<hipStream_t>(stream)));
 }
 

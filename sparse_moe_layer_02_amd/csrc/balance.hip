@@ -9,96 +9,191 @@
 //               + the selected weights' part (w = scale s / sum_sel s, or scale s)
 //   dL/dl[t, e] = dL/ds[t, e] s'(l), softmax: s_e (dL/ds_e - sum_i dL/ds_i s_i)
 //
-// Both directions read the logits once and are bound by memory.  A wavefront
-// takes a token; lane l holds experts l, l + 64, ...
+// Both directions read the logits once.  G lanes take a token (16 up to 256 experts,
+// so that a wavefront has four and a sum over experts is four DPP steps; 64 beyond):
+// lane `sub` holds four experts in a row, from 4 (sub + G j), j = 0 .. J - 1.
 //
 // Forward: a workgroup takes a range of tokens, sequence by sequence.  Its
 // wavefronts' sums meet in LDS in a fixed order and go to the slot (range +
 // sequence) of the workspace: along the tokens each step to the next range or
 // the next sequence is one slot further, so no two sums share one and none has
-// to be cleared first.  A second launch adds each sequence's slots in fp64.  No
-// floating-point atomics: the same bits every time.
+// to be cleared first.  A second launch adds each sequence's slots in fp64 (one
+// range and few sequences: the same workgroup does).  No floating-point atomics:
+// the same bits every time.
+#include <algorithm>
+#include <type_traits>
+
 #include "balance.h"
 #include "common.h"
 
 namespace moe {
 namespace {
 
-constexpr int BW = 16;  // wavefronts per workgroup of the forward pass
+constexpr int BW = 8;   // wavefronts per workgroup of the forward pass
 
-// Sequences.  q(t): the last sequence that begins at or before t (-1: none).
-// Offsets that do not ascend give some sequence, never an index out of range.
+// Sequences.  q(t): the last sequence that begins at or before t (-1: none;
+// n_seq: behind the last one), t the same in all lanes, which look at 64 offsets
+// at once.  Offsets that do not ascend give some sequence, never an index out of
+// range.
 __device__ __forceinline__ int seq_of(const int32_t* off, int n_seq, int t) {
-    int lo = 0, hi = n_seq + 1;  // off[lo - 1] <= t < off[hi]
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (off[mid] <= t) lo = mid + 1;
-        else hi = mid;
+    int lo = 0, n = n_seq + 1;  // off[lo - 1] <= t < off[lo + n]
+    while (n > 0) {
+        const int step = (n + WAVE - 1) / WAVE, i = lo + step * (lane_id() + 1) - 1;  // the last of the lane's offsets
+        const int at = min(i, lo + n - 1);
+        const int below = __popcll(__ballot(lo + step * lane_id() < lo + n && off[at] <= t));
+        const int end = lo + n;
+        lo += step * below;
+        if (lo >= end) return end - 1;
+        n = step == 1 ? 0 : min(step, end - lo) - 1;
     }
-    return lo - 1;  // n_seq: behind the last sequence
+    return lo - 1;
 }
 
-// Scores of one token, up to a common factor (softmax), and the derivatives
-// that do not need the sum.
-template <int KPL>
-struct Scores {
-    float s[KPL], ds[KPL];  // ds: s'(l) (not softmax)
-    float inv;              // 1 / sum s, 0 where the scores vanish
-};
+// e^x for x <= 0, off by less than two units (2^r 2^f with |f| <= 1/2, f from the
+// product's exact low part); 0 where it vanishes, NaN stays.
+__device__ __forceinline__ float exp_neg(float x) {
+    constexpr float L = 1.44269502f, L_LO = 1.92596299e-8f, BIG = 12582912.0f;  // log2 e; 1.5 * 2^23
+    x = x < -200.0f ? -200.0f : x;
+    const float t = fmaf(x, L, BIG), r = t - BIG;
+    const float p = __builtin_amdgcn_exp2f(fmaf(x, L_LO, fmaf(x, L, -r)));
+    return __builtin_ldexpf(p, (int)(__float_as_uint(t) - __float_as_uint(BIG)));
+}
 
-template <int KPL, bool GRAD>
-__device__ __forceinline__ void token_scores(const float (&l)[KPL], int E, int kind, Scores<KPL>& r) {
-    const int lane = lane_id();
-    if (kind == MOE_SCORE_SOFTMAX) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < KPL; ++j)
-            if (lane + WAVE * j < E) m = fmaxf(m, l[j]);
-#pragma unroll
-        for (int o = 1; o < WAVE; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) r.s[j] = m == -INFINITY ? (l[j] != l[j] ? l[j] : 0.0f) : expf(l[j] - m);
+// Score of a logit (softmax: up to the common factor, m the row's maximum) and
+// its derivative (not softmax).  The reciprocal, root and logarithm instructions
+// are off by one unit each.
+template <int KIND, bool GRAD>
+__device__ __forceinline__ float score_of(float l, float m, float& ds) {
+    if constexpr (KIND == MOE_SCORE_SOFTMAX) {
+        return exp_neg(l - m);
     } else {
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) {
-            // a = e^-|l|: neither direction overflows, and 1 - sigmoid keeps its digits
-            const float a = expf(-fabsf(l[j])), h = __fdiv_rn(1.0f, 1.0f + a);
-            const float sg = l[j] >= 0.0f ? h : a * h, one = l[j] >= 0.0f ? a * h : h;
-            if (kind == MOE_SCORE_SIGMOID) {
-                r.s[j] = l[j] != l[j] ? l[j] : sg;
-                if (GRAD) r.ds[j] = sg * one;
-            } else {
-                r.s[j] = sqrtf((l[j] < 0.0f ? 0.0f : l[j]) + log1pf(a));
-                if (GRAD) r.ds[j] = r.s[j] > 0.0f ? __fdiv_rn(0.5f * sg, r.s[j]) : 0.0f;
-            }
+        // a = e^-|l|: neither direction overflows, and 1 - sigmoid keeps its digits
+        const float a = exp_neg(-fabsf(l)), u = 1.0f + a, h = __builtin_amdgcn_rcpf(u), ah = a * h;
+        const float sg = l >= 0.0f ? h : ah;
+        if constexpr (KIND == MOE_SCORE_SIGMOID) {
+            if (GRAD) ds = ah * h;
+            return sg;
+        } else {
+            // log(1 + a) = log u + (a - (u - 1)) / u, the difference being exact
+            const float lg = fmaf(__builtin_amdgcn_logf(u), 0.693147181f, (a - (u - 1.0f)) * h);
+            const float x = (l < 0.0f ? 0.0f : l) + lg;
+            const bool tiny = x < 0x1p-96f;  // (the root flushes denormals)
+            const float s = __builtin_amdgcn_sqrtf(tiny ? x * 0x1p64f : x) * (tiny ? 0x1p-32f : 1.0f);
+            if (GRAD) ds = s > 0.0f ? 0.5f * sg * __builtin_amdgcn_rcpf(s) : (s != s ? s : 0.0f);
+            return s;
         }
     }
+}
+
+template <class F>
+__device__ __forceinline__ void with_score(int kind, F&& f) {
+    if (kind == MOE_SCORE_SOFTMAX) f(std::integral_constant<int, MOE_SCORE_SOFTMAX>());
+    else if (kind == MOE_SCORE_SIGMOID) f(std::integral_constant<int, MOE_SCORE_SIGMOID>());
+    else f(std::integral_constant<int, MOE_SCORE_SQRT_SOFTPLUS>());
+}
+
+// Over the G lanes of a token; each of them receives the same bits.
+template <int G, class Op>
+__device__ __forceinline__ float row_reduce(float v, Op op) {
+    v = op(v, __uint_as_float(dpp_u32<0x128>(__float_as_uint(v))));  // row_ror 8, 4, 2, 1
+    v = op(v, __uint_as_float(dpp_u32<0x124>(__float_as_uint(v))));
+    v = op(v, __uint_as_float(dpp_u32<0x122>(__float_as_uint(v))));
+    v = op(v, __uint_as_float(dpp_u32<0x121>(__float_as_uint(v))));
+    if constexpr (G == WAVE) {
+        const auto row = [&](int r) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 16 * r)); };
+        v = op(op(row(0), row(1)), op(row(2), row(3)));
+    }
+    return v;
+}
+struct MaxF { __device__ float operator()(float a, float b) const { return fmaxf(a, b); } };
+template <int G> __device__ __forceinline__ float row_sum(float v) { return row_reduce<G>(v, AddF()); }
+
+// The sum of the four rows of 16 lanes, in each of them.
+__device__ __forceinline__ float rows_sum(float v) {
+    const uint32_t a = __float_as_uint(v);
+    const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    const float w = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    const uint32_t b = __float_as_uint(w);
+    const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+
+// Expert of a lane's value 4 j + v.
+template <int G>
+__device__ __forceinline__ int expert_of(int sub, int v) { return 4 * (sub + G * (v / 4)) + v % 4; }
+
+// A token's row; WIDE: its length and address are multiples of 16 bytes.
+template <int G, int J, bool WIDE, class T4, class T>
+__device__ __forceinline__ void load_row(const T* row, int E, int sub, T (&l)[4 * J]) {
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int e = expert_of<G>(sub, 4 * j);
+            const T4 x = *reinterpret_cast<const T4*>(row + (e < E ? e : 0));
+            l[4 * j] = x.x, l[4 * j + 1] = x.y, l[4 * j + 2] = x.z, l[4 * j + 3] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < 4 * J; ++v) {
+            const int e = expert_of<G>(sub, v);
+            l[v] = row[e < E ? e : 0];
+        }
+    }
+}
+
+// The scores of a token; inv = 1 / sum s (0 where the scores vanish), m as for score_of.
+template <int G, int J, bool GRAD>
+__device__ __forceinline__ void token_scores(const float (&l)[4 * J], int E, int sub, int kind, float (&s)[4 * J],
+                                             float (&ds)[4 * J], float& m, float& inv) {
+    m = 0.0f;
+    if (kind == MOE_SCORE_SOFTMAX) {
+        m = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < 4 * J; ++v)
+            if (expert_of<G>(sub, v) < E) m = fmaxf(m, l[v]);
+        m = row_reduce<G>(m, MaxF());
+        if (m == -INFINITY) m = 0.0f;  // (no score, rather than NaN)
+    }
     float sum = 0.0f;
+    with_score(kind, [&](auto KIND) {
 #pragma unroll
-    for (int j = 0; j < KPL; ++j) {
-        if (lane + WAVE * j >= E) r.s[j] = 0.0f;
-        sum += r.s[j];
-    }
-    sum = wave_sum(sum);
-    r.inv = sum < 0x1p-126f ? 0.0f : __fdiv_rn(1.0f, sum);
+        for (int v = 0; v < 4 * J; ++v) {
+            s[v] = score_of<KIND.value, GRAD>(l[v], m, ds[v]);
+            if (expert_of<G>(sub, v) >= E) s[v] = 0.0f;
+            sum += s[v];
+            if (v % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // four at once: all of them take too many registers
+        }
+    });
+    sum = row_sum<G>(sum);
+    inv = sum < 0x1p-126f ? 0.0f : __builtin_amdgcn_rcpf(sum);
 }
 
-template <int KPL>
-__device__ __forceinline__ void load_row(const float* row, int E, float (&l)[KPL]) {
-#pragma unroll
-    for (int j = 0; j < KPL; ++j) {
-        const int e = lane_id() + WAVE * j;
-        l[j] = e < E ? row[e] : 0.0f;
-    }
+// A sequence's sum of the wavefronts' parts of its loss, in their order, for thread 0.
+template <int W>
+__device__ __forceinline__ double loss_sum(double loss, double (&parts)[W]) {
+    loss = wave_sum_f64(loss);
+    if (lane_id() == 0) parts[wave_index()] = loss;
+    __syncthreads();
+    for (int w = 1; w < W; ++w) loss += parts[w];
+    return loss;
 }
 
-template <int KPL>
+template <int G, int J, bool WIDE>
 __global__ __launch_bounds__(BW * WAVE) void balance_kernel(BalanceArgs a) {
-    __shared__ float part[BW][KPL * WAVE];
-    __shared__ int hist[KPL * WAVE], alive[BW];
+    constexpr int V = 4 * J, NT = WAVE / G, KI = (BALANCE_MAX_K + G - 1) / G;  // a lane's values, a wavefront's tokens, a lane's selections
+    constexpr int EP = G * V;
+    __shared__ __attribute__((aligned(16))) float part[BW][EP];
+    __shared__ int hist[EP], alive[BW];
+    __shared__ double losses[BW];
     const int tid = threadIdx.x, lane = lane_id(), wave = wave_index(), E = a.E;
+    const int sub = lane % G, first = wave * NT + lane / G;
     const int t1 = min(a.T, (int)(blockIdx.x + 1) * a.chunk);
     int t0 = blockIdx.x * a.chunk;
+    struct Token {
+        float l[V];
+        int x[KI];
+        bool live;
+    };
     while (t0 < t1) {
         int q = 0, e = t1;
         if (a.off) {
@@ -110,220 +205,404 @@ __global__ __launch_bounds__(BW * WAVE) void balance_kernel(BalanceArgs a) {
                 continue;
             }
         }
+        const auto load = [&](int t, Token& k) {
+            k.live = t < e;
+            t = min(t, e - 1);
+            if (a.mask) k.live = k.live && a.mask[t];
+            load_row<G, J, WIDE, float4>(a.logits + (size_t)t * E, E, sub, k.l);
+#pragma unroll
+            for (int i = 0; i < KI; ++i) {
+                const int j = sub + G * i;
+                k.x[i] = j < a.k ? a.idx[(size_t)t * a.k + j] : -1;
+            }
+        };
+        Token cur;
+        load(t0 + first, cur);
         for (int i = tid; i < E; i += BW * WAVE) hist[i] = 0;
         __syncthreads();
-        float P[KPL];
+        float P[V];
         int n = 0;
 #pragma unroll
-        for (int j = 0; j < KPL; ++j) P[j] = 0.0f;
-        for (int t = t0 + wave; t < e; t += BW) {
-            if (a.mask && !a.mask[t]) continue;
-            ++n;
-            float l[KPL];
-            Scores<KPL> r;
-            load_row(a.logits + (size_t)t * E, E, l);
-            for (int j = lane; j < a.k; j += WAVE) {
-                const int x = a.idx[(size_t)t * a.k + j];
-                if (x >= 0 && x < E) atomicAdd(&hist[x], 1);
-            }
-            token_scores<KPL, false>(l, E, a.score, r);
+        for (int v = 0; v < V; ++v) P[v] = 0.0f;
+        for (int t = t0; t < e; t += BW * NT) {
+            float s[V], ds[V], top, inv;
+            token_scores<G, J, false>(cur.l, E, sub, a.score, s, ds, top, inv);
+            const bool live = cur.live;
+            n += live;
 #pragma unroll
-            for (int j = 0; j < KPL; ++j) P[j] += r.s[j] * r.inv;
+            for (int i = 0; i < KI; ++i)
+                if (live && cur.x[i] >= 0 && cur.x[i] < E) atomicAdd(&hist[cur.x[i]], 1);
+            if (t + BW * NT < e) load(t + BW * NT + first, cur);
+#pragma unroll
+            for (int v = 0; v < V; ++v) P[v] = live ? fmaf(s[v], inv, P[v]) : P[v];
         }
+        if constexpr (NT > 1) {
 #pragma unroll
-        for (int j = 0; j < KPL; ++j) part[wave][lane + WAVE * j] = P[j];
+            for (int v = 0; v < V; ++v) P[v] = rows_sum(P[v]);
+        }
+        if (lane < G) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                *reinterpret_cast<float4*>(&part[wave][expert_of<G>(sub, 4 * j)]) =
+                    make_float4(P[4 * j], P[4 * j + 1], P[4 * j + 2], P[4 * j + 3]);
+        }
+        n = sub == 0 ? n : 0;
+#pragma unroll
+        for (int o = G; o < WAVE; o <<= 1) n += __shfl_xor(n, o);
         if (lane == 0) alive[wave] = n;
         __syncthreads();
-        const size_t slot = (size_t)(blockIdx.x + q);
-        for (int i = tid; i < E; i += BW * WAVE) {
+        int tokens = 0;
+#pragma unroll
+        for (int w = 0; w < BW; ++w) tokens += alive[w];
+        const size_t slot = (size_t)(blockIdx.x + q), Ep = (E + 3) / 4 * 4;
+        const double rn = tokens > 0 ? 1.0 / tokens : 0.0, rf = rn * E / a.k;
+        double loss = 0.0;
+        for (int i = tid; i < Ep; i += BW * WAVE) {
             float s = part[0][i];
 #pragma unroll
             for (int w = 1; w < BW; ++w) s += part[w][i];
-            a.sum[slot * E + i] = s;
-            a.cnt[slot * E + i] = hist[i];
+            const int c = i < E ? hist[i] : 0;
+            if (!a.one_launch) {
+                a.sum[slot * Ep + i] = s;
+                a.cnt[slot * Ep + i] = c;
+            } else if (i < E) {
+                a.prob[i] = (float)(s * rn);
+                a.counts[i] = c;
+                loss += (c * rf) * (s * rn);
+            }
         }
-        if (tid == 0) {
-            int m = 0;
-            for (int w = 0; w < BW; ++w) m += alive[w];
-            a.num[slot] = m;
+        if (a.one_launch) {
+            loss = loss_sum(loss, losses);
+            if (tid == 0) a.loss[0] = (float)loss, a.tokens[0] = tokens;
+            return;
         }
+        if (tid == 0) a.num[slot] = tokens;
         __syncthreads();
         t0 = e;
     }
+    if (a.one_launch) {  // no tokens
+        for (int i = tid; i < E; i += BW * WAVE) a.prob[i] = 0.0f, a.counts[i] = 0;
+        if (tid == 0) a.loss[0] = 0.0f, a.tokens[0] = 0;
+        return;
+    }
+    if (a.blocks == 1) return;
+    for (int64_t i = (int64_t)blockIdx.x * BW * WAVE + tid; i < a.n_seq; i += (int64_t)gridDim.x * BW * WAVE) a.done[i] = 0;
 }
 
-// One sequence per workgroup: BW slot lanes x 64 experts at a time.
-__global__ __launch_bounds__(BW * WAVE) void balance_join_kernel(BalanceArgs a) {
-    __shared__ double sums[BW][WAVE];
-    __shared__ int cnts[BW][WAVE];
-    const int q = blockIdx.x, lane = lane_id(), wave = wave_index(), E = a.E;
+// The second launch: a sequence's experts, or a block of 64 of them, by a workgroup:
+// quads of experts x ranges, then the ranges' sums in order.  The last block of a
+// sequence to end adds the parts of the loss, in the blocks' order.
+constexpr int JW = 16;
+__global__ __launch_bounds__(JW * WAVE) void balance_join_kernel(BalanceArgs a) {
+    __shared__ double sum[JW * WAVE * 4], losses[JW];
+    __shared__ int cnt[JW * WAVE * 4];
+    const int q = blockIdx.x / a.blocks, block = blockIdx.x % a.blocks;
+    const int tid = threadIdx.x, lane = lane_id(), E = a.E, Q = (E + 3) / 4;
+    const int width = a.blocks > 1 ? 16 : Q;  // quads of the block
+    const int way = tid / width, quad = block * width + tid % width;
     int b = 0, e = a.T;
     if (a.off) {
         b = max(0, min(a.off[q], a.T));
         e = max(b, min(a.off[q + 1], a.T));
     }
     const int c0 = b / a.chunk, c1 = e > b ? (e - 1) / a.chunk + 1 : c0;
+    const int ways = min(min(64, JW * WAVE / width), c1 - c0);
     int n = 0;
     for (int c = c0 + lane; c < c1; c += WAVE) n += a.num[c + q];
+    if (way < ways && quad < Q) {
+        double s[4] = {};
+        int k[4] = {};
+#pragma unroll 4
+        for (int c = c0 + way; c < c1; c += ways) {
+            const size_t at = (size_t)(c + q) * Q + quad;
+            const float4 x = reinterpret_cast<const float4*>(a.sum)[at];
+            const int4 y = reinterpret_cast<const int4*>(a.cnt)[at];
+            s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w;
+            k[0] += y.x, k[1] += y.y, k[2] += y.z, k[3] += y.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[4 * tid + i] = s[i], cnt[4 * tid + i] = k[i];
+    }
 #pragma unroll
     for (int o = 1; o < WAVE; o <<= 1) n += __shfl_xor(n, o);
-    if (threadIdx.x == 0) a.tokens[q] = n;
+    __syncthreads();
     const double rn = n > 0 ? 1.0 / n : 0.0, rf = rn * E / a.k;
     double loss = 0.0;
-    for (int i0 = 0; i0 < E; i0 += WAVE) {
-        const int i = i0 + lane;
+    const int x = 4 * width * block + tid;
+    if (tid < 4 * width && x < E) {
         double s = 0.0;
-        int m = 0;
-        if (i < E) {
-            for (int c = c0 + wave; c < c1; c += BW) {
-                s += (double)a.sum[(size_t)(c + q) * E + i];
-                m += a.cnt[(size_t)(c + q) * E + i];
-            }
-        }
-        sums[wave][lane] = s;
-        cnts[wave][lane] = m;
-        __syncthreads();
-        if (wave == 0 && i < E) {
-            for (int w = 1; w < BW; ++w) {
-                s += sums[w][lane];
-                m += cnts[w][lane];
-            }
-            a.prob[(size_t)q * E + i] = (float)(s * rn);
-            a.counts[(size_t)q * E + i] = m;
-            loss += (m * rf) * (s * rn);
-        }
-        __syncthreads();
+        int k = 0;
+        for (int w = 0; w < ways; ++w) s += sum[4 * width * w + tid], k += cnt[4 * width * w + tid];
+        a.prob[(size_t)q * E + x] = (float)(s * rn);
+        a.counts[(size_t)q * E + x] = k;
+        loss = (k * rf) * (s * rn);
     }
-    if (wave == 0) {
-        loss = wave_sum_f64(loss);
-        if (lane == 0) a.loss[q] = (float)loss;
+    loss = loss_sum(loss, losses);
+    if (tid != 0) return;
+    if (block == 0) a.tokens[q] = n;
+    if (a.blocks > 1) {
+        double* part = a.loss_part + (size_t)q * a.blocks;
+        __hip_atomic_store(part + block, loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (__hip_atomic_fetch_add(a.done + q, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) != a.blocks - 1) return;
+        loss = 0.0;
+        for (int i = 0; i < a.blocks; ++i) loss += __hip_atomic_load(part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
+    a.loss[q] = (float)loss;
 }
 
 constexpr int GW = 4;  // wavefronts per workgroup of the backward pass
 
-template <int KPL>
-__global__ __launch_bounds__(GW * WAVE) void route_backward_kernel(RouteGradArgs a) {
-    const int lane = lane_id(), E = a.E;
+// What a wavefront's lanes write to LDS others of them read: in order there, kept
+// in order by the compiler too.
+__device__ __forceinline__ void lds_in_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+template <int G, int J, bool WIDE>
+__global__ __launch_bounds__(GW * WAVE, 4) void route_backward_kernel(RouteGradArgs a) {
+    constexpr int V = 4 * J, NT = WAVE / G, KI = (BALANCE_MAX_K + G - 1) / G, EP = G * V;
+    __shared__ __attribute__((aligned(16))) float selected[GW][NT][EP];  // dL/ds of the selected weights, 0 between tokens
+    const int lane = lane_id(), sub = lane % G, grp = lane / G, E = a.E;
     const int w0 = blockIdx.x * GW + wave_index();
-    int q = -2, q_end = 0;  // the sequence of the last token, and its end
-    float f[KPL], rate = 0.0f;
+    float* buf = selected[wave_index()][grp];
+    const bool soft = a.score == MOE_SCORE_SOFTMAX;
+    if (a.d_w) {
 #pragma unroll
-    for (int j = 0; j < KPL; ++j) f[j] = 0.0f;
-    for (int t = w0 * a.chunk; t < min(a.T, (w0 + 1) * a.chunk); ++t) {
-        float* out = a.d_logits + (size_t)t * E;
-        if (q == -2 || t >= q_end) {
-            q = 0;
-            q_end = a.T;
-            if (a.off) {
-                q = seq_of(a.off, a.n_seq, t);
-                q_end = q >= a.n_seq ? a.T : max(a.off[q + 1], t + 1);
-                if (q >= a.n_seq) q = -1;
+        for (int j = 0; j < J; ++j) *reinterpret_cast<float4*>(buf + expert_of<G>(sub, 4 * j)) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    struct Token {
+        float l[V], dw[KI];
+        int x[KI];
+        bool live;
+    };
+    const auto load = [&](int t, Token& k) {
+        k.live = t < a.T;
+        t = min(t, a.T - 1);
+        if (a.mask) k.live = k.live && a.mask[t];
+        if (a.d_w) {
+#pragma unroll
+            for (int i = 0; i < KI; ++i) {
+                const int j = sub + G * i;
+                const int x = j < a.k ? a.idx[(size_t)t * a.k + j] : -1;
+                k.x[i] = x >= 0 && x < E ? x : E;
+                k.dw[i] = x >= 0 && x < E ? a.scale * a.d_w[(size_t)t * a.k + j] : 0.0f;
             }
+        }
+        load_row<G, J, WIDE, float4>(a.logits + (size_t)t * E, E, sub, k.l);
+    };
+    int q = 0, q_end = 0;  // the sequence of the last token, and its end
+    float f[V], rate = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) f[v] = 0.0f;
+    Token cur;
+    const int b = w0 * a.chunk * NT, e = min(a.T, b + a.chunk * NT);
+    for (int t_ = b; t_ < e; t_ += NT) {
+        const int t = t_ + grp;
+        load(t, cur);
+        bool entered = false;
+        while (const uint64_t need = __ballot(t >= q_end && t < a.T)) {
+            const int tn = __builtin_amdgcn_readlane(t, __ffsll((unsigned long long)need) - 1);
+            int qn = 0, end = a.T;
+            if (a.off) {
+                qn = seq_of(a.off, a.n_seq, tn);
+                end = qn >= a.n_seq ? a.T : max(a.off[qn + 1], tn + 1);
+                if (qn >= a.n_seq) qn = -1;
+            }
+            if (t >= tn && t >= q_end && t < end) {
+                q = qn;
+                q_end = end;
+                entered = true;
+            }
+        }
+        if (entered) {
             if (a.d_loss && q >= 0) {
                 // f - 1: of the gradient's f - sum f p only differences of f count,
                 // and small numbers lose less in them
                 const int n = max(a.tokens[q], 1);
                 const double rf = (double)E / ((double)a.k * n);
                 rate = __fdiv_rn(a.d_loss[q], (float)n);
+                int c[V];
+                load_row<G, J, WIDE, int4>(a.counts + (size_t)q * E, E, sub, c);
 #pragma unroll
-                for (int j = 0; j < KPL; ++j) {
-                    const int e = lane + WAVE * j;
-                    f[j] = e < E ? (float)(a.counts[(size_t)q * E + e] * rf - 1.0) : 0.0f;
-                }
+                for (int v = 0; v < V; ++v) f[v] = expert_of<G>(sub, v) < E ? (float)(c[v] * rf - 1.0) : 0.0f;
             }
         }
-        if (q < 0 || (a.mask && !a.mask[t])) {  // no gradient
+        float ls[KI];
+        if (a.d_w) {
 #pragma unroll
-            for (int j = 0; j < KPL; ++j)
-                if (lane + WAVE * j < E) out[lane + WAVE * j] = 0.0f;
-            continue;
+            for (int i = 0; i < KI; ++i)
+                if (G * i < a.k) ls[i] = a.logits[(size_t)min(t, a.T - 1) * E + (cur.x[i] < E ? cur.x[i] : 0)];
         }
-        float l[KPL], g[KPL];
-        Scores<KPL> r;
-        load_row(a.logits + (size_t)t * E, E, l);
-        token_scores<KPL, true>(l, E, a.score, r);
-        const bool soft = a.score == MOE_SCORE_SOFTMAX;
-        const float norm = soft ? r.inv : 1.0f;  // s as the router has it
+        float s[V], ds[V], g[V], top, total;  // total: 1 / sum s
+        token_scores<G, J, true>(cur.l, E, sub, a.score, s, ds, top, total);
+        const float norm = soft ? total : 1.0f;  // s as the router has it
+        const float inv = soft ? 1.0f : total;
 #pragma unroll
-        for (int j = 0; j < KPL; ++j) {
-            r.s[j] *= norm;
-            g[j] = 0.0f;
+        for (int v = 0; v < V; ++v) {
+            s[v] *= norm;
+            g[v] = 0.0f;
         }
         if (a.d_loss) {
             float fp = 0.0f;
-            const float inv = soft ? 1.0f : r.inv;
 #pragma unroll
-            for (int j = 0; j < KPL; ++j) fp += f[j] * (r.s[j] * inv);
-            fp = wave_sum(fp);
+            for (int v = 0; v < V; ++v) fp = fmaf(f[v], s[v] * inv, fp);
+            fp = row_sum<G>(fp);
 #pragma unroll
-            for (int j = 0; j < KPL; ++j) g[j] = rate * (f[j] - fp) * inv;
+            for (int v = 0; v < V; ++v) g[v] = rate * (f[v] - fp) * inv;
         }
         if (a.d_w) {
-            // lane j < k: the j-th selected expert (E: none), its score and weight's gradient
-            const int x0 = lane < a.k ? a.idx[(size_t)t * a.k + lane] : E;
-            const int x = x0 >= 0 && x0 < E ? x0 : E;
-            float dw = x < E ? a.scale * a.d_w[(size_t)t * a.k + lane] : 0.0f, sel = 0.0f;
+            // a lane's selected experts (E: none), their scores and weights' gradients
+            float sel[KI], add[KI], S = 0.0f;
+            with_score(a.score, [&](auto KIND) {
 #pragma unroll
-            for (int j = 0; j < KPL; ++j) {
-                const float v = __shfl(r.s[j], x & 63);
-                if (x >> 6 == j) sel = v;
-            }
-            if (x >= E) sel = 0.0f;
+                for (int i = 0; i < KI; ++i) {
+                    float unused;
+                    sel[i] = 0.0f;
+                    if (G * i < a.k && cur.x[i] < E) sel[i] = score_of<KIND.value, false>(ls[i], top, unused) * norm;
+                    S += sel[i];
+                }
+            });
             if (a.normalise) {
-                const float S = wave_sum(sel), rS = S < 0x1p-126f ? 0.0f : __fdiv_rn(1.0f, S);
-                const float dot = wave_sum(dw * (sel * rS));
-                dw = x < E ? (dw - dot) * rS : 0.0f;
-            }
-            for (int i = 0; i < a.k; ++i) {
-                const int xi = __builtin_amdgcn_readlane(x, i);
-                const float di = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(dw), i));
+                S = row_sum<G>(S);
+                const float rS = S < 0x1p-126f ? 0.0f : __builtin_amdgcn_rcpf(S);
+                float dot = 0.0f;
 #pragma unroll
-                for (int j = 0; j < KPL; ++j)
-                    if (lane + WAVE * j == xi) g[j] += di;
+                for (int i = 0; i < KI; ++i) dot += cur.dw[i] * (sel[i] * rS);
+                dot = row_sum<G>(dot);
+#pragma unroll
+                for (int i = 0; i < KI; ++i) cur.dw[i] = cur.x[i] < E ? (cur.dw[i] - dot) * rS : 0.0f;
             }
+            // an expert listed twice: one of its lanes reads the other's mark, and all
+            // of them take the sum in the order of the list
+            bool twice = false;
+#pragma unroll
+            for (int i = 0; i < KI; ++i) {
+                add[i] = cur.dw[i];
+                if (cur.x[i] < E) reinterpret_cast<int*>(buf)[cur.x[i]] = lane + WAVE * i;
+            }
+            lds_in_order();
+#pragma unroll
+            for (int i = 0; i < KI; ++i)
+                if (cur.x[i] < E) twice |= reinterpret_cast<int*>(buf)[cur.x[i]] != lane + WAVE * i;
+            if (__ballot(twice)) {
+#pragma unroll
+                for (int i = 0; i < KI; ++i) add[i] = 0.0f;
+                for (int j = 0; j < a.k; ++j) {
+                    int xj = E;
+                    float dj = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < KI; ++i) {
+                        const int x = __shfl(cur.x[i], j % G, G);
+                        const float d = __shfl(cur.dw[i], j % G, G);
+                        if (j / G == i) xj = x, dj = d;
+                    }
+#pragma unroll
+                    for (int i = 0; i < KI; ++i)
+                        if (cur.x[i] == xj) add[i] += dj;
+                }
+            }
+            lds_in_order();
+#pragma unroll
+            for (int i = 0; i < KI; ++i)
+                if (cur.x[i] < E) buf[cur.x[i]] = add[i];
+            lds_in_order();
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float4 d = *reinterpret_cast<const float4*>(buf + expert_of<G>(sub, 4 * j));
+                g[4 * j] += d.x, g[4 * j + 1] += d.y, g[4 * j + 2] += d.z, g[4 * j + 3] += d.w;
+            }
+            lds_in_order();
+#pragma unroll
+            for (int i = 0; i < KI; ++i)
+                if (cur.x[i] < E) buf[cur.x[i]] = 0.0f;
+            lds_in_order();
         }
         if (soft) {
             float dot = 0.0f;
 #pragma unroll
-            for (int j = 0; j < KPL; ++j) dot += g[j] * r.s[j];
-            dot = wave_sum(dot);
+            for (int v = 0; v < V; ++v) dot = fmaf(g[v], s[v], dot);
+            dot = row_sum<G>(dot);
 #pragma unroll
-            for (int j = 0; j < KPL; ++j) g[j] = r.s[j] * (g[j] - dot);
+            for (int v = 0; v < V; ++v) g[v] = s[v] * (g[v] - dot);
         } else {
 #pragma unroll
-            for (int j = 0; j < KPL; ++j) g[j] *= r.ds[j];
+            for (int v = 0; v < V; ++v) g[v] *= ds[v];
         }
+        const bool live = cur.live && q >= 0;  // else no gradient
 #pragma unroll
-        for (int j = 0; j < KPL; ++j)
-            if (lane + WAVE * j < E) out[lane + WAVE * j] = g[j];
+        for (int v = 0; v < V; ++v) g[v] = live ? g[v] : 0.0f;
+        if (t < a.T) {
+            float* out = a.d_logits + (size_t)t * E;
+            if constexpr (WIDE) {
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int x = expert_of<G>(sub, 4 * j);
+                    if (x < E) *reinterpret_cast<float4*>(out + x) = make_float4(g[4 * j], g[4 * j + 1], g[4 * j + 2], g[4 * j + 3]);
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (expert_of<G>(sub, v) < E) out[expert_of<G>(sub, v)] = g[v];
+            }
+        }
     }
+}
+
+// Lanes a token, quads of experts a lane, and whether rows are read as quads.
+template <class F>
+void with_layout(int E, uintptr_t addresses, F&& f) {
+    using std::integral_constant;
+    const auto go = [&](auto G, auto J) {
+        if (E % 4 == 0 && addresses % 16 == 0) f(G, J, std::true_type());
+        else f(G, J, std::false_type());
+    };
+    const integral_constant<int, 16> g16;
+    const integral_constant<int, WAVE> g64;
+    if (E <= 64) go(g16, integral_constant<int, 1>());
+    else if (E <= 128) go(g16, integral_constant<int, 2>());
+    else if (E <= 192) go(g16, integral_constant<int, 3>());
+    else if (E <= 256) go(g16, integral_constant<int, 4>());
+    else if (E <= 512) go(g64, integral_constant<int, 2>());
+    else go(g64, integral_constant<int, 4>());
 }
 
 }  // namespace
 
-int balance_chunk(int T) {
-    // whole rounds of a workgroup's wavefronts
-    static_assert(BW == 16, "ranges of the workspace");
+int balance_chunk(int T, int E, int n_seq) {
+    // whole rounds of a workgroup's wavefronts; two of them stay in one workgroup, and
+    // one launch (37 tokens of 192 experts: 5.2 us, two launches 7.1; four rounds of
+    // 256 experts: 8.6, 7.9), where there are no more sequences to take one by one
+    const int round = BW * (E <= 256 ? 4 : 1);
+    if (T <= 2 * round && n_seq == 1) return 2 * round;
     const int per = (T + BALANCE_MAX_RANGES - 1) / BALANCE_MAX_RANGES;
-    return (per + BW - 1) / BW * BW;
+    return (per + round - 1) / round * round;
 }
 
-hipError_t launch_balance(const BalanceArgs& a, hipStream_t st) {
+hipError_t launch_balance(BalanceArgs a, hipStream_t st) {
     const int grid = (a.T + a.chunk - 1) / a.chunk;
-    if (a.E <= 256) balance_kernel<4><<<grid, BW * WAVE, 0, st>>>(a);
-    else balance_kernel<16><<<grid, BW * WAVE, 0, st>>>(a);
+    // 64 experts a workgroup of the second launch where a sequence has many ranges
+    // (65536 tokens of 256 experts: 26.5 us, 29.1 with all of them; 256 tokens: 9.2, 7.9)
+    a.blocks = grid / a.n_seq >= 256 ? (a.E + 63) / 64 : 1;
+    a.one_launch = grid == 1 && a.n_seq == 1;
+    with_layout(a.E, reinterpret_cast<uintptr_t>(a.logits), [&](auto G, auto J, auto WIDE) {
+        balance_kernel<G.value, J.value, WIDE.value><<<grid, BW * WAVE, 0, st>>>(a);
+    });
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    balance_join_kernel<<<a.n_seq, BW * WAVE, 0, st>>>(a);
+    if (e != hipSuccess || a.one_launch) return e;
+    balance_join_kernel<<<a.n_seq * a.blocks, JW * WAVE, 0, st>>>(a);
     return hipGetLastError();
 }
 
 hipError_t launch_route_backward(RouteGradArgs a, hipStream_t st) {
-    a.chunk = a.T < 8192 ? 1 : a.T < 65536 ? 4 : 8;
-    const int grid = (int)(((int64_t)a.T + GW * a.chunk - 1) / (GW * a.chunk));
-    if (a.E <= 256) route_backward_kernel<4><<<grid, GW * WAVE, 0, st>>>(a);
-    else route_backward_kernel<16><<<grid, GW * WAVE, 0, st>>>(a);
+    const uintptr_t addresses = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.d_logits) |
+                                reinterpret_cast<uintptr_t>(a.counts);
+    with_layout(a.E, addresses, [&](auto G, auto J, auto WIDE) {
+        const int64_t rounds = ((int64_t)a.T * G.value + WAVE - 1) / WAVE;  // a wavefront's tokens at a time
+        a.chunk = (int)std::min<int64_t>(std::max<int64_t>(rounds / 4096, 1), 8);
+        const int grid = (int)((rounds + GW * a.chunk - 1) / (GW * a.chunk));
+        route_backward_kernel<G.value, J.value, WIDE.value><<<grid, GW * WAVE, 0, st>>>(a);
+    });
     return hipGetLastError();
 }
 

@@ -96,6 +96,47 @@ def test_balance(dev, T, E, k, n_seq, kind):
         assert (np.abs(loss - rl) <= rel * rl).all()
 
 
+# the last tokens of one workgroup and the first of two, one sequence's ranges joined by one workgroup and by several
+EDGES = [(16, 300, 4), (17, 300, 4), (64, 100, 8), (65, 100, 8), (128, 200, 8), (5000, 200, 8), (8191, 130, 6), (8193, 130, 6),
+         (20001, 260, 4)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,E,k", EDGES)
+def test_balance_of_one_sequence(dev, T, E, k, kind):
+    l, idx, off, mask, rng = batch(T, E, k, 1, T + E)
+    say("one sequence", T, E, k, kind)
+    for o, m in ((None, mask), (np.array([T // 3, T - T // 5], np.int32), mask), (np.array([T, T], np.int32), None)):
+        counts, tokens, prob, loss = run_balance(dev, l, idx, kind, o, m, 1)
+        rc, rt, rp, rl, rel = R.balance(l, idx, kind, o, m, 1)
+        assert np.array_equal(counts, rc) and np.array_equal(tokens, rt)
+        assert (np.abs(prob - rp) <= rel * rp).all()
+        assert (np.abs(loss - rl) <= rel * rl).all()
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3])
+def test_rows_at_any_address(dev, shift):
+    """Rows that begin 4, 8 and 12 bytes off a multiple of 16: the same bits."""
+    torch, moe = dev
+    T, E, k = 300, 128, 4
+    l, idx, _, _, rng = batch(T, E, k, 1, 3, seqs=False)
+    c = moe.make_config(T, 64, E, k, 64, n_shared=0, score="sigmoid")
+    idx, d_w, d_loss = (torch.from_numpy(a).cuda() for a in (idx, rng.standard_normal((T, k)).astype(np.float32), np.ones(1, np.float32)))
+    out = []
+    for s in (0, shift):
+        lg = torch.empty(T * E + s, device="cuda")[s:].view(T, E)
+        lg.copy_(torch.from_numpy(l))
+        counts = torch.empty(E + s, dtype=torch.int32, device="cuda")[s:].view(1, E)
+        tokens, prob, loss = torch.empty(1, dtype=torch.int32, device="cuda"), torch.empty((1, E), device="cuda"), torch.empty(1, device="cuda")
+        d = torch.empty(T * E + s, device="cuda")[s:].view(T, E)
+        say("address", s)
+        moe.moe_balance(c, lg, idx, counts, tokens, prob, loss, moe.balance_workspace(c, 1))
+        moe.moe_route_backward(c, None, lg, idx, d, d_topk_w=d_w, counts=counts, tokens=tokens, d_loss=d_loss)
+        torch.cuda.synchronize()
+        out.append((counts, prob, loss, d))
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
 @pytest.mark.parametrize("normalise", [True, False])
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("T,E,k,n_seq", SIZES)
