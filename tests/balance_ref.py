@@ -4,12 +4,12 @@ library's fp32 arithmetic that the tests use.
 Bounds.  U = 2^-24.  A score takes an exponential of an fp32 argument (softmax: a difference of logits, rounded: off by
 |l - max| U, which is the exponential's relative error too), and a few operations of at most two units each: relative
 error below (R + 16) 2 U, R the largest |l - max| (0 for the other scores, whose argument is the logit itself).  The sum
-over E experts adds at most 16 additions on a path through the tree, the division two more roundings: p is off by
-``eps_p`` = (2 R + 64) U relative.  prob adds non-negative fp32 numbers: at most ceil(T / 4096) + 16 on a path (a
-workgroup's 16 wavefronts go round its range of tokens, then their sums are added), fp64 beyond.
+over E experts adds at most 21 additions on a path through the tree, the reciprocal and its product three more units: p
+is off by ``eps_p`` = (2 R + 64) U relative.  prob adds non-negative fp32 numbers: at most ceil(T / 4096) + 16 on a path
+(a workgroup's wavefronts go round its range of tokens, then their sums are added), fp64 beyond.
 
 The gradient's terms are differences, so its bound goes by magnitudes: for ds the sum of the magnitudes of its parts,
-(|f - 1| + sum |f - 1| p) and (|dw| + sum |dw| s / S), each made of numbers with the errors above and of up to 16
+(|f - 1| + sum |f - 1| p) and (|dw| + sum |dw| s / S), each made of numbers with the errors above and of up to 21
 additions: 4 eps_p + 64 U of it in all.
 """
 import numpy as np
