@@ -314,6 +314,57 @@ def test_same_bits_streams_and_graph(dev):
             assert same(s, want), i
 
 
+def test_long_sequence_again_streams_and_graph(dev):
+    """A sequence whose ranges several workgroups join: the same bits from calls in a row over one workspace, from two
+    streams at once with workspaces of their own, and from a graph replayed on new inputs."""
+    torch, moe = dev
+    T, E, k = 20000, 130, 6
+    l0, idx, _, mask, rng = batch(T, E, k, 1, 9, seqs=False)
+    c = moe.make_config(T, 64, E, k, 64, n_shared=0, score="softmax")
+    idx = torch.from_numpy(idx).cuda()
+
+    def state():
+        return dict(l=torch.from_numpy(l0).cuda(), counts=torch.empty((1, E), dtype=torch.int32, device="cuda"),
+                    tokens=torch.empty(1, dtype=torch.int32, device="cuda"), prob=torch.empty((1, E), device="cuda"),
+                    loss=torch.empty(1, device="cuda"), ws=moe.balance_workspace(c, 1))
+
+    def call(s):
+        moe.moe_balance(c, s["l"], idx, s["counts"], s["tokens"], s["prob"], s["loss"], s["ws"])
+
+    def same(a, b):
+        torch.cuda.synchronize()
+        return all(torch.equal(a[key], b[key]) for key in ("counts", "tokens", "prob", "loss"))
+
+    want, got, other = state(), state(), state()
+    call(want)
+    say("in a row")
+    for _ in range(5):
+        got["loss"].fill_(-1.0)
+        call(got)
+        assert same(got, want)
+    say("two streams")
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st, s in zip(streams, (got, other)):
+        s["loss"].fill_(-1.0)
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            for _ in range(3):
+                call(s)
+    torch.cuda.synchronize()
+    assert same(got, want) and same(other, want)
+    say("graph")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(got)
+    for _ in range(3):
+        got["l"].copy_(torch.randn((T, E), device="cuda"))
+        want["l"].copy_(got["l"])
+        got["loss"].fill_(-1.0)
+        g.replay()
+        call(want)
+        assert same(got, want)
+
+
 def test_run_together(dev):
     """A step of tuning a router over int8 experts: routing, load and balance loss, the layer over that selection, the
     gradient of the selected weights from the experts' outputs, of the logits, of the router's weights; against
