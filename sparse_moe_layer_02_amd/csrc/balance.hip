@@ -5,9 +5,10 @@
 //   c[q, e] = selections of expert e by sequence q's tokens, n[q] its tokens
 //   f[q, e] = E c[q, e] / (k n[q]),      P[q, e] = mean of p over its tokens
 //   loss[q] = sum_e f[q, e] P[q, e]      (f is a constant of the gradient)
-//   dL/ds[t, e] = d_loss[q] / n[q] (f[q, e] - sum_i f[q, i] p[t, i]) / sum s
+//   dL/dl[t, e] = d_loss[q] / n[q] (f[q, e] - sum_i f[q, i] p[t, i]) d(log s)/dl p[t, e]
 //               + the selected weights' part (w = scale s / sum_sel s, or scale s)
-//   dL/dl[t, e] = dL/ds[t, e] s'(l), softmax: s_e (dL/ds_e - sum_i dL/ds_i s_i)
+//   (softmax: d(log s)/dl is 1, and weights that are not renormalised take
+//   p[t, e] sum_j d_w[t, j] w[t, j] off)
 //
 // Both directions read the logits once.  G lanes take a token (16 up to 256 experts,
 // so that a wavefront has four and a sum over experts is four DPP steps; 64 beyond):
@@ -49,39 +50,45 @@ __device__ __forceinline__ int seq_of(const int32_t* off, int n_seq, int t) {
     return lo - 1;
 }
 
-// e^x for x <= 0, off by less than two units (2^r 2^f with |f| <= 1/2, f from the
-// product's exact low part); 0 where it vanishes, NaN stays.
-__device__ __forceinline__ float exp_neg(float x) {
+// 2^add e^x for x <= 0 and 0 <= add <= 32, off by less than two units where that is no
+// denormal (2^r 2^f with |f| <= 1/2, f from the product's exact low part); 0 where it
+// vanishes, NaN stays.
+__device__ __forceinline__ float exp_neg(float x, int add = 0) {
     constexpr float L = 1.44269502f, L_LO = 1.92596299e-8f, BIG = 12582912.0f;  // log2 e; 1.5 * 2^23
     x = x < -200.0f ? -200.0f : x;
     const float t = fmaf(x, L, BIG), r = t - BIG;
     const float p = __builtin_amdgcn_exp2f(fmaf(x, L_LO, fmaf(x, L, -r)));
-    return __builtin_ldexpf(p, (int)(__float_as_uint(t) - __float_as_uint(BIG)));
+    return __builtin_ldexpf(p, (int)(__float_as_uint(t) - __float_as_uint(BIG)) + add);
 }
 
-// Score of a logit (softmax: up to the common factor, m the row's maximum) and
-// its derivative (not softmax).  The reciprocal, root and logarithm instructions
+// 2^32 s and 2^32 ds/dl, s the score of a logit (softmax: up to the common factor, m the
+// row's maximum, and the score itself in the derivative's place).  Scores are products of e^l, or e^(l / 2), and so
+// denormal, or zero, long before a token's probabilities lose their meaning: with the
+// factor all those count in full whose sum is 2^-126 and more, and none overflows
+// (the largest is 2^32 sqrt(FLT_MAX)).  The reciprocal, root and logarithm instructions
 // are off by one unit each.
+constexpr int UP_BITS = 32;
+constexpr float UP = 0x1p32f, DOWN = 0x1p-32f;
 template <int KIND, bool GRAD>
 __device__ __forceinline__ float score_of(float l, float m, float& ds) {
     if constexpr (KIND == MOE_SCORE_SOFTMAX) {
-        return exp_neg(l - m);
+        const float s = exp_neg(l - m, UP_BITS);
+        if (GRAD) ds = s;
+        return s;
+    } else if constexpr (KIND == MOE_SCORE_SIGMOID) {
+        // a = 2^32 e^-|l|: neither direction overflows, and 1 - sigmoid keeps its digits
+        const float a = exp_neg(-fabsf(l), UP_BITS), h = __builtin_amdgcn_rcpf(fmaf(a, DOWN, 1.0f));
+        if (GRAD) ds = a * h * h;
+        return (l >= 0.0f ? UP : a) * h;
     } else {
-        // a = e^-|l|: neither direction overflows, and 1 - sigmoid keeps its digits
-        const float a = exp_neg(-fabsf(l)), u = 1.0f + a, h = __builtin_amdgcn_rcpf(u), ah = a * h;
-        const float sg = l >= 0.0f ? h : ah;
-        if constexpr (KIND == MOE_SCORE_SIGMOID) {
-            if (GRAD) ds = ah * h;
-            return sg;
-        } else {
-            // log(1 + a) = log u + (a - (u - 1)) / u, the difference being exact
-            const float lg = fmaf(__builtin_amdgcn_logf(u), 0.693147181f, (a - (u - 1.0f)) * h);
-            const float x = (l < 0.0f ? 0.0f : l) + lg;
-            const bool tiny = x < 0x1p-96f;  // (the root flushes denormals)
-            const float s = __builtin_amdgcn_sqrtf(tiny ? x * 0x1p64f : x) * (tiny ? 0x1p-32f : 1.0f);
-            if (GRAD) ds = s > 0.0f ? 0.5f * sg * __builtin_amdgcn_rcpf(s) : (s != s ? s : 0.0f);
-            return s;
-        }
+        // below -20 softplus is e^l, off by e^-20 / 2 of itself at most, and the score e^(l / 2)
+        const bool low = l < -20.0f;
+        const float e = exp_neg(low ? 0.5f * l : -fabsf(l), UP_BITS), a = e * DOWN, u = 1.0f + a;
+        // log(1 + a) = log u + (a - (u - 1)) / u, the difference being exact
+        const float h = __builtin_amdgcn_rcpf(u), lg = fmaf(__builtin_amdgcn_logf(u), 0.693147181f, (a - (u - 1.0f)) * h);
+        const float x = (l < 0.0f ? 0.0f : l) + lg, s = __builtin_amdgcn_sqrtf(x);
+        if (GRAD) ds = low ? 0.5f * e : 0.5f * UP * ((l >= 0.0f ? 1.0f : a) * h) * __builtin_amdgcn_rcpf(s);
+        return low ? e : s * UP;
     }
 }
 
@@ -141,7 +148,7 @@ __device__ __forceinline__ void load_row(const T* row, int E, int sub, T (&l)[4 
     }
 }
 
-// The scores of a token; inv = 1 / sum s (0 where the scores vanish), m as for score_of.
+// score_of for a token's experts; inv = 1 / their sum (0 where sum s is below 2^-126).
 template <int G, int J, bool GRAD>
 __device__ __forceinline__ void token_scores(const float (&l)[4 * J], int E, int sub, int kind, float (&s)[4 * J],
                                              float (&ds)[4 * J], float& m, float& inv) {
@@ -165,7 +172,7 @@ __device__ __forceinline__ void token_scores(const float (&l)[4 * J], int E, int
         }
     });
     sum = row_sum<G>(sum);
-    inv = sum < 0x1p-126f ? 0.0f : __builtin_amdgcn_rcpf(sum);
+    inv = sum < 0x1p-126f * UP ? 0.0f : __builtin_amdgcn_rcpf(sum);
 }
 
 // A sequence's sum of the wavefronts' parts of its loss, in their order, for thread 0.
@@ -362,7 +369,7 @@ __device__ __forceinline__ void lds_in_order() {
 template <int G, int J, bool WIDE>
 __global__ __launch_bounds__(GW * WAVE, 4) void route_backward_kernel(RouteGradArgs a) {
     constexpr int V = 4 * J, NT = WAVE / G, KI = (BALANCE_MAX_K + G - 1) / G, EP = G * V;
-    __shared__ __attribute__((aligned(16))) float selected[GW][NT][EP];  // dL/ds of the selected weights, 0 between tokens
+    __shared__ __attribute__((aligned(16))) float selected[GW][NT][EP];  // the selected weights' part, 0 between tokens
     const int lane = lane_id(), sub = lane % G, grp = lane / G, E = a.E;
     const int w0 = blockIdx.x * GW + wave_index();
     float* buf = selected[wave_index()][grp];
@@ -434,32 +441,25 @@ __global__ __launch_bounds__(GW * WAVE, 4) void route_backward_kernel(RouteGradA
             for (int i = 0; i < KI; ++i)
                 if (G * i < a.k) ls[i] = a.logits[(size_t)min(t, a.T - 1) * E + (cur.x[i] < E ? cur.x[i] : 0)];
         }
-        float s[V], ds[V], g[V], top, total;  // total: 1 / sum s
-        token_scores<G, J, true>(cur.l, E, sub, a.score, s, ds, top, total);
-        const float norm = soft ? total : 1.0f;  // s as the router has it
-        const float inv = soft ? 1.0f : total;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            s[v] *= norm;
-            g[v] = 0.0f;
-        }
+        float s[V], ds[V], top, inv;
+        token_scores<G, J, true>(cur.l, E, sub, a.score, s, ds, top, inv);
+        float off = 0.0f;
         if (a.d_loss) {
             float fp = 0.0f;
 #pragma unroll
-            for (int v = 0; v < V; ++v) fp = fmaf(f[v], s[v] * inv, fp);
-            fp = row_sum<G>(fp);
-#pragma unroll
-            for (int v = 0; v < V; ++v) g[v] = rate * (f[v] - fp) * inv;
+            for (int v = 0; v < V; ++v) fp = fmaf(f[v], s[v], fp);
+            off = rate * (row_sum<G>(fp) * inv);
         }
         if (a.d_w) {
-            // a lane's selected experts (E: none), their scores and weights' gradients
-            float sel[KI], add[KI], S = 0.0f;
+            // a lane's selected experts (E: none), their scores, the scores' derivatives
+            // and the weights' gradients
+            const float unit = soft ? inv : DOWN;
+            float sel[KI], dsel[KI], add[KI], S = 0.0f;
             with_score(a.score, [&](auto KIND) {
 #pragma unroll
                 for (int i = 0; i < KI; ++i) {
-                    float unused;
-                    sel[i] = 0.0f;
-                    if (G * i < a.k && cur.x[i] < E) sel[i] = score_of<KIND.value, false>(ls[i], top, unused) * norm;
+                    sel[i] = dsel[i] = 0.0f;
+                    if (G * i < a.k && cur.x[i] < E) sel[i] = score_of<KIND.value, true>(ls[i], top, dsel[i]) * unit;
                     S += sel[i];
                 }
             });
@@ -472,6 +472,14 @@ __global__ __launch_bounds__(GW * WAVE, 4) void route_backward_kernel(RouteGradA
                 dot = row_sum<G>(dot);
 #pragma unroll
                 for (int i = 0; i < KI; ++i) cur.dw[i] = cur.x[i] < E ? (cur.dw[i] - dot) * rS : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < KI; ++i) cur.dw[i] = cur.dw[i] * dsel[i] * unit;
+            if (soft && !a.normalise) {  // (of renormalised weights they add up to nothing, as the balance part does)
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < KI; ++i) sum += cur.dw[i];
+                off += row_sum<G>(sum);
             }
             // an expert listed twice: one of its lanes reads the other's mark, and all
             // of them take the sum in the order of the list
@@ -507,6 +515,12 @@ __global__ __launch_bounds__(GW * WAVE, 4) void route_backward_kernel(RouteGradA
             for (int i = 0; i < KI; ++i)
                 if (cur.x[i] < E) buf[cur.x[i]] = add[i];
             lds_in_order();
+        }
+        const float unit = a.d_loss || soft ? inv : 1.0f;  // (1: zeros, or NaN of a NaN logit)
+        float g[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) g[v] = fmaf(rate, f[v], -off) * ds[v] * unit;
+        if (a.d_w) {
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const float4 d = *reinterpret_cast<const float4*>(buf + expert_of<G>(sub, 4 * j));
@@ -517,17 +531,6 @@ __global__ __launch_bounds__(GW * WAVE, 4) void route_backward_kernel(RouteGradA
             for (int i = 0; i < KI; ++i)
                 if (cur.x[i] < E) buf[cur.x[i]] = 0.0f;
             lds_in_order();
-        }
-        if (soft) {
-            float dot = 0.0f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) dot = fmaf(g[v], s[v], dot);
-            dot = row_sum<G>(dot);
-#pragma unroll
-            for (int v = 0; v < V; ++v) g[v] = s[v] * (g[v] - dot);
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) g[v] *= ds[v];
         }
         const bool live = cur.live && q >= 0;  // else no gradient
 #pragma unroll
