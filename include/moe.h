@@ -368,6 +368,8 @@ int moe_balance(const moe_config *cfg, const float *logits, const int32_t *topk_
  * are.  d_topk_w [T, k] and d_loss [n_seq] may be NULL (one of them at most);
  * with d_loss, counts and tokens are moe_balance's outputs.  topk_idx entries
  * outside [0, E) have no weight; an expert listed twice has the sum of both.
+ * Renormalised weights whose scores are all 0 as the selection's fp32 scores
+ * (below 2^-150) are 0, as there, and have no gradient.
  * Every row is written: rows of tokens that the mask or the offsets leave out are
  * zeros, whatever their logits and d_topk_w hold.  The other arguments as for
  * moe_balance.  No workspace; d_logits must not overlap an input. */

@@ -64,9 +64,9 @@ __device__ __forceinline__ float exp_neg(float x, int add = 0) {
 // 2^32 s and 2^32 ds/dl, s the score of a logit (softmax: up to the common factor, m the
 // row's maximum, and the score itself in the derivative's place).  Scores are products of e^l, or e^(l / 2), and so
 // denormal, or zero, long before a token's probabilities lose their meaning: with the
-// factor all those count in full whose sum is 2^-126 and more, and none overflows
-// (the largest is 2^32 sqrt(FLT_MAX)).  The reciprocal, root and logarithm instructions
-// are off by one unit each.
+// factor all those count in full whose sum is 2^-126 and more, or that are not 0 as the
+// selection's fp32 scores, and none overflows (the largest is 2^32 sqrt(FLT_MAX)).  The
+// reciprocal, root and logarithm instructions are off by one unit each.
 constexpr int UP_BITS = 32;
 constexpr float UP = 0x1p32f, DOWN = 0x1p-32f;
 template <int KIND, bool GRAD>
@@ -115,6 +115,13 @@ __device__ __forceinline__ float row_reduce(float v, Op op) {
 struct MaxF { __device__ float operator()(float a, float b) const { return fmaxf(a, b); } };
 template <int G> __device__ __forceinline__ float row_sum(float v) { return row_reduce<G>(v, AddF()); }
 
+// Whether it holds for one of a token's lanes.
+template <int G>
+__device__ __forceinline__ bool row_any(bool b) {
+    const uint64_t m = __ballot(b);
+    return G == WAVE ? m != 0 : (m >> (lane_id() & -G) & ((1ull << (G % WAVE)) - 1)) != 0;
+}
+
 // The sum of the four rows of 16 lanes, in each of them.
 __device__ __forceinline__ float rows_sum(float v) {
     const uint32_t a = __float_as_uint(v);
@@ -129,21 +136,28 @@ __device__ __forceinline__ float rows_sum(float v) {
 template <int G>
 __device__ __forceinline__ int expert_of(int sub, int v) { return 4 * (sub + G * (v / 4)) + v % 4; }
 
-// A token's row; WIDE: its length and address are multiples of 16 bytes.
+// Element at of an array of up to 2^20 x 1024 fp32 or int32 values: its bytes are counted
+// in 32 bits, which the compiler keeps in one register and adds to a scalar base.
+template <class U, class T>
+__device__ __forceinline__ U load_at(const T* base, uint32_t at) {
+    return *reinterpret_cast<const U*>(reinterpret_cast<const char*>(base) + 4u * at);
+}
+// A token's row, or a sequence's; WIDE: its length and address are multiples of 16 bytes.
 template <int G, int J, bool WIDE, class T4, class T>
-__device__ __forceinline__ void load_row(const T* row, int E, int sub, T (&l)[4 * J]) {
+__device__ __forceinline__ void load_row(const T* base, int row, int E, int sub, T (&l)[4 * J]) {
+    const uint32_t at = (uint32_t)row * E;
     if constexpr (WIDE) {
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const int e = expert_of<G>(sub, 4 * j);
-            const T4 x = *reinterpret_cast<const T4*>(row + (e < E ? e : 0));
+            const T4 x = load_at<T4>(base, at + (e < E ? e : 0));
             l[4 * j] = x.x, l[4 * j + 1] = x.y, l[4 * j + 2] = x.z, l[4 * j + 3] = x.w;
         }
     } else {
 #pragma unroll
         for (int v = 0; v < 4 * J; ++v) {
             const int e = expert_of<G>(sub, v);
-            l[v] = row[e < E ? e : 0];
+            l[v] = load_at<T>(base, at + (e < E ? e : 0));
         }
     }
 }
@@ -216,11 +230,11 @@ __global__ __launch_bounds__(BW * WAVE) void balance_kernel(BalanceArgs a) {
             k.live = t < e;
             t = min(t, e - 1);
             if (a.mask) k.live = k.live && a.mask[t];
-            load_row<G, J, WIDE, float4>(a.logits + (size_t)t * E, E, sub, k.l);
+            load_row<G, J, WIDE, float4>(a.logits, t, E, sub, k.l);
 #pragma unroll
             for (int i = 0; i < KI; ++i) {
                 const int j = sub + G * i;
-                k.x[i] = j < a.k ? a.idx[(size_t)t * a.k + j] : -1;
+                k.x[i] = j < a.k ? load_at<int>(a.idx, t * a.k + j) : -1;
             }
         };
         Token cur;
@@ -391,12 +405,12 @@ __global__ __launch_bounds__(GW * WAVE, 4) void route_backward_kernel(RouteGradA
 #pragma unroll
             for (int i = 0; i < KI; ++i) {
                 const int j = sub + G * i;
-                const int x = j < a.k ? a.idx[(size_t)t * a.k + j] : -1;
+                const int x = j < a.k ? load_at<int>(a.idx, t * a.k + j) : -1;
                 k.x[i] = x >= 0 && x < E ? x : E;
-                k.dw[i] = x >= 0 && x < E ? a.scale * a.d_w[(size_t)t * a.k + j] : 0.0f;
+                k.dw[i] = x >= 0 && x < E ? a.scale * load_at<float>(a.d_w, t * a.k + j) : 0.0f;
             }
         }
-        load_row<G, J, WIDE, float4>(a.logits + (size_t)t * E, E, sub, k.l);
+        load_row<G, J, WIDE, float4>(a.logits, t, E, sub, k.l);
     };
     int q = 0, q_end = 0;  // the sequence of the last token, and its end
     float f[V], rate = 0.0f;
@@ -430,7 +444,7 @@ __global__ __launch_bounds__(GW * WAVE, 4) void route_backward_kernel(RouteGradA
                 const double rf = (double)E / ((double)a.k * n);
                 rate = __fdiv_rn(a.d_loss[q], (float)n);
                 int c[V];
-                load_row<G, J, WIDE, int4>(a.counts + (size_t)q * E, E, sub, c);
+                load_row<G, J, WIDE, int4>(a.counts, q, E, sub, c);
 #pragma unroll
                 for (int v = 0; v < V; ++v) f[v] = expert_of<G>(sub, v) < E ? (float)(c[v] * rf - 1.0) : 0.0f;
             }
@@ -439,7 +453,7 @@ __global__ __launch_bounds__(GW * WAVE, 4) void route_backward_kernel(RouteGradA
         if (a.d_w) {
 #pragma unroll
             for (int i = 0; i < KI; ++i)
-                if (G * i < a.k) ls[i] = a.logits[(size_t)min(t, a.T - 1) * E + (cur.x[i] < E ? cur.x[i] : 0)];
+                if (G * i < a.k) ls[i] = load_at<float>(a.logits, (uint32_t)min(t, a.T - 1) * E + (cur.x[i] < E ? cur.x[i] : 0));
         }
         float s[V], ds[V], top, inv;
         token_scores<G, J, true>(cur.l, E, sub, a.score, s, ds, top, inv);
@@ -455,31 +469,35 @@ __global__ __launch_bounds__(GW * WAVE, 4) void route_backward_kernel(RouteGradA
             // and the weights' gradients
             const float unit = soft ? inv : DOWN;
             float sel[KI], dsel[KI], add[KI], S = 0.0f;
+            bool weighs = false;  // some score is not 0 as the selection's fp32 score (or NaN)
             with_score(a.score, [&](auto KIND) {
 #pragma unroll
                 for (int i = 0; i < KI; ++i) {
                     sel[i] = dsel[i] = 0.0f;
-                    if (G * i < a.k && cur.x[i] < E) sel[i] = score_of<KIND.value, true>(ls[i], top, dsel[i]) * unit;
+                    if (G * i < a.k && cur.x[i] < E) sel[i] = score_of<KIND.value, true>(ls[i], top, dsel[i]);
                     S += sel[i];
+                    weighs = weighs || sel[i] * unit != 0.0f;
                 }
             });
             if (a.normalise) {
+                // 1 / S only ever multiplies scores and their derivatives, which are as small
+                // as S: with dL/ds = (dw - dot) / S first, small scores would overflow
                 S = row_sum<G>(S);
-                const float rS = S < 0x1p-126f ? 0.0f : __builtin_amdgcn_rcpf(S);
+                const float rS = row_any<G>(weighs) ? __builtin_amdgcn_rcpf(S) : 0.0f;
                 float dot = 0.0f;
 #pragma unroll
                 for (int i = 0; i < KI; ++i) dot += cur.dw[i] * (sel[i] * rS);
                 dot = row_sum<G>(dot);
 #pragma unroll
-                for (int i = 0; i < KI; ++i) cur.dw[i] = cur.x[i] < E ? (cur.dw[i] - dot) * rS : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < KI; ++i) cur.dw[i] = cur.dw[i] * dsel[i] * unit;
-            if (soft && !a.normalise) {  // (of renormalised weights they add up to nothing, as the balance part does)
+                for (int i = 0; i < KI; ++i) cur.dw[i] = cur.x[i] < E ? (cur.dw[i] - dot) * (dsel[i] * rS) : 0.0f;
+            } else {
                 float sum = 0.0f;
 #pragma unroll
-                for (int i = 0; i < KI; ++i) sum += cur.dw[i];
-                off += row_sum<G>(sum);
+                for (int i = 0; i < KI; ++i) {
+                    cur.dw[i] = cur.dw[i] * dsel[i] * unit;
+                    sum += cur.dw[i];
+                }
+                if (soft) off += row_sum<G>(sum);  // (renormalised weights' add up to nothing, as the balance part does)
             }
             // an expert listed twice: one of its lanes reads the other's mark, and all
             // of them take the sum in the order of the list

@@ -71,3 +71,70 @@ def test_gradients_of_saturated_rows(dev, kind):
         with np.errstate(all="ignore"):
             want, err = R.backward(l, idx, kind, off=off, eps=64 * R.U, **kw)  # (no finite softmax exponent but 0)
         assert (np.abs(got - want) <= err + DENORMAL).all(), np.abs(got - want).max()
+
+
+# A renormalised weight's gradient, (dw_j - sum dw w) w_j (log s)'(l_j), has no factor that leaves fp32's range: its bound
+# is balance_ref's, whose terms are these (for softmax with the range of its logits, which an exponential's argument can
+# reach).  The selection's own weights tell where it is no more: scores below 2^-150 are 0 in fp32, and weights and gradient
+# with them.
+@pytest.mark.parametrize("E,k", [(12, 2), (61, 5), (256, 8), (1024, 32)])
+@pytest.mark.parametrize("kind,lowest", [("sigmoid", -99.0), ("sqrt_softplus", -203.0), ("softmax", -88.0)])
+def test_renormalised_weights_of_small_scores(dev, kind, lowest, E, k):
+    """Selected scores from ordinary ones down to fp32's smallest, large gradients of the weights."""
+    centres = np.arange(lowest, 10.0, 2.5 if kind != "sqrt_softplus" else 5.0)
+    T = len(centres)
+    l, idx, off, rng = rows_around(centres, E, k, 3.0, E + 1)
+    if kind == "softmax":
+        top = np.setdiff1d(np.arange(E), idx[0])[0]  # not selected: the others' scores are small beside it
+        l[:, top] = 0.0
+        for t in range(T):
+            sel = np.argsort(-np.where(np.arange(E) == top, -np.inf, l[t]))[:k]
+            idx[t] = rng.permutation(sel)
+    d_w = (rng.choice([-1.0, 1.0], (T, k)) * rng.uniform(10.0, 1e4, (T, k))).astype(np.float32)
+    kw = dict(scale=2.5, normalise=True, d_w=d_w)
+    say("renormalised", kind, E)
+    got = run_backward(dev, l, idx, kind, off, None, **kw)
+    want, err = R.backward(l, idx, kind, off=off, **kw)
+    bad = ~(np.abs(got - want) <= err + DENORMAL).all(1)
+    assert not bad.any(), (centres[bad], np.abs(got - want)[bad].max(1), np.abs(want)[bad].max(1))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_gradient_ends_where_the_weights_do(dev, kind):
+    """Tokens whose selected scores are all 0 in fp32 have weights of 0 (moe_select_grouped) and no gradient; just above,
+    both are there."""
+    torch, moe = dev
+    E, k, T = 64, 4, 4
+    half = 2.0 if kind == "sqrt_softplus" else 1.0
+    l = np.full((T, E), -1e4, np.float32)
+    l[:, :k] = half * np.array([[-103.0], [-103.5], [-104.5], [-120.0]]) + 0.25 * np.arange(k) * np.array([1, 1, -1, -1])[:, None]
+    bias = np.zeros(E, np.float32)
+    bias[:k] = 2.0  # selected whatever their scores
+    if kind == "softmax":
+        l[:, k] = 0.0
+    c = moe.make_config(T, 64, E, k, 64, n_shared=0, score=kind)
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    idx, w = torch.empty((T, k), dtype=torch.int32, device="cuda"), torch.empty((T, k), device="cuda")
+    say("weights' end", kind)
+    moe.moe_select_grouped(c, None, up(l), up(bias), idx, w)
+    torch.cuda.synchronize()
+    idx, w = idx.cpu().numpy(), w.cpu().numpy()
+    assert sorted(idx[0].tolist()) == list(range(k))
+    d_w = np.tile(np.array([[1.0, -2.0, 3.0, 50.0]], np.float32), (T, 1))
+    got = run_backward(dev, l, idx, kind, None, None, d_w=d_w)
+    assert np.isfinite(got).all()
+    assert (w > 0).any(1).tolist() == [True, True, False, False] == (got != 0).any(1).tolist()
+    # (a selection's fp32 scores there are one or two multiples of 2^-149; the gradient is the definition's)
+    want, err = R.backward(l, idx, kind, d_w=d_w)
+    assert (np.abs(got - want) <= err + DENORMAL)[:2].all()
+
+
+def test_renormalised_weights_with_nan(dev):
+    """A NaN among a token's selected logits reaches its gradient, for softmax one anywhere in the row; no other token's."""
+    E, k = 61, 5
+    for kind in KINDS:
+        l, idx, off, rng = rows_around(np.array([0.0, -90.0, -90.0]), E, k, 2.0, 7)
+        l[1, idx[1, 2] if kind != "softmax" else np.setdiff1d(np.arange(E), idx[1])[3]] = np.nan
+        say("nan", kind)
+        got = run_backward(dev, l, idx, kind, off, None, d_w=rng.standard_normal((3, k)))
+        assert np.isnan(got[1]).any() and np.isfinite(got[[0, 2]]).all()
