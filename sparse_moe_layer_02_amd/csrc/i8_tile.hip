@@ -100,8 +100,9 @@ struct I8Sums {
 // knows of before reads of LDS, and where paths or rounds of a ring meet it takes
 // copies just sent for ones the read needs.  Here it sees none, every wait is the
 // loop's own, and the rings need no names of their own for their stages.  (M0,
-// where a copy finds its LDS address, is set with each; nothing the compiler
-// makes of these kernels uses it.)
+// where a copy finds its LDS address, is set with each.  The compiler reserves it, so
+// that a clobber of it cannot be declared: nothing else in these kernels may use it,
+// such as a builtin that copies to LDS; tests/test_i8_assembly.py looks.)
 // 16 bytes per lane from src + off + k0 to LDS at dst (wave-uniform) + 16 lane.
 template <bool NT>
 __device__ __forceinline__ void send16(i32x4_t src, uint32_t off, int k0, uint32_t dst) {
