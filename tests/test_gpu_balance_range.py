@@ -22,7 +22,7 @@ def rows_around(centres, E, k, width, seed):
     return l, idx, np.arange(T + 1, dtype=np.int32), rng
 
 
-@pytest.mark.parametrize("E,k", [(61, 5), (256, 8), (300, 4), (1024, 32)])
+@pytest.mark.parametrize("E,k", [(61, 5), (100, 32), (256, 8), (300, 4), (1024, 32)])
 @pytest.mark.parametrize("kind", ["sigmoid", "sqrt_softplus"])
 def test_low_scores(dev, kind, E, k):
     """Logits down to where a token's scores sum to 2^-126: probabilities, losses and gradients keep their digits."""
@@ -77,7 +77,7 @@ def test_gradients_of_saturated_rows(dev, kind):
 # is balance_ref's, whose terms are these (for softmax with the range of its logits, which an exponential's argument can
 # reach).  The selection's own weights tell where it is no more: scores below 2^-150 are 0 in fp32, and weights and gradient
 # with them.
-@pytest.mark.parametrize("E,k", [(12, 2), (61, 5), (256, 8), (1024, 32)])
+@pytest.mark.parametrize("E,k", [(12, 2), (61, 5), (100, 32), (256, 8), (1024, 32)])
 @pytest.mark.parametrize("kind,lowest", [("sigmoid", -99.0), ("sqrt_softplus", -203.0), ("softmax", -88.0)])
 def test_renormalised_weights_of_small_scores(dev, kind, lowest, E, k):
     """Selected scores from ordinary ones down to fp32's smallest, large gradients of the weights."""
@@ -138,3 +138,24 @@ def test_renormalised_weights_with_nan(dev):
         say("nan", kind)
         got = run_backward(dev, l, idx, kind, off, None, d_w=rng.standard_normal((3, k)))
         assert np.isnan(got[1]).any() and np.isfinite(got[[0, 2]]).all()
+
+
+@pytest.mark.parametrize("normalise", [True, False])
+@pytest.mark.parametrize("kind,centre", [("sigmoid", -95.0), ("sqrt_softplus", -190.0), ("softmax", -20.0)])
+def test_small_scores_listed_again(dev, kind, centre, normalise):
+    """Experts listed several times, and entries that are none, among small scores."""
+    for E, k in ((61, 7), (100, 32), (300, 9)):
+        l, idx, off, rng = rows_around(np.full(6, centre), E, k, 3.0, E)
+        if kind == "softmax":
+            l[:, -1] = 60.0
+        idx[0] = idx[0, 0]
+        idx[1, 1:3] = idx[1, 0]
+        idx[2, 2] = idx[2, k - 1]
+        idx[3, :3] = -1, E, 2 ** 31 - 1
+        idx[4] = -1
+        kw = dict(scale=1.5, normalise=normalise, d_w=(rng.standard_normal((6, k)) * 100).astype(np.float32))
+        say("listed again", kind, E, normalise)
+        got = run_backward(dev, l, idx, kind, off, None, **kw)
+        want, err = R.backward(l, idx, kind, off=off, **kw)
+        # (a sum of up to k parts, each rounded to a multiple of 2^-149 where it is that small)
+        assert (np.abs(got - want) <= err + DENORMAL + k * 2.0 ** -150).all(), np.abs(got - want).max()
