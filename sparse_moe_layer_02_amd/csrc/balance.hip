@@ -592,8 +592,8 @@ void with_layout(int E, uintptr_t addresses, F&& f) {
 
 int balance_chunk(int T, int E, int n_seq) {
     // whole rounds of a workgroup's wavefronts; two of them stay in one workgroup, and
-    // one launch (37 tokens of 192 experts: 5.2 us, two launches 7.1; four rounds of
-    // 256 experts: 8.6, 7.9), where there are no more sequences to take one by one
+    // one launch (37 tokens of 192 experts: 4.9 us, two launches 6.9; four rounds of
+    // 256 experts: 8.4, 7.5), where there are no more sequences to take one by one
     const int round = BW * (E <= 256 ? 4 : 1);
     if (T <= 2 * round && n_seq == 1) return 2 * round;
     const int per = (T + BALANCE_MAX_RANGES - 1) / BALANCE_MAX_RANGES;
@@ -603,7 +603,8 @@ int balance_chunk(int T, int E, int n_seq) {
 hipError_t launch_balance(BalanceArgs a, hipStream_t st) {
     const int grid = (a.T + a.chunk - 1) / a.chunk;
     // 64 experts a workgroup of the second launch where a sequence has many ranges
-    // (65536 tokens of 256 experts: 26.5 us, 29.1 with all of them; 256 tokens: 9.2, 7.9)
+    // (one sequence of 65536 tokens and 256 experts: 25.4 us, 28.9 with all of them; of
+    // 2048 tokens: 10.9, 9.0)
     a.blocks = grid / a.n_seq >= 256 ? (a.E + 63) / 64 : 1;
     a.one_launch = grid == 1 && a.n_seq == 1;
     with_layout(a.E, reinterpret_cast<uintptr_t>(a.logits), [&](auto G, auto J, auto WIDE) {

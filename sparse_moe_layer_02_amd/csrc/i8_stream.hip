@@ -13,8 +13,10 @@
 // are exact, so K is split as the sizes suggest; the partial sums meet in LDS.
 // Rows that no expert has repeat the last one; their results are not stored.
 //
-// One token, d 4096, F 2048, six experts and the shared one: gate/up 21.4 us (5.5 TB/s
-// of weights), down 12.9 (4.6).
+// d 4096, F 2048, top-6 and the shared expert, other experts' weights in each call
+// (medians): one token gate/up 25.0 us (4.7 TB/s of weights) and down 14.8 (4.0; the same
+// weights again, from the memory-side cache: 23.0 and 13.7), 16 tokens with 80 experts
+// 225 (6.1) and 114 (6.0).
 //
 // Column tails: a load past the end of K re-reads the row's last 16 columns, and
 // the activation operand is zero there.
@@ -31,8 +33,9 @@ constexpr int SW = 8;  // wavefronts per workgroup
 constexpr int SK = 64; // columns of a step
 // Steps loaded at once.  A wavefront's share of K is a multiple of them: with 8 at
 // once and 12 for a wavefront the loads past its end, repeats of its last step,
-// cost more than they hid (1 x 4096 x 6144: 9.7 us, 7.3 so; non-temporal loads 7.9;
-// two groups ahead in place of one 8.1; 24576 x 6144: 30 us, 5.0 TB/s).
+// cost more than they hid (weights in the memory-side cache, 1 x 4096 x 6144: 9.7 us,
+// 7.3 so; non-temporal loads 7.9; two groups ahead in place of one 8.1; 24576 x 6144: 30
+// us, 5.0 TB/s.  Weights in memory, 1 x 4096 x 6144: 9.1 us).
 constexpr int UU = 4;
 constexpr int I8_FUSE_VALUES = 24 * 1024;  // values a workgroup quantises itself, at most (their codes lie in LDS)
 
@@ -283,7 +286,8 @@ __global__ __launch_bounds__(WAVE * SW) void i8_gateup_stream_kernel(I8Ffn a) {
 // whose int32 sums are added in LDS.  A slot's sums become rows in LDS (with the
 // routing weights), and at the end the rows of a token are added in the order the
 // combine has.  (Quantising the rows of h here too, in every workgroup under its
-// first weights, took as long as the launch that does it: one token 51.5 / 50.2 us.)
+// first weights, took as long as the launch that does it: a call of one token on the same inputs 51.5 /
+// 50.2 us.)
 constexpr int DI = 8;  // steps of a chunk
 struct DownRow {  // of h
     int f;        // its result row

@@ -12,9 +12,9 @@
 // stage.  The sums stay in int32 accumulators over the whole of K; the scales of
 // rows and columns are applied once, behind the loop.
 //
-// Measured: 4096 x 4096 x 6144 83.5 us (2.5 POP/s; matrix cores); layers of d 6144, F
-// 2048 and 256 experts: 512 tokens gate/up 1.08 and down 0.62 ms (weight bytes, 6.0
-// and 5.2 TB/s), 4096 tokens 1.64 and 0.99.
+// Measured: 4096 x 4096 x 6144 83.0 us (2.5 POP/s; matrix cores); layers of d 6144, F
+// 2048 and 256 experts: 512 tokens gate/up 1.09 and down 0.62 ms (weight bytes, 5.9
+// and 5.2 TB/s), 4096 tokens 1.67 and 0.99.
 //
 // A tile computes only the 32-row blocks that hold rows: blocks are dealt to the
 // two wavefront rows in turn, and each wavefront runs the K loop built for its
@@ -44,7 +44,7 @@ struct Rings : Shape<NB_, NJ_, GM_, GN_, 2> {
     static_assert(WQ * CW * 1024 == Base::WB && XQ * CW * 1024 == Base::XB, "whole copies");
 };
 // Expert tiles (256 weight rows): up to 64 rows, two workgroups per compute unit
-// (16 rows per expert: gate/up 1.05 ms, 6.1 TB/s of weights); beyond, all of LDS in
+// (16 rows per expert: gate/up 1.09 ms, 5.9 TB/s of weights); beyond, all of LDS in
 // one.  The rows come through the L2 as slowly as the weights do (a tile's 786 KB of
 // a 6144-column x beside 31 others' in 4 MB): gate/up of 4096 tokens, 128 rows per
 // expert, stages of weights + of rows: 128-row tiles 4 + 2 2.03 ms, 3 + 3 1.70, 3 + 4
