@@ -53,7 +53,7 @@ __device__ __forceinline__ int seq_of(const int32_t* off, int n_seq, int t) {
 // 2^add e^x for x <= 0 and 0 <= add <= 32, off by less than two units where that is no
 // denormal (2^r 2^f with |f| <= 1/2, f from the product's exact low part); 0 where it
 // vanishes, NaN stays.
-__device__ __forceinline__ float exp_neg(float x, int add = 0) {
+__device__ __forceinline__ float exp_neg(float x, int add) {
     constexpr float L = 1.44269502f, L_LO = 1.92596299e-8f, BIG = 12582912.0f;  // log2 e; 1.5 * 2^23
     x = x < -200.0f ? -200.0f : x;
     const float t = fmaf(x, L, BIG), r = t - BIG;
@@ -62,11 +62,12 @@ __device__ __forceinline__ float exp_neg(float x, int add = 0) {
 }
 
 // 2^32 s and 2^32 ds/dl, s the score of a logit (softmax: up to the common factor, m the
-// row's maximum, and the score itself in the derivative's place).  Scores are products of e^l, or e^(l / 2), and so
-// denormal, or zero, long before a token's probabilities lose their meaning: with the
-// factor all those count in full whose sum is 2^-126 and more, or that are not 0 as the
-// selection's fp32 scores, and none overflows (the largest is 2^32 sqrt(FLT_MAX)).  The
-// reciprocal, root and logarithm instructions are off by one unit each.
+// row's maximum, and the score itself in the derivative's place).  Scores are products
+// of e^l, or e^(l / 2), and so denormal, or zero, long before a token's probabilities
+// lose their meaning: with the factor all those count in full whose sum is 2^-126 and
+// more, or that are not 0 as the selection's fp32 scores, and none overflows (the
+// largest is 2^32 sqrt(FLT_MAX)).  The reciprocal, root and logarithm instructions are
+// off by one unit each.
 constexpr int UP_BITS = 32;
 constexpr float UP = 0x1p32f, DOWN = 0x1p-32f;
 template <int KIND, bool GRAD>
